@@ -2,7 +2,10 @@
  * nmsparse.h -- C ABI of the MI355X (gfx950) library for semi-structured
  * sparse feed-forward matmuls: magnitude N:M and V:N:M pruning, compression
  * to values plus packed position metadata, and the sparse x dense products of
- * the FFN forward pass and of the double-pruned backward pass.
+ * the FFN forward pass and of the double-pruned backward pass.  The last part
+ * is the mixture-of-experts FFN in 8-bit floating point: routing, the rows'
+ * order by expert, quantisation to blocks of 128, products with a scale per
+ * block, and the weighted combine.
  *
  * Sources (page title, section):
  *   "Success story: ESPLAG" (inno4scale) -- Highlights, Research Topic,
@@ -532,6 +535,191 @@ nm_status sddmm_nm(nm_dtype dt, const void* D, int64_t ldd, const void* X, int64
 nm_status sddmm_nm_dt(nm_dtype dt, const void* D, int64_t ldd, const void* X, int64_t ldx, int64_t R,
                       int64_t Kc, int64_t T, const uint8_t* meta, float* values_out, void* Dt,
                       int64_t lddt, nm_stream stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The mixture-of-experts FFN in 8-bit floating point ("To 2:4 Sparsity and
+ * Beyond", abstract: the method is orthogonal to quantisation and applies to
+ * mixture-of-experts FFNs).  A layer's forward is
+ *   moe_route -> moe_plan -> fp8_quantize (rows gathered by expert)
+ *   -> fp8_gemm_nt_grouped (up) -> fp8_quantize (ReLU) -> fp8_gemm_nt_grouped (down) -> moe_combine
+ * and its backward moe_combine_bwd, the same products on transposed weights
+ * (input gradient), fp8_quantize_t and fp8_gemm_nt_grouped_k (weight
+ * gradients), moe_combine with no weights, and moe_route_bwd.
+ *
+ * 8-bit matrices are OCP e4m3 (largest value 448, no infinities) or e5m2
+ * (57344) bytes with an fp32 scale for each block of 128 elements along the
+ * reduction dimension: value = byte's value * scale.  Scales lie block-major:
+ *   by rows   s[kb][lds], kb = k / 128: one per row and 128-block, contiguous
+ *             along the rows (a tile's scales of one block are one load);
+ *   by blocks s[r / 128][lds], lds >= ceil(K / 128): one per 128 x 128 block.
+ * ---------------------------------------------------------------------------
+ */
+
+typedef enum { NM_E4M3 = 0, NM_E5M2 = 1 } nm_fp8;
+typedef enum { NM_SOFTMAX = 0, NM_SIGMOID = 1 } nm_score;
+
+/*
+ * moe_route -- the experts of every token and their weights.
+ *   s[t][e] = softmax over e of logits[t], or sigmoid(logits[t][e])
+ *   c[t][e] = s[t][e] + bias[e]                (bias NULL: c = s)
+ *   With groups > 1, the E experts are `groups` equal runs; a run's score is the
+ *   sum of its group_top (1 or 2) largest c; only experts of the topk_groups best
+ *   runs stay.  ids[t][0..k-1] are the k experts of largest c, in descending
+ *   order; on equal c (and equal run scores) the lower index wins.
+ *   weights[t][j] = scale * s[t][ids[t][j]], divided by the sum of the chosen s
+ *   when renorm.
+ *   logits [T][ldl] dtype dt; bias fp32 [E]; ids int32 [T][k], weights fp32 [T][k]
+ * An expert whose logit is -infinity or NaN (or whose bias is NaN) is never
+ * chosen; +infinity counts as the largest finite value.  Where fewer than k
+ * experts can be chosen, the remaining ids are -1 and their weights 0.  Scores
+ * are computed in fp32; with no bias the order is that of the logits themselves.
+ * 1 <= E <= 1024, 1 <= k <= 64, groups <= 64 (NM_ERR_UNSUPPORTED, also for a
+ * scale that is 0 or not finite); E % groups == 0, topk_groups <= groups,
+ * k <= E / groups * topk_groups, T * k < 2^31 (NM_ERR_SHAPE).
+ */
+nm_status moe_route(nm_dtype dt, const void* logits, int64_t ldl, int64_t T, int64_t E, nm_score score,
+                    const float* bias, int groups, int topk_groups, int group_top, int k, int renorm,
+                    float scale, int32_t* ids, float* weights, nm_stream stream);
+
+/*
+ * moe_route_bwd -- the gradient of moe_route's weights with respect to the logits.
+ * The choice itself has no gradient.  With g = sum_j dweights_j weights_j / scale:
+ *   softmax, renorm   dl_j = weights_j (dweights_j - g) at the chosen, 0 elsewhere
+ *   sigmoid, renorm   the same times 1 - s_j
+ *   softmax           dl_e = weights_e dweights_e (chosen e) - s_e g scale
+ *   sigmoid           dl_j = weights_j dweights_j (1 - s_j) at the chosen, 0 elsewhere
+ *   logits, ids, weights as moe_route takes and writes them (the ids of a token
+ *   are distinct; an id outside 0 .. E-1 has no part in it); dweights fp32
+ *   [T][k]; dlogits [T][lddl] dtype dt output.  Limits and errors as for moe_route.
+ */
+nm_status moe_route_bwd(nm_dtype dt, const void* logits, int64_t ldl, int64_t T, int64_t E, nm_score score, int k,
+                        int renorm, float scale, const int32_t* ids, const float* weights, const float* dweights,
+                        void* dlogits, int64_t lddl, nm_stream stream);
+
+/*
+ * moe_plan -- the order of the T * k (token, choice) slots by expert, slots of one
+ * expert in ascending order; each expert's run of rows starts at a multiple of
+ * `align` (1, or a power of two up to 256).
+ *   ids [T][k]; a slot whose id lies outside 0 .. E-1 belongs to no expert
+ *   offsets int32 [E + 1]: expert e's rows are offsets[e] .. offsets[e + 1] - 1, the
+ *           last of them padding; counts int32 [E]: how many are not padding
+ *   src int32 [rows]: the slot t * k + j of each row, -1 for padding and for every
+ *           row from offsets[E] on
+ *   pos int32 [T][k]: the row of each slot, -1 for a slot of no expert
+ *   rows >= T * k + min(T * k, E) * (align - 1) rounded up to align (NM_ERR_SHAPE)
+ *   work device memory, 4-byte aligned, of moe_plan_work_bytes bytes (NULL when that is 0;
+ *           NM_ERR_SHAPE when work_bytes is less)
+ * rows < 2^31, 1 <= E <= 1024 and T * k <= 2^30.  The result does not depend on the
+ * order in which threads run.
+ */
+nm_status moe_plan(const int32_t* ids, int64_t T, int k, int64_t E, int align, int32_t* offsets, int32_t* counts,
+                   int32_t* src, int64_t rows, int32_t* pos, void* work, int64_t work_bytes, nm_stream stream);
+
+/* Host only: the work bytes moe_plan uses (*bytes; 0 for small T * k). */
+nm_status moe_plan_work_bytes(int64_t T, int k, int64_t E, int64_t* bytes);
+
+/*
+ * fp8_quantize -- rows to 8 bits in blocks of 128 along K, with a power-of-two scale:
+ *   x[r][c] = X[src[r] / div][c] (src NULL: X[r][c]); 0 where src[r] / div is not a row of X;
+ *             0 where gate is given and gate[r][c] is not > 0 (gate = X: ReLU; gate = the
+ *             forward's pre-activations: the gradient of ReLU)
+ *   S[kb][r] = the smallest power of two (at least 2^-126) that is >= amax / 448 (e4m3) or
+ *             amax / 57344 (e5m2), amax the largest finite |x| of the block; 1 when that is 0
+ *   Q[r][c] = x[r][c] / S[kb][r] rounded to nearest even (the division is exact)
+ * so no finite value saturates, and a NaN or infinite x becomes NaN.
+ *   X [RX][ldx] dtype dt, src int32 [R], gate [R][ldg] dtype dt
+ *   Q [R][ldq] bytes, ldq >= Kp = K rounded up to 128: columns K .. Kp-1 are written 0
+ *   S fp32 [Kp / 128][lds], lds >= R
+ * src == NULL needs R <= RX.  16-byte aligned rows run with vector loads.
+ */
+nm_status fp8_quantize(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, const int32_t* src, int div,
+                       const void* gate, int64_t ldg, int64_t R, int64_t K, nm_fp8 fmt, uint8_t* Q, int64_t ldq,
+                       float* S, int64_t lds, nm_stream stream);
+
+/*
+ * fp8_quantize_t -- the same x transposed, in blocks of 128 along its rows: the operands of a
+ * weight gradient, whose reduction runs over the rows.
+ *   Qt [K][ldqt] bytes, ldqt >= Rp = R rounded up to 128: columns R .. Rp-1 are written 0
+ *   St fp32 [Rp / 128][ldst], ldst >= K
+ */
+nm_status fp8_quantize_t(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, const int32_t* src, int div,
+                         const void* gate, int64_t ldg, int64_t R, int64_t K, nm_fp8 fmt, uint8_t* Qt, int64_t ldqt,
+                         float* St, int64_t ldst, nm_stream stream);
+
+/*
+ * fp8_quantize_weight -- E weights [N][K] (W[e] = W + e * N * ldw) to 8 bits in 128 x 128 blocks
+ * (scales as fp8_quantize's), and optionally the same bytes transposed, for the input gradient.
+ *   Q [E][N][ldq], ldq >= Kp, columns K .. Kp-1 written 0; S fp32 [E][ceil(N / 128)][Kp / 128]
+ *   Qt [E][K][ldqt], ldqt >= Np = N rounded up to 128, columns N .. Np-1 written 0, and
+ *   St fp32 [E][Kp / 128][Np / 128]: both given or both NULL
+ */
+nm_status fp8_quantize_weight(nm_dtype dt, const void* W, int64_t ldw, int64_t E, int64_t N, int64_t K, nm_fp8 fmt,
+                              uint8_t* Q, int64_t ldq, float* S, uint8_t* Qt, int64_t ldqt, float* St,
+                              nm_stream stream);
+
+/*
+ * fp8_gemm_nt -- the product of two 8-bit matrices, both K-contiguous:
+ *   C[m][n] = sum_kb sa[kb][m] sb(n, kb) sum_{k in kb} A[m][k] B[n][k]
+ *   A [M][lda] format fa, sa fp32 [ceil(K / 128)][ldsa], ldsa >= M
+ *   B [N][ldb] format fb; sb by blocks (b_block 128): [ceil(N / 128)][ldsb], ldsb >= ceil(K / 128),
+ *     or by rows (b_block 1): [ceil(K / 128)][ldsb], ldsb >= N
+ *   C [M][ldc] fp32 or bf16 (out)
+ * Each 128-block is summed in fp32 by the matrix instructions, scaled and added in fp32; the result
+ * is rounded once.  The tiled kernels run when lda and ldb are multiples of 16, A and B are 16-byte
+ * aligned (the rows are then read whole, up to K rounded up to 16); other calls take a slower
+ * general kernel.
+ */
+nm_status fp8_gemm_nt(nm_fp8 fa, const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, nm_fp8 fb,
+                      const uint8_t* B, int64_t ldb, const float* sb, int64_t ldsb, int b_block, int64_t M,
+                      int64_t N, int64_t K, nm_dtype out, void* C, int64_t ldc, nm_stream stream);
+
+/*
+ * fp8_gemm_nt_grouped -- fp8_gemm_nt with a B for every group of A's rows (a mixture-of-experts
+ * layer's forward, and its input gradient with the transposed weights):
+ *   C[m][n] = the product of A's row m with B[e], offsets[e] <= m < offsets[e + 1]
+ *   A [rows][lda], sa [ceil(K / 128)][ldsa], ldsa >= rows
+ *   B [E][N][ldb], sb [E][ceil(N / 128)][ldsb] by blocks
+ *   offsets device int32 [E + 1], not decreasing (values are taken as at least 0 and at most rows)
+ *   C [rows][ldc]; rows outside every group are written 0.  1 <= E <= 1024, rows < 2^31.
+ */
+nm_status fp8_gemm_nt_grouped(nm_fp8 fa, const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, nm_fp8 fb,
+                              const uint8_t* B, int64_t ldb, const float* sb, int64_t ldsb, const int32_t* offsets,
+                              int64_t E, int64_t rows, int64_t N, int64_t K, nm_dtype out, void* C, int64_t ldc,
+                              nm_stream stream);
+
+/*
+ * fp8_gemm_nt_grouped_k -- a product for every run of the reduction dimension (the experts' weight
+ * gradients):
+ *   C[e][m][n] = sum over offsets[e] <= k < offsets[e + 1] of A[m][k] B[n][k], scaled as above
+ *   A [M][lda], sa [rows / 128][ldsa], ldsa >= M; B [N][ldb], sb [rows / 128][ldsb], ldsb >= N
+ *   offsets device int32 [E + 1] multiples of 128, as moe_plan writes them with align 128 or 256
+ *           (any other value counts as the next lower multiple of 128)
+ *   C [E][M][ldc]; a group with no columns is written 0.  rows % 128 == 0 (NM_ERR_SHAPE).
+ */
+nm_status fp8_gemm_nt_grouped_k(nm_fp8 fa, const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, nm_fp8 fb,
+                                const uint8_t* B, int64_t ldb, const float* sb, int64_t ldsb,
+                                const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t rows, nm_dtype out,
+                                void* C, int64_t ldc, nm_stream stream);
+
+/*
+ * moe_combine -- Y[t][c] = sum_j weights[t][j] O[pos[t][j]][c], summed in fp32 in ascending j
+ * (weights NULL: all 1, the gradient of gathering the tokens' rows); a pos outside 0 .. rows-1 adds
+ * nothing, whatever its weight.
+ *   O [rows][ldo] dtype dt, pos int32 [T][k], weights fp32 [T][k], Y [T][ldy] dtype dt.  1 <= k <= 64.
+ */
+nm_status moe_combine(nm_dtype dt, const void* O, int64_t ldo, int64_t rows, const int32_t* pos,
+                      const float* weights, int64_t T, int k, int64_t D, void* Y, int64_t ldy, nm_stream stream);
+
+/*
+ * moe_combine_bwd -- the gradients of moe_combine:
+ *   dO[pos[t][j]][c] = weights[t][j] dY[t][c], and 0 in the rows whose src is negative
+ *   dweights[t][j] = sum_c dY[t][c] O[pos[t][j]][c], 0 where pos is outside 0 .. rows-1
+ *   src [rows] and pos [T][k] as moe_plan writes them; dO [rows][lddo] dtype dt, dweights fp32 [T][k]
+ */
+nm_status moe_combine_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int64_t rows,
+                          const int32_t* src, const int32_t* pos, const float* weights, int64_t T, int k, int64_t D,
+                          void* dO, int64_t lddo, float* dweights, nm_stream stream);
 
 /*
  * nm_sizes -- host-only helper: element count of values, bytes of meta and of

@@ -1,5 +1,6 @@
 """MI355X (gfx950) semi-structured sparse FFN matmuls: N:M and V:N:M pruning,
-compression and sparse x dense products behind the libnmsparse C ABI.
+compression and sparse x dense products, and the mixture-of-experts FFN in
+8-bit floating point, behind the libnmsparse C ABI.
 
 The binding functions live in `sparse_matmul_ffns_amd.nmsparse`; the library
 is loaded on first use and must have been built with
@@ -9,8 +10,20 @@ is loaded on first use and must have been built with
 from .nmsparse import (  # noqa: F401
     NM_ERR_TOO_LARGE,
     NmError,
+    fp8_gemm_nt,
+    fp8_gemm_nt_grouped,
+    fp8_gemm_nt_grouped_k,
+    fp8_quantize,
+    fp8_quantize_t,
+    fp8_quantize_weight,
     lib,
     mfma_rate_probe,
+    moe_combine,
+    moe_combine_bwd,
+    moe_plan,
+    moe_plan_rows,
+    moe_route,
+    moe_route_bwd,
     nm_compress,
     nm_decompress,
     nm_prune,

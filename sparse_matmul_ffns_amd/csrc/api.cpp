@@ -2,6 +2,7 @@
 // Every check runs on the host before anything is launched; a call that
 // returns an error has touched no device memory.
 #include <hip/hip_runtime.h>
+#include <stdint.h>
 #include <string.h>
 
 #include "../../include/nmsparse.h"
@@ -26,6 +27,36 @@ bool m_ok(int M) { return M == 4 || M == 8 || M == 16; }
 bool nm_ok(int N, int M) { return m_ok(M) && N >= 1 && N < M; }
 bool v_ok(int V) { return V >= 1 && V <= 256; }
 hipStream_t hs(nm_stream s) { return reinterpret_cast<hipStream_t>(s); }
+
+bool score_ok(nm_score s) { return s == NM_SOFTMAX || s == NM_SIGMOID; }
+bool scale_ok(float s) { return s != 0.f && s - s == 0.f; }   // not 0, infinite or NaN
+bool fp8_ok(nm_fp8 f) { return f == NM_E4M3 || f == NM_E5M2; }
+int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
+
+// the checks fp8_quantize and fp8_quantize_t share
+nm_status quantize_check(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, const int32_t* src, int div,
+                         const void* gate, int64_t ldg, int64_t R, int64_t K, nm_fp8 fmt, const void* Q, const void* S) {
+  if (!X || !Q || !S) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || !fp8_ok(fmt)) return NM_ERR_UNSUPPORTED;
+  if (R <= 0 || K <= 0 || RX <= 0 || R > INT32_MAX || K > INT32_MAX || ldx < K || (src ? div < 1 : R > RX) ||
+      (gate && ldg < K))
+    return NM_ERR_SHAPE;
+  if (!aligned(X, esize(dt)) || !aligned(gate, esize(dt)) || !aligned(src, 4) || !aligned(S, 4)) return NM_ERR_ALIGN;
+  return NM_OK;
+}
+
+// the checks the 8-bit products share
+nm_status fp8_gemm_check(nm_fp8 fa, const void* A, int64_t lda, const void* sa, int64_t ldsa, nm_fp8 fb, const void* B,
+                         int64_t ldb, const void* sb, int64_t M, int64_t N, int64_t K, nm_dtype out, const void* C,
+                         int64_t ldc) {
+  if (!A || !sa || !B || !sb || !C) return NM_ERR_NULL;
+  if (!fp8_ok(fa) || !fp8_ok(fb) || !dtype_ok(out)) return NM_ERR_UNSUPPORTED;
+  if (M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || lda < K || ldb < K || ldsa < M ||
+      ldc < N)
+    return NM_ERR_SHAPE;
+  if (!aligned(sa, 4) || !aligned(sb, 4) || !aligned(C, esize(out))) return NM_ERR_ALIGN;
+  return NM_OK;
+}
 
 }  // namespace
 
@@ -331,6 +362,161 @@ nm_status sddmm_nm_dt(nm_dtype dt, const void* D, int64_t ldd, const void* X, in
   return hip_status(nms::launch_sddmm_nm_dt(dt, D, ldd, X, ldx, R, Kc, T, meta, values_out, Dt, lddt, hs(stream)));
 }
 
+nm_status moe_route(nm_dtype dt, const void* logits, int64_t ldl, int64_t T, int64_t E, nm_score score,
+                    const float* bias, int groups, int topk_groups, int group_top, int k, int renorm, float scale,
+                    int32_t* ids, float* weights, nm_stream stream) {
+  if (!logits || !ids || !weights) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || !score_ok(score) || E > 1024 || k > 64 || groups > 64 || group_top < 1 || group_top > 2 ||
+      !scale_ok(scale))
+    return NM_ERR_UNSUPPORTED;
+  if (T <= 0 || E <= 0 || k <= 0 || groups <= 0 || topk_groups <= 0 || topk_groups > groups || E % groups != 0 ||
+      k > E / groups * topk_groups || ldl < E || T > INT32_MAX / k)
+    return NM_ERR_SHAPE;
+  if (!aligned(logits, esize(dt)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return NM_ERR_ALIGN;
+  const nms::RouteArgs a{logits, ldl, T, (int)E, score == NM_SIGMOID, bias, groups, topk_groups, group_top, k,
+                         renorm != 0, scale, ids, weights};
+  return hip_status(nms::launch_moe_route(dt, a, hs(stream)));
+}
+
+nm_status moe_route_bwd(nm_dtype dt, const void* logits, int64_t ldl, int64_t T, int64_t E, nm_score score, int k,
+                        int renorm, float scale, const int32_t* ids, const float* weights, const float* dweights,
+                        void* dlogits, int64_t lddl, nm_stream stream) {
+  if (!logits || !ids || !weights || !dweights || !dlogits) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || !score_ok(score) || E > 1024 || k > 64 || !scale_ok(scale)) return NM_ERR_UNSUPPORTED;
+  if (T <= 0 || E <= 0 || k <= 0 || k > E || ldl < E || lddl < E || T > INT32_MAX / k) return NM_ERR_SHAPE;
+  if (!aligned(logits, esize(dt)) || !aligned(dlogits, esize(dt)) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(dweights, 4))
+    return NM_ERR_ALIGN;
+  return hip_status(nms::launch_moe_route_bwd(dt, logits, ldl, T, (int)E, score == NM_SIGMOID, k, renorm != 0, scale,
+                                              ids, weights, dweights, dlogits, lddl, hs(stream)));
+}
+
+nm_status moe_plan_work_bytes(int64_t T, int k, int64_t E, int64_t* bytes) {
+  if (!bytes) return NM_ERR_NULL;
+  *bytes = 0;
+  if (E > 1024 || k > 64) return NM_ERR_UNSUPPORTED;
+  if (T <= 0 || k <= 0 || E <= 0 || T > (int64_t(1) << 30) / k) return NM_ERR_SHAPE;
+  *bytes = nms::moe_plan_work_bytes(T * k, E);
+  return NM_OK;
+}
+
+nm_status moe_plan(const int32_t* ids, int64_t T, int k, int64_t E, int align, int32_t* offsets, int32_t* counts,
+                   int32_t* src, int64_t rows, int32_t* pos, void* work, int64_t work_bytes, nm_stream stream) {
+  if (!ids || !offsets || !counts || !src || !pos) return NM_ERR_NULL;
+  if (E > 1024 || k > 64 || align < 1 || align > 256 || (align & (align - 1)) != 0) return NM_ERR_UNSUPPORTED;
+  if (T <= 0 || k <= 0 || E <= 0 || T > (int64_t(1) << 30) / k || rows > INT32_MAX) return NM_ERR_SHAPE;
+  const int64_t n = T * k;
+  const int64_t need = (n + (n < E ? n : E) * (align - 1) + align - 1) / align * align;
+  if (rows < need) return NM_ERR_SHAPE;
+  const int64_t wb = nms::moe_plan_work_bytes(n, E);
+  if (wb > 0 && !work) return NM_ERR_NULL;
+  if (work_bytes < wb) return NM_ERR_SHAPE;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(src, 4) || !aligned(pos, 4) ||
+      !aligned(work, 4))
+    return NM_ERR_ALIGN;
+  return hip_status(nms::launch_moe_plan(ids, n, (int)E, align, offsets, counts, src, rows, pos, (int32_t*)work,
+                                         hs(stream)));
+}
+
+nm_status fp8_quantize(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, const int32_t* src, int div,
+                       const void* gate, int64_t ldg, int64_t R, int64_t K, nm_fp8 fmt, uint8_t* Q, int64_t ldq,
+                       float* S, int64_t lds, nm_stream stream) {
+  const nm_status st = quantize_check(dt, X, ldx, RX, src, div, gate, ldg, R, K, fmt, Q, S);
+  if (st != NM_OK) return st;
+  if (ldq < up128(K) || lds < R) return NM_ERR_SHAPE;
+  const nms::QuantArgs a{X, ldx, RX, src, div, gate, ldg, R, K, fmt == NM_E5M2, Q, ldq, S, lds};
+  return hip_status(nms::launch_fp8_quantize(dt, a, hs(stream)));
+}
+
+nm_status fp8_quantize_t(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, const int32_t* src, int div,
+                         const void* gate, int64_t ldg, int64_t R, int64_t K, nm_fp8 fmt, uint8_t* Qt, int64_t ldqt,
+                         float* St, int64_t ldst, nm_stream stream) {
+  const nm_status st = quantize_check(dt, X, ldx, RX, src, div, gate, ldg, R, K, fmt, Qt, St);
+  if (st != NM_OK) return st;
+  if (ldqt < up128(R) || ldst < K) return NM_ERR_SHAPE;
+  const nms::QuantArgs a{X, ldx, RX, src, div, gate, ldg, R, K, fmt == NM_E5M2, Qt, ldqt, St, ldst};
+  return hip_status(nms::launch_fp8_quantize_t(dt, a, hs(stream)));
+}
+
+nm_status fp8_quantize_weight(nm_dtype dt, const void* W, int64_t ldw, int64_t E, int64_t N, int64_t K, nm_fp8 fmt,
+                              uint8_t* Q, int64_t ldq, float* S, uint8_t* Qt, int64_t ldqt, float* St,
+                              nm_stream stream) {
+  if (!W || !Q || !S || (!Qt != !St)) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || !fp8_ok(fmt)) return NM_ERR_UNSUPPORTED;
+  if (E <= 0 || E > 65535 || N <= 0 || K <= 0 || N > INT32_MAX || K > INT32_MAX || ldw < K || ldq < up128(K) ||
+      (Qt && ldqt < up128(N)))
+    return NM_ERR_SHAPE;
+  if (!aligned(W, esize(dt)) || !aligned(S, 4) || !aligned(St, 4)) return NM_ERR_ALIGN;
+  return hip_status(nms::launch_fp8_quantize_weight(dt, W, ldw, E, N, K, fmt == NM_E5M2, Q, ldq, S, Qt, ldqt, St,
+                                                    hs(stream)));
+}
+
+nm_status fp8_gemm_nt(nm_fp8 fa, const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, nm_fp8 fb,
+                      const uint8_t* B, int64_t ldb, const float* sb, int64_t ldsb, int b_block, int64_t M, int64_t N,
+                      int64_t K, nm_dtype out, void* C, int64_t ldc, nm_stream stream) {
+  const nm_status st = fp8_gemm_check(fa, A, lda, sa, ldsa, fb, B, ldb, sb, M, N, K, out, C, ldc);
+  if (st != NM_OK) return st;
+  if (b_block != 1 && b_block != 128) return NM_ERR_UNSUPPORTED;
+  if (ldsb < (b_block == 1 ? N : up128(K) / 128)) return NM_ERR_SHAPE;
+  const nms::Fp8Gemm g{nms::G_DENSE, fa == NM_E5M2, fb == NM_E5M2, b_block, out == NM_BF16, A, lda, sa, ldsa, B, ldb,
+                       sb, ldsb, nullptr, 1, M, N, K, C, ldc};
+  return hip_status(nms::launch_fp8_gemm(g, hs(stream)));
+}
+
+nm_status fp8_gemm_nt_grouped(nm_fp8 fa, const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, nm_fp8 fb,
+                              const uint8_t* B, int64_t ldb, const float* sb, int64_t ldsb, const int32_t* offsets,
+                              int64_t E, int64_t rows, int64_t N, int64_t K, nm_dtype out, void* C, int64_t ldc,
+                              nm_stream stream) {
+  if (!offsets) return NM_ERR_NULL;
+  const nm_status st = fp8_gemm_check(fa, A, lda, sa, ldsa, fb, B, ldb, sb, rows, N, K, out, C, ldc);
+  if (st != NM_OK) return st;
+  if (E > 1024) return NM_ERR_UNSUPPORTED;
+  if (E <= 0 || rows > INT32_MAX || ldsb < up128(K) / 128) return NM_ERR_SHAPE;
+  if (!aligned(offsets, 4)) return NM_ERR_ALIGN;
+  const nms::Fp8Gemm g{nms::G_ROWS, fa == NM_E5M2, fb == NM_E5M2, 128, out == NM_BF16, A, lda, sa, ldsa, B, ldb, sb,
+                       ldsb, offsets, (int)E, rows, N, K, C, ldc};
+  return hip_status(nms::launch_fp8_gemm(g, hs(stream)));
+}
+
+nm_status fp8_gemm_nt_grouped_k(nm_fp8 fa, const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, nm_fp8 fb,
+                                const uint8_t* B, int64_t ldb, const float* sb, int64_t ldsb, const int32_t* offsets,
+                                int64_t E, int64_t M, int64_t N, int64_t rows, nm_dtype out, void* C, int64_t ldc,
+                                nm_stream stream) {
+  if (!offsets) return NM_ERR_NULL;
+  const nm_status st = fp8_gemm_check(fa, A, lda, sa, ldsa, fb, B, ldb, sb, M, N, rows, out, C, ldc);
+  if (st != NM_OK) return st;
+  if (E > 1024) return NM_ERR_UNSUPPORTED;
+  if (E <= 0 || rows > INT32_MAX || rows % 128 != 0 || ldsb < N) return NM_ERR_SHAPE;
+  if (!aligned(offsets, 4)) return NM_ERR_ALIGN;
+  const nms::Fp8Gemm g{nms::G_RED, fa == NM_E5M2, fb == NM_E5M2, 1, out == NM_BF16, A, lda, sa, ldsa, B, ldb, sb, ldsb,
+                       offsets, (int)E, M, N, rows, C, ldc};
+  return hip_status(nms::launch_fp8_gemm(g, hs(stream)));
+}
+
+nm_status moe_combine(nm_dtype dt, const void* O, int64_t ldo, int64_t rows, const int32_t* pos, const float* weights,
+                      int64_t T, int k, int64_t D, void* Y, int64_t ldy, nm_stream stream) {
+  if (!O || !pos || !Y) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || k > 64) return NM_ERR_UNSUPPORTED;
+  if (T <= 0 || k <= 0 || D <= 0 || rows <= 0 || rows > INT32_MAX || T > INT32_MAX / k || ldo < D || ldy < D)
+    return NM_ERR_SHAPE;
+  if (!aligned(O, esize(dt)) || !aligned(Y, esize(dt)) || !aligned(pos, 4) || !aligned(weights, 4)) return NM_ERR_ALIGN;
+  return hip_status(nms::launch_moe_combine(dt, O, ldo, rows, pos, weights, T, k, D, Y, ldy, hs(stream)));
+}
+
+nm_status moe_combine_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int64_t rows,
+                          const int32_t* src, const int32_t* pos, const float* weights, int64_t T, int k, int64_t D,
+                          void* dO, int64_t lddo, float* dweights, nm_stream stream) {
+  if (!dY || !O || !src || !pos || !weights || !dO || !dweights) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || k > 64) return NM_ERR_UNSUPPORTED;
+  if (T <= 0 || k <= 0 || D <= 0 || rows <= 0 || rows > INT32_MAX || T > INT32_MAX / k || lddy < D || ldo < D || lddo < D)
+    return NM_ERR_SHAPE;
+  if (!aligned(dY, esize(dt)) || !aligned(O, esize(dt)) || !aligned(dO, esize(dt)) || !aligned(src, 4) ||
+      !aligned(pos, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    return NM_ERR_ALIGN;
+  return hip_status(nms::launch_moe_combine_bwd(dt, dY, lddy, O, ldo, rows, src, pos, weights, T, k, D, dO, lddo,
+                                                dweights, hs(stream)));
+}
+
 void nm_sizes(int64_t R, int64_t K, int N, int M, int V, int64_t* n_values, int64_t* meta_bytes,
               int64_t* colsel_bytes) {
   if (M <= 0) M = 4;
@@ -351,7 +537,7 @@ const char* nm_status_str(nm_status status) {
     case NM_OK: return "ok";
     case NM_ERR_NULL: return "a required pointer is NULL";
     case NM_ERR_SHAPE: return "invalid shape or leading dimension";
-    case NM_ERR_UNSUPPORTED: return "unsupported dtype, N:M pattern or block size";
+    case NM_ERR_UNSUPPORTED: return "unsupported dtype, N:M pattern, block size or option";
     case NM_ERR_ALIGN: return "pointer not aligned to its element size";
     case NM_ERR_HIP: return "HIP launch failed";
     case NM_ERR_TOO_LARGE: return "the operand needs more scratch memory than the library's fixed buffer holds";

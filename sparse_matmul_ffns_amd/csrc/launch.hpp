@@ -115,4 +115,65 @@ hipError_t launch_spmm_venom_tn(int dt, const void* hv, const uint8_t* hm, const
 hipError_t launch_sddmm_nm(int dt, const void* D, int64_t ldd, const void* X, int64_t ldx, int64_t R,
                            int64_t Kc, int64_t T, const uint8_t* meta, float* out, hipStream_t s);
 
+// The mixture-of-experts FFN in 8 bits.
+struct RouteArgs {
+  const void* logits;
+  int64_t ldl, T;
+  int E, sigmoid;
+  const float* bias;
+  int groups, topk_groups, group_top, k, renorm;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+hipError_t launch_moe_route(int dt, const RouteArgs& a, hipStream_t s);
+hipError_t launch_moe_route_bwd(int dt, const void* logits, int64_t ldl, int64_t T, int E, int sigmoid, int k, int renorm,
+                                float scale, const int32_t* ids, const float* weights, const float* dweights,
+                                void* dlogits, int64_t lddl, hipStream_t s);
+int64_t moe_plan_work_bytes(int64_t n, int64_t E);
+hipError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int align, int32_t* offsets, int32_t* counts,
+                           int32_t* src, int64_t rows, int32_t* pos, int32_t* work, hipStream_t s);
+hipError_t launch_moe_combine(int dt, const void* O, int64_t ldo, int64_t rows, const int32_t* pos, const float* w,
+                              int64_t T, int k, int64_t D, void* Y, int64_t ldy, hipStream_t s);
+hipError_t launch_moe_combine_bwd(int dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int64_t rows,
+                                  const int32_t* src, const int32_t* pos, const float* w, int64_t T, int k, int64_t D,
+                                  void* dO, int64_t lddo, float* dw, hipStream_t s);
+struct QuantArgs {
+  const void* X;
+  int64_t ldx, RX;
+  const int32_t* src;
+  int div;
+  const void* gate;
+  int64_t ldg, R, K;
+  int e5m2;
+  uint8_t* Q;
+  int64_t ldq;
+  float* S;
+  int64_t lds;
+};
+hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s);
+hipError_t launch_fp8_quantize_t(int dt, const QuantArgs& a, hipStream_t s);
+hipError_t launch_fp8_quantize_weight(int dt, const void* W, int64_t ldw, int64_t E, int64_t N, int64_t K, int e5m2,
+                                      uint8_t* Q, int64_t ldq, float* S, uint8_t* Qt, int64_t ldqt, float* St,
+                                      hipStream_t s);
+// One product (mode 0), or one for every group of A's rows (1) or of the reduction (2).
+enum { G_DENSE = 0, G_ROWS = 1, G_RED = 2 };
+struct Fp8Gemm {
+  int mode, a_e5m2, b_e5m2, b_block, bf16_out;
+  const uint8_t* A;
+  int64_t lda;
+  const float* sa;
+  int64_t ldsa;
+  const uint8_t* B;
+  int64_t ldb;
+  const float* sb;
+  int64_t ldsb;
+  const int32_t* offsets;   // G_ROWS, G_RED
+  int E;
+  int64_t M, N, K;          // G_ROWS: M = rows; G_RED: K = rows
+  void* C;
+  int64_t ldc;
+};
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s);
+
 }  // namespace nms

@@ -21,10 +21,13 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "nmsparse.h")
 
 NM_OK, NM_ERR_NULL, NM_ERR_SHAPE, NM_ERR_UNSUPPORTED, NM_ERR_ALIGN, NM_ERR_HIP, NM_ERR_TOO_LARGE = range(7)
 NM_F32, NM_BF16 = 0, 1
+NM_E4M3, NM_E5M2 = 0, 1
+NM_SOFTMAX, NM_SIGMOID = 0, 1
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _vp = ctypes.c_void_p
+_f32 = ctypes.c_float
 
 # name -> argument types, in header order
 _SIGNATURES = {
@@ -56,6 +59,21 @@ _SIGNATURES = {
     "nm_reprune_t": [_int, _vp, _vp, _i64, _i64, _vp, _vp, _vp],
     "sddmm_nm": [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp],
     "sddmm_nm_dt": [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp],
+    "moe_route": [_int, _vp, _i64, _i64, _i64, _int, _vp, _int, _int, _int, _int, _int, _f32, _vp, _vp, _vp],
+    "moe_route_bwd": [_int, _vp, _i64, _i64, _i64, _int, _int, _int, _f32, _vp, _vp, _vp, _vp, _i64, _vp],
+    "moe_plan": [_vp, _i64, _int, _i64, _int, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp],
+    "moe_plan_work_bytes": [_i64, _int, _i64, ctypes.POINTER(_i64)],
+    "fp8_quantize": [_int, _vp, _i64, _i64, _vp, _int, _vp, _i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp],
+    "fp8_quantize_t": [_int, _vp, _i64, _i64, _vp, _int, _vp, _i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp],
+    "fp8_quantize_weight": [_int, _vp, _i64, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp, _vp],
+    "fp8_gemm_nt": [_int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _int, _i64, _i64, _i64, _int, _vp, _i64,
+                    _vp],
+    "fp8_gemm_nt_grouped": [_int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int,
+                            _vp, _i64, _vp],
+    "fp8_gemm_nt_grouped_k": [_int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64,
+                              _int, _vp, _i64, _vp],
+    "moe_combine": [_int, _vp, _i64, _i64, _vp, _vp, _i64, _int, _i64, _vp, _i64, _vp],
+    "moe_combine_bwd": [_int, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _int, _i64, _vp, _i64, _vp, _vp],
 }
 
 _lib = None
@@ -618,3 +636,322 @@ def sddmm_nm(D: torch.Tensor, X: torch.Tensor, meta: torch.Tensor, out=None, Dt=
     _check(lib().sddmm_nm(_dt(D), _p(D), _rows(D, "D"), _p(X), _rows(X, "X"), R, Kc, T, _p(meta), _p(out),
                           _stream()), "sddmm_nm")
     return out
+
+
+# ---------------------------------------------------------------------------
+# The mixture-of-experts FFN in 8-bit floating point
+# ---------------------------------------------------------------------------
+_SCORES = {"softmax": NM_SOFTMAX, "sigmoid": NM_SIGMOID}
+_FP8 = {torch.float8_e4m3fn: NM_E4M3, torch.float8_e5m2: NM_E5M2}
+
+
+def _up(n: int, m: int) -> int:
+    return (n + m - 1) // m * m
+
+
+def _ld(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous; strides of dimensions of one element are
+    whatever torch left there and do not count."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _fp8(t: torch.Tensor, name: str) -> int:
+    fmt = _FP8.get(t.dtype)
+    if fmt is None:
+        raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, not {t.dtype}")
+    return fmt
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return _SCORES[score]
+
+
+def _of(t: torch.Tensor, shape, dtype, name: str) -> None:
+    """A contiguous tensor of the given shape and dtype."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+
+
+def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+              group_top: int = 2, renorm: bool = True, scale: float = 1.0, ids=None, weights=None):
+    """The k experts of every token and their weights from router logits [T, E]: returns (ids [T, k]
+    int32, weights [T, k] fp32).  Experts are taken by softmax or sigmoid score plus `bias` [E] (which
+    has no part in the weights), from the topk_groups best of `groups` runs of experts; -1 and weight 0
+    where fewer than k experts have a logit above -infinity."""
+    _dev(logits, bias, ids, weights)
+    ldl = _ld(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _of(bias, (E,), torch.float32, "bias")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _of(ids, (T, k), torch.int32, "ids"), _of(weights, (T, k), torch.float32, "weights")
+    _check(lib().moe_route(_dt(logits), _p(logits), ldl, T, E, _score(score), _p(bias), groups, topk_groups, group_top,
+                           k, int(bool(renorm)), scale, _p(ids), _p(weights), _stream()), "moe_route")
+    return ids, weights
+
+
+def moe_route_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, dweights: torch.Tensor,
+                  score: str = "softmax", renorm: bool = True, scale: float = 1.0, dlogits=None) -> torch.Tensor:
+    """The gradient [T, E] of moe_route's weights with respect to the logits, in the logits' dtype."""
+    _dev(logits, ids, weights, dweights, dlogits)
+    ldl = _ld(logits, "logits")
+    T, E = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    k = ids.shape[1]
+    _of(ids, (T, k), torch.int32, "ids"), _of(weights, (T, k), torch.float32, "weights")
+    _of(dweights, (T, k), torch.float32, "dweights")
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    if tuple(dlogits.shape) != (T, E) or dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must be [T, E] with the logits' dtype")
+    _check(lib().moe_route_bwd(_dt(logits), _p(logits), ldl, T, E, _score(score), k, int(bool(renorm)), scale, _p(ids),
+                               _p(weights), _p(dweights), _p(dlogits), _ld(dlogits, "dlogits"), _stream()),
+           "moe_route_bwd")
+    return dlogits
+
+
+def moe_plan_rows(n: int, E: int, align: int = 1) -> int:
+    """Rows that n (token, choice) slots can take with every expert's run padded to `align`."""
+    return _up(n + min(n, E) * (align - 1), align)
+
+
+def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=None, src=None, pos=None, work="auto"):
+    """The order of the T * k slots by expert: returns (offsets [E + 1], counts [E], src [rows], pos
+    [T, k]), int32.  `work`: an int32 device tensor, or "auto" (allocated with torch when the call uses
+    it)."""
+    _dev(ids, offsets, counts, src, pos)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    T, k = ids.shape
+    _of(ids, (T, k), torch.int32, "ids")
+    dev = ids.device
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if src is None:
+        src = torch.empty(moe_plan_rows(T * k, E, align), dtype=torch.int32, device=dev)
+    if pos is None:
+        pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    _of(offsets, (E + 1,), torch.int32, "offsets"), _of(counts, (E,), torch.int32, "counts")
+    _of(src, (src.numel(),), torch.int32, "src"), _of(pos, (T, k), torch.int32, "pos")
+    if isinstance(work, str):
+        if work != "auto":
+            raise ValueError("work must be a tensor, None or 'auto'")
+        need = _i64()
+        _check(lib().moe_plan_work_bytes(T, k, E, ctypes.byref(need)), "moe_plan_work_bytes")
+        work = torch.empty(need.value // 4, dtype=torch.int32, device=dev) if need.value else None
+    if work is not None:
+        _dev(work)
+        _flat(work, "work")
+    _check(lib().moe_plan(_p(ids), T, k, E, align, _p(offsets), _p(counts), _p(src), src.numel(), _p(pos), _p(work),
+                          work.numel() * work.element_size() if work is not None else 0, _stream()), "moe_plan")
+    return offsets, counts, src, pos
+
+
+def _quantize_args(X, src, gate):
+    _dev(X, src, gate)
+    ldx = _ld(X, "X")
+    RX, K = X.shape
+    R = RX
+    if src is not None:
+        R = src.numel()
+        _of(src, (R,), torch.int32, "src")
+    if gate is not None and (tuple(gate.shape) != (R, K) or gate.dtype != X.dtype):
+        raise ValueError("gate must be [rows, K] with X's dtype")
+    return ldx, RX, R, K, 0 if gate is None else _ld(gate, "gate")
+
+
+def fp8_quantize(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=None, div: int = 1, gate=None, Q=None,
+                 S=None):
+    """X [rows, K] (or its rows src // div, 0 where src is negative; 0 where gate is not > 0) in 8 bits
+    with a power-of-two scale per row and 128 columns: returns (Q [rows, Kp], S [Kp / 128, rows]), Kp = K
+    rounded up to 128, the columns beyond K 0."""
+    ldx, RX, R, K, ldg = _quantize_args(X, src, gate)
+    _dev(Q, S)
+    Kp = _up(K, 128)
+    if Q is None:
+        Q = torch.empty((R, Kp), dtype=fmt, device=X.device)
+    if S is None:
+        S = torch.empty((Kp // 128, R), dtype=torch.float32, device=X.device)
+    if tuple(Q.shape) != (R, Kp) or tuple(S.shape) != (Kp // 128, R) or S.dtype != torch.float32:
+        raise ValueError("Q must be [rows, Kp] and S an fp32 [Kp / 128, rows] tensor")
+    _check(lib().fp8_quantize(_dt(X), _p(X), ldx, RX, _p(src), div, _p(gate), ldg, R, K, _fp8(Q, "Q"), _p(Q),
+                              _ld(Q, "Q"), _p(S), _ld(S, "S"), _stream()), "fp8_quantize")
+    return Q, S
+
+
+def fp8_quantize_t(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=None, div: int = 1, gate=None, Q=None,
+                   S=None):
+    """fp8_quantize's input transposed, with a scale per column of X and 128 rows: returns (Q [K, Rp],
+    S [Rp / 128, K]), Rp = the rows rounded up to 128, the columns beyond them 0."""
+    ldx, RX, R, K, ldg = _quantize_args(X, src, gate)
+    _dev(Q, S)
+    Rp = _up(R, 128)
+    if Q is None:
+        Q = torch.empty((K, Rp), dtype=fmt, device=X.device)
+    if S is None:
+        S = torch.empty((Rp // 128, K), dtype=torch.float32, device=X.device)
+    if tuple(Q.shape) != (K, Rp) or tuple(S.shape) != (Rp // 128, K) or S.dtype != torch.float32:
+        raise ValueError("Q must be [K, Rp] and S an fp32 [Rp / 128, K] tensor")
+    _check(lib().fp8_quantize_t(_dt(X), _p(X), ldx, RX, _p(src), div, _p(gate), ldg, R, K, _fp8(Q, "Q"), _p(Q),
+                                _ld(Q, "Q"), _p(S), _ld(S, "S"), _stream()), "fp8_quantize_t")
+    return Q, S
+
+
+def fp8_quantize_weight(W: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, transposed: bool = False):
+    """A weight [N, K], or the experts' [E, N, K], in 8 bits with a power-of-two scale per 128 x 128 block:
+    returns (Q [E, N, Kp], S [E, N / 128, K / 128]), and with `transposed` also the same bytes as the
+    input gradient reads them (Qt [E, K, Np], St [E, K / 128, N / 128]).  Without E for a 2-D W."""
+    _dev(W)
+    W3 = W.unsqueeze(0) if W.dim() == 2 else W
+    if W3.dim() != 3:
+        raise ValueError("W must be [N, K] or [E, N, K]")
+    E, N, K = W3.shape
+    ldw = W3.stride(1) if N > 1 else max(W3.stride(1), K)
+    if (W3.stride(2) != 1 and K > 1) or (E > 1 and W3.stride(0) != N * ldw):
+        raise ValueError("W must have contiguous rows and evenly spaced experts")
+    Np, Kp = _up(N, 128), _up(K, 128)
+    dev = W.device
+    Q = torch.empty((E, N, Kp), dtype=fmt, device=dev)
+    S = torch.empty((E, Np // 128, Kp // 128), dtype=torch.float32, device=dev)
+    Qt = torch.empty((E, K, Np), dtype=fmt, device=dev) if transposed else None
+    St = torch.empty((E, Kp // 128, Np // 128), dtype=torch.float32, device=dev) if transposed else None
+    _check(lib().fp8_quantize_weight(_dt(W), _p(W), ldw, E, N, K, _fp8(Q, "fmt"), _p(Q), Kp, _p(S), _p(Qt), Np,
+                                     _p(St), _stream()), "fp8_quantize_weight")
+    out = (Q, S, Qt, St) if transposed else (Q, S)
+    return tuple(t[0] for t in out) if W.dim() == 2 else out
+
+
+def _gemm_out(out, shape, out_dtype, dev):
+    if out is None:
+        return torch.empty(shape, dtype=out_dtype, device=dev)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {list(shape)}")
+    return out
+
+
+def _scales(s: torch.Tensor, shape, name: str) -> int:
+    """Row stride of fp32 scales of at least the given shape."""
+    if s.dtype != torch.float32 or s.shape[0] != shape[0] or s.shape[1] < shape[1]:
+        raise ValueError(f"{name} must be an fp32 tensor of shape {list(shape)}")
+    return _ld(s, name)
+
+
+def fp8_gemm_nt(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, b_block: int = 128,
+                out_dtype: torch.dtype = torch.bfloat16, out=None) -> torch.Tensor:
+    """C = (A with its scales) @ (B with its scales).T for 8-bit A [M, K] and B [N, K]: sa [K / 128, M] per
+    row and 128-block of A; sb [N / 128, K / 128] per 128 x 128 block of B (b_block 128) or [K / 128, N] per
+    row (b_block 1).  C is bf16 or fp32."""
+    _dev(A, sa, B, sb, out)
+    M, K = A.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError("A and B must have the same number of columns")
+    if b_block not in (1, 128):
+        raise ValueError("b_block must be 1 or 128")
+    Kb = _up(K, 128) // 128
+    out = _gemm_out(out, (M, N), out_dtype, A.device)
+    ldsa = _scales(sa, (Kb, M), "sa")
+    ldsb = _scales(sb, (Kb, N) if b_block == 1 else (_up(N, 128) // 128, Kb), "sb")
+    _check(lib().fp8_gemm_nt(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), ldsa, _fp8(B, "B"), _p(B), _ld(B, "B"),
+                             _p(sb), ldsb, b_block, M, N, K, _dt(out), _p(out), _ld(out, "out"), _stream()),
+           "fp8_gemm_nt")
+    return out
+
+
+def fp8_gemm_nt_grouped(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, offsets: torch.Tensor,
+                        out_dtype: torch.dtype = torch.bfloat16, out=None) -> torch.Tensor:
+    """Rows offsets[e] .. offsets[e + 1] - 1 of A [rows, K] times expert e's B [E, N, K] transposed, with
+    sa [K / 128, rows] and sb [E, N / 128, K / 128]: C [rows, N], 0 in the rows of no expert."""
+    _dev(A, sa, B, sb, offsets, out)
+    rows, K = A.shape
+    if B.dim() != 3 or B.shape[2] != K:
+        raise ValueError("B must be [E, N, K] with A's number of columns")
+    E, N = B.shape[:2]
+    Nb, Kb = _up(N, 128) // 128, _up(K, 128) // 128
+    ldb = B.stride(1) if N > 1 else max(B.stride(1), K)
+    if (B.stride(2) != 1 and K > 1) or (E > 1 and B.stride(0) != N * ldb):
+        raise ValueError("B must have contiguous rows and evenly spaced experts")
+    _of(offsets, (E + 1,), torch.int32, "offsets"), _of(sb, (E, Nb, Kb), torch.float32, "sb")
+    out = _gemm_out(out, (rows, N), out_dtype, A.device)
+    _check(lib().fp8_gemm_nt_grouped(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), _scales(sa, (Kb, rows), "sa"),
+                                     _fp8(B, "B"), _p(B), ldb, _p(sb), Kb, _p(offsets), E, rows, N, K, _dt(out), _p(out),
+                                     _ld(out, "out"), _stream()), "fp8_gemm_nt_grouped")
+    return out
+
+
+def fp8_gemm_nt_grouped_k(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, offsets: torch.Tensor,
+                          out_dtype: torch.dtype = torch.float32, out=None) -> torch.Tensor:
+    """For every expert, columns offsets[e] .. offsets[e + 1] - 1 of A [M, rows] times those of B [N, rows]
+    transposed, with sa [rows / 128, M] and sb [rows / 128, N]: C [E, M, N].  The offsets are multiples of
+    128 (moe_plan with align 128)."""
+    _dev(A, sa, B, sb, offsets, out)
+    M, rows = A.shape
+    N = B.shape[0]
+    if B.shape[1] != rows:
+        raise ValueError("A and B must have the same number of columns")
+    E = offsets.numel() - 1
+    _of(offsets, (E + 1,), torch.int32, "offsets")
+    Rb = _up(rows, 128) // 128
+    out = _gemm_out(out, (E, M, N), out_dtype, A.device)
+    _flat(out, "out")
+    _check(lib().fp8_gemm_nt_grouped_k(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), _scales(sa, (Rb, M), "sa"),
+                                       _fp8(B, "B"), _p(B), _ld(B, "B"), _p(sb), _scales(sb, (Rb, N), "sb"),
+                                       _p(offsets), E, M, N, rows, _dt(out), _p(out), N, _stream()),
+           "fp8_gemm_nt_grouped_k")
+    return out
+
+
+def moe_combine(O: torch.Tensor, pos: torch.Tensor, weights=None, out=None) -> torch.Tensor:
+    """Y [T, D]: the sum over j of weights[t, j] times row pos[t, j] of O [rows, D] (weights None: 1)."""
+    _dev(O, pos, weights, out)
+    rows, D = O.shape
+    if pos.dim() != 2:
+        raise ValueError("pos must be [T, k]")
+    T, k = pos.shape
+    _of(pos, (T, k), torch.int32, "pos")
+    if weights is not None:
+        _of(weights, (T, k), torch.float32, "weights")
+    if out is None:
+        out = torch.empty((T, D), dtype=O.dtype, device=O.device)
+    if tuple(out.shape) != (T, D) or out.dtype != O.dtype:
+        raise ValueError("out must be [T, D] with O's dtype")
+    _check(lib().moe_combine(_dt(O), _p(O), _ld(O, "O"), rows, _p(pos), _p(weights), T, k, D, _p(out),
+                             _ld(out, "out"), _stream()), "moe_combine")
+    return out
+
+
+def moe_combine_bwd(dY: torch.Tensor, O: torch.Tensor, src: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
+                    dO=None, dweights=None):
+    """The gradients of moe_combine: (dO [rows, D] in O's dtype, 0 in the rows of no slot; dweights [T, k])."""
+    _dev(dY, O, src, pos, weights, dO, dweights)
+    rows, D = O.shape
+    if pos.dim() != 2:
+        raise ValueError("pos must be [T, k]")
+    T, k = pos.shape
+    if tuple(dY.shape) != (T, D) or dY.dtype != O.dtype:
+        raise ValueError("dY must be [T, D] with O's dtype")
+    _of(src, (rows,), torch.int32, "src"), _of(pos, (T, k), torch.int32, "pos")
+    _of(weights, (T, k), torch.float32, "weights")
+    if dO is None:
+        dO = torch.empty((rows, D), dtype=O.dtype, device=O.device)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=O.device)
+    if tuple(dO.shape) != (rows, D) or dO.dtype != O.dtype:
+        raise ValueError("dO must be [rows, D] with O's dtype")
+    _of(dweights, (T, k), torch.float32, "dweights")
+    _check(lib().moe_combine_bwd(_dt(O), _p(dY), _ld(dY, "dY"), _p(O), _ld(O, "O"), rows, _p(src), _p(pos),
+                                 _p(weights), T, k, D, _p(dO), _ld(dO, "dO"), _p(dweights), _stream()),
+           "moe_combine_bwd")
+    return dO, dweights

@@ -5,6 +5,7 @@
 // which the vector unit scales and adds to the accumulator.  B takes the instruction's row operand
 // and A its column operand, so a lane holds four consecutive columns n of one row m of C.
 #include "common.hpp"
+#include "dma.hpp"
 #include "launch.hpp"
 
 namespace nms {
@@ -29,57 +30,80 @@ struct Tile {
 
 __device__ inline int clamp_off(int v, int64_t rows) { return v < 0 ? 0 : (v > rows ? (int)rows : v); }
 
-// Row tile t of the groups' rows, BM rows at a time per group, then of the rows behind the last
-// group (and before the first).  Every wave finds it by itself: 64 groups at a time, an inclusive
-// sum of their tile counts over the lanes, and the first lane whose sum exceeds t.
-template <int BM>
-__device__ inline bool find_rows(const Fp8Gemm& g, int64_t t, Tile& out) {
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  int end = 0, first = 0;   // rows covered so far
-  for (int e0 = 0; e0 < g.E; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < g.E) {
-      lo = clamp_off(g.offsets[e], g.M);
-      hi = clamp_off(g.offsets[e + 1], g.M);
-      hi = hi < lo ? lo : hi;
-    }
-    if (e0 == 0) first = __shfl(lo, 0);
-    int sum = (hi - lo + BM - 1) / BM;
+// The row tiles of a grouped product: every group's rows BM at a time, in order, then the rows before
+// the first group and those behind the last (which are cleared).  Every wave counts them by itself, 64
+// groups at a time: a sum of the tile counts over the lanes.
+struct RowTiles {
+  int64_t grouped;    // tiles of the groups
+  int64_t total;
+  int first, end;     // rows [0, first) and [end, M) belong to no group
+};
+__device__ inline void group_rows(const Fp8Gemm& g, int e, int& lo, int& hi) {
+  lo = hi = 0;
+  if (e < g.E) {
+    lo = clamp_off(g.offsets[e], g.M);
+    hi = clamp_off(g.offsets[e + 1], g.M);
+    hi = hi < lo ? lo : hi;
+  }
+}
+__device__ inline int wave_scan(int v, int lane) {   // sum of the lanes up to and including this one
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(sum, d);
-      if (lane >= d) sum += o;
-    }
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+template <int BM>
+__device__ inline RowTiles count_rows(const Fp8Gemm& g) {
+  const int lane = threadIdx.x & 63;
+  RowTiles r;
+  int sum = 0;
+  for (int e = lane; e < g.E; e += 64) {
+    int lo, hi;
+    group_rows(g, e, lo, hi);
+    sum += (hi - lo + BM - 1) / BM;
+  }
+  r.grouped = __builtin_amdgcn_readlane(wave_scan(sum, lane), 63);
+  r.first = clamp_off(g.offsets[0], g.M);
+  const int last = clamp_off(g.offsets[g.E], g.M);
+  r.end = last < r.first ? r.first : last;
+  r.total = r.grouped + (r.first + BM - 1) / BM + (g.M - r.end + BM - 1) / BM;
+  return r;
+}
+// Row tile t < r.total.
+template <int BM>
+__device__ inline void find_rows(const Fp8Gemm& g, const RowTiles& r, int64_t t, Tile& out) {
+  const int lane = threadIdx.x & 63;
+  if (t >= r.grouped) {
+    t -= r.grouped;
+    const int64_t head = (r.first + BM - 1) / BM;
+    const bool front = t < head;
+    const int64_t stop = front ? r.first : g.M;
+    out.e = 0;
+    out.zero = true;
+    out.m0 = front ? t * BM : r.end + (t - head) * BM;
+    out.m_end = out.m0 + BM < stop ? out.m0 + BM : stop;
+    return;
+  }
+  int64_t before = 0;
+  out.zero = false;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int lo, hi;
+    group_rows(g, e0 + lane, lo, hi);
+    const int sum = wave_scan((hi - lo + BM - 1) / BM, lane);
     const uint64_t past = __ballot(before + sum > t);
     if (past) {
-      const int w = __builtin_ctzll(past);
-      const int64_t prev = before + (w ? __shfl(sum, w - 1) : 0);
-      const int glo = __shfl(lo, w), ghi = __shfl(hi, w);
+      const int w = __builtin_ctzll(past);   // the first lane whose sum exceeds t
+      const int64_t prev = before + (w ? __builtin_amdgcn_readlane(sum, w - 1) : 0);
+      const int glo = __builtin_amdgcn_readlane(lo, w), ghi = __builtin_amdgcn_readlane(hi, w);
       out.e = e0 + w;
       out.m0 = glo + (t - prev) * BM;
       out.m_end = out.m0 + BM < ghi ? out.m0 + BM : ghi;
-      out.zero = false;
-      return true;
+      return;
     }
-    before += __shfl(sum, 63);
-    const int last = __shfl(hi, g.E - 1 - e0 < 63 ? g.E - 1 - e0 : 63);
-    end = last;
+    before += __builtin_amdgcn_readlane(sum, 63);
   }
-  // the rows of no group: [0, first) and [end, M)
-  t -= before;
-  const int64_t head = (first + BM - 1) / BM;
-  out.e = 0;
-  out.zero = true;
-  if (t < head) {
-    out.m0 = t * BM;
-    out.m_end = out.m0 + BM < first ? out.m0 + BM : first;
-    return true;
-  }
-  out.m0 = end + (t - head) * BM;
-  out.m_end = out.m0 + BM < g.M ? out.m0 + BM : g.M;
-  return out.m0 < g.M;
 }
 
 __device__ inline void store4(const Fp8Gemm& g, int64_t crow, int64_t n, const float (&v)[4]) {
@@ -112,7 +136,9 @@ __global__ __launch_bounds__(256) void fp8_gemm_general_kernel(Fp8Gemm g, bool v
   t.zero = false;
   t.e = 0;
   if (g.mode == G_ROWS) {
-    if (!find_rows<64>(g, blockIdx.x, t)) return;
+    const RowTiles r = count_rows<64>(g);
+    if (blockIdx.x >= r.total) return;
+    find_rows<64>(g, r, blockIdx.x, t);
   } else {
     t.m0 = (int64_t)blockIdx.x * 64;
     t.m_end = t.m0 + 64 < g.M ? t.m0 + 64 : g.M;
@@ -202,9 +228,245 @@ hipError_t run_general(const Fp8Gemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Tiled kernel: BM x BN tiles of C, 128-k stages of both operands in two LDS buffers filled by
+// direct-to-LDS loads, which for stage kt + 1 are in flight while stage kt is computed.
+//
+// An LDS row is 128 bytes of one row, its 16-byte chunk c at slot c ^ (row & 7): eight rows' reads of
+// the same chunk cover all banks.  A wave computes TM rows of A by TN rows of B as fragments of 16 x 16:
+// it keeps the TM / 16 fragments of A for the stage and walks over B's, so that per B fragment TM / 16
+// matrix instructions run while the vector unit scales the previous fragment's results.  Two waves per
+// SIMD (their accumulators stay in vector registers: the scaling cannot read accumulation registers).
+// The scales of a stage are a row of floats behind the operands, loaded the same way.
+// ---------------------------------------------------------------------------
+template <int BM_, int BN_, int WM_, int WN_>
+struct TileCfg {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WM_, WAVES_N = WN_, WAVES = WM_ * WN_, NT = 64 * WAVES;
+  static constexpr int TM = BM / WAVES_M, TN = BN / WAVES_N, FM = TM / 16, FN = TN / 16;
+  static constexpr int OPER = (BM + BN) * 128, STAGE = OPER + (BM + BN) * 4, LDS = 2 * STAGE;
+  static constexpr int LOADS = OPER / 1024 / WAVES;   // 16-byte loads a lane and stage
+  static_assert((BM + BN) / 64 == WAVES, "one load of 64 scales a wave");
+};
+
+template <int FA, int FB, bool ROWB, typename Cfg>
+__global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
+  constexpr int BM = Cfg::BM, BN = Cfg::BN, FM = Cfg::FM, FN = Cfg::FN;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int ntn = (int)((g.N + BN - 1) / BN);
+
+  Tile t;
+  t.e = 0;
+  t.zero = false;
+  t.kb0 = 0;
+  t.kb1 = (g.K + 127) / 128;
+  if (g.mode == G_ROWS) {
+    // XCD x takes a run of the row tiles that there are, all column tiles of one after the other
+    const RowTiles r = count_rows<BM>(g);
+    const int x = blockIdx.x % 8, local = blockIdx.x / 8;
+    const int64_t per = (r.total + 7) / 8, rt = x * per + local / ntn;
+    if (local / ntn >= per || rt >= r.total) return;
+    find_rows<BM>(g, r, rt, t);
+    t.n0 = (int64_t)(local % ntn) * BN;
+    if (t.zero) t.kb1 = 0;
+  } else {
+    const int ntm = (int)((g.M + BM - 1) / BM);
+    int tm, tn;
+    if (g.mode == G_RED) {
+      const int wg = xcd_remap(blockIdx.x, gridDim.x);
+      t.e = wg / (ntm * ntn);
+      const int within = wg % (ntm * ntn);
+      tm = within % ntm;
+      tn = within / ntm;
+      t.kb0 = clamp_off(g.offsets[t.e], g.K) / 128;
+      t.kb1 = clamp_off(g.offsets[t.e + 1], g.K) / 128;
+    } else {
+      panel_major_tile(blockIdx.x, ntm, ntn, 4, tm, tn);
+    }
+    t.m0 = (int64_t)tm * BM;
+    t.m_end = t.m0 + BM < g.M ? t.m0 + BM : g.M;
+    t.n0 = (int64_t)tn * BN;
+  }
+  // the same in every lane, in scalar registers (rows and columns are below 2^31)
+  t.m0 = (int)uniform((uint32_t)t.m0);
+  t.m_end = (int)uniform((uint32_t)t.m_end);
+  t.n0 = (int)uniform((uint32_t)t.n0);
+  t.e = (int)uniform((uint32_t)t.e);
+  t.kb0 = (int)uniform((uint32_t)t.kb0);
+  t.kb1 = (int)uniform((uint32_t)t.kb1);
+  const uint8_t* B = g.B;
+  const float* sb = g.sb;
+  if (g.mode == G_ROWS) {
+    B += (int64_t)t.e * g.N * g.ldb;
+    sb += (int64_t)t.e * ((g.N + 127) / 128) * g.ldsb;
+  }
+  const int wm = (wave / Cfg::WAVES_N) * Cfg::TM, wn = (wave % Cfg::WAVES_N) * Cfg::TN;
+  const int KT = (int)(t.kb1 - t.kb0);
+
+  // Load q of a wave: LDS rows 8 (LOADS wave + q) .. +7 of A's and then B's rows; lane -> row lane / 8
+  // of them, slot lane % 8, so source chunk (lane % 8) ^ (lane / 8).  Byte offsets from the tile's first
+  // row (rows past the last are read as the last).
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t off[Cfg::LOADS];
+#pragma unroll
+  for (int q = 0; q < Cfg::LOADS; ++q) {
+    const int r = 8 * (Cfg::LOADS * wave + q) + (lane >> 3);
+    const bool a = r < BM;
+    const int64_t last = a ? g.M - 1 - t.m0 : g.N - 1 - t.n0;
+    const int64_t row = a ? r : r - BM;
+    off[q] = (uint32_t)((row < last ? row : last) * (a ? g.lda : g.ldb) + chunk);
+  }
+  // the 64 scales of this wave's part of a stage
+  const float* sc;
+  int64_t sc_step;
+  {
+    const int r = 64 * wave + lane;
+    if (r < BM) {
+      const int64_t m = t.m0 + r < g.M ? t.m0 + r : g.M - 1;
+      sc = g.sa + t.kb0 * g.ldsa + m;
+      sc_step = g.ldsa;
+    } else {
+      const int64_t n = t.n0 + r - BM < g.N ? t.n0 + r - BM : g.N - 1;
+      sc = ROWB ? sb + t.kb0 * g.ldsb + n : sb + n / 128 * g.ldsb + t.kb0;
+      sc_step = ROWB ? g.ldsb : 1;
+    }
+  }
+  const uint8_t* baseA = g.A + t.m0 * g.lda + t.kb0 * 128;
+  const uint8_t* baseB = B + t.n0 * g.ldb + t.kb0 * 128;
+  const uint32_t lds0 = lds_addr(smem);
+  // past the last whole chunk of K the source is that chunk: those bytes are cleared below
+  const int rem = (int)(g.K - (t.kb1 - 1) * 128);
+  const uint32_t back = chunk >= rem ? chunk - (rem - 1) / 16 * 16 : 0;
+  auto issue = [&](int kt) {
+    const uint32_t dst = lds0 + (kt & 1) * Cfg::STAGE;
+    const uint32_t cut = kt == KT - 1 ? back : 0;
+#pragma unroll
+    for (int q = 0; q < Cfg::LOADS; ++q) {
+      const int blk = Cfg::LOADS * wave + q;
+      dma16s(off[q] - cut, (8 * blk < BM ? baseA : baseB) + (int64_t)kt * 128, uniform(dst + blk * 1024));
+    }
+    dma4(sc + kt * sc_step, uniform(dst + Cfg::OPER + wave * 256));
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // a lane's 32 bytes of a fragment row: chunks 2 lq and 2 lq + 1
+  const int sl0 = ((2 * lq) ^ (l16 & 7)) * 16, sl1 = ((2 * lq + 1) ^ (l16 & 7)) * 16;
+  const int a_row = (wm + l16) * 128, b_row = (BM + wn + l16) * 128;
+  auto frag = [&](const unsigned char* st, int row) {
+    i32x8 v;
+    u32x4* h = reinterpret_cast<u32x4*>(&v);
+    h[0] = *reinterpret_cast<const u32x4*>(st + row + sl0);
+    h[1] = *reinterpret_cast<const u32x4*>(st + row + sl1);
+    return v;
+  };
+  auto compute = [&](int kt) {
+    const unsigned char* st = smem + (kt & 1) * Cfg::STAGE;
+    const float* scales = reinterpret_cast<const float*>(st + Cfg::OPER);
+    i32x8 a[FM];
+    float s[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a[i] = frag(st, a_row + i * 2048);
+    const float sbw = scales[BM + wn];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) s[i] = scales[wm + 16 * i + l16] * (ROWB ? 1.f : sbw);
+    f32x4 p[2][FM];
+    i32x8 b = frag(st, b_row);
+#pragma unroll
+    for (int j = 0; j <= FN; ++j) {
+      if (j < FN) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) p[j & 1][i] = mfma128<FB, FA>(b, a[i]);
+        if (j + 1 < FN) b = frag(st, b_row + (j + 1) * 2048);
+      }
+      if (j > 0) {
+        f32x4 sn;
+        if (ROWB) sn = *reinterpret_cast<const f32x4*>(scales + BM + wn + 16 * (j - 1) + 4 * lq);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float v = ROWB ? p[(j - 1) & 1][i][q] * sn[q] : p[(j - 1) & 1][i][q];
+            acc[i][j - 1][q] = __builtin_fmaf(v, s[i], acc[i][j - 1][q]);
+          }
+      }
+    }
+  };
+
+  if (KT > 0) issue(0);
+  for (int kt = 0; kt < KT; ++kt) {
+    wait_vmcnt<0>();   // this wave's loads of stage kt have landed
+    lds_barrier();     // ... every wave's, and every wave has read stage kt - 1 (the other buffer)
+    if (kt + 1 < KT) {
+      issue(kt + 1);
+    } else if (rem < 128) {
+      // K ends inside the block: clear the bytes behind it in every row of both operands
+      for (int r = tid; r < BM + BN; r += Cfg::NT) {
+        unsigned char* row = smem + (kt & 1) * Cfg::STAGE + r * 128;
+        for (int c = rem / 16; c < 8; ++c) {
+          u32x4* p = reinterpret_cast<u32x4*>(row + ((c ^ (r & 7)) * 16));
+          u32x4 v = *p;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int keep = rem - 16 * c - 4 * w;   // bytes of this word before K
+            v[w] = keep >= 4 ? v[w] : keep <= 0 ? 0u : v[w] & ((1u << (8 * keep)) - 1);
+          }
+          *p = v;
+        }
+      }
+      lds_barrier();
+    }
+    compute(kt);
+  }
+
+  const int64_t crow0 = g.mode == G_RED ? (int64_t)t.e * g.M : 0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = t.m0 + wm + i * 16 + l16;
+    if (m >= t.m_end) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      store4(g, crow0 + m, t.n0 + wn + j * 16 + lq * 4, v);
+    }
+  }
+}
+
+template <int FA, int FB, bool ROWB, typename Cfg>
+hipError_t run_tile(const Fp8Gemm& g, hipStream_t s) {
+  auto kern = fp8_gemm_tile_kernel<FA, FB, ROWB, Cfg>;
+  (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS);
+  const int64_t ntn = (g.N + Cfg::BN - 1) / Cfg::BN, ntm = (g.M + Cfg::BM - 1) / Cfg::BM;
+  int64_t wgs = ntm * ntn;
+  if (g.mode == G_ROWS) wgs = (g.M / Cfg::BM + g.E + 2 + 7) / 8 * 8 * ntn;   // at most so many row tiles
+  if (g.mode == G_RED) wgs *= g.E;
+  if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(Cfg::NT), Cfg::LDS, s, g);
+  return hipGetLastError();
+}
+
+// The tiled kernel's conditions: 16-byte loads of both operands, 32-bit offsets inside a tile.
+bool tile_ok(const Fp8Gemm& g) {
+  return (uintptr_t)g.A % 16 == 0 && (uintptr_t)g.B % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 &&
+         g.lda < (1 << 23) && g.ldb < (1 << 23);
+}
+
+using Tile256 = TileCfg<256, 256, 4, 2>;
+using Tile128 = TileCfg<128, 128, 2, 2>;
+
 template <int FA, int FB>
 hipError_t run(const Fp8Gemm& g, hipStream_t s) {
-  return run_general<FA, FB>(g, s);
+  if (force_generic() || !tile_ok(g)) return run_general<FA, FB>(g, s);
+  const int64_t tiles = (g.M + 255) / 256 * ((g.N + 255) / 256) * (g.mode == G_RED ? g.E : 1);
+  if (g.b_block == 1)
+    return tiles >= 192 ? run_tile<FA, FB, true, Tile256>(g, s) : run_tile<FA, FB, true, Tile128>(g, s);
+  return tiles >= 192 ? run_tile<FA, FB, false, Tile256>(g, s) : run_tile<FA, FB, false, Tile128>(g, s);
 }
 
 }  // namespace

@@ -106,18 +106,25 @@ __device__ inline void find_rows(const Fp8Gemm& g, const RowTiles& r, int64_t t,
   }
 }
 
-__device__ inline void store4(const Fp8Gemm& g, int64_t crow, int64_t n, const float (&v)[4]) {
-  if (g.bf16_out) {
-    uint16_t* p = (uint16_t*)g.C + crow * g.ldc + n;
+// Four consecutive elements of row crow of C from column n: one store when the row allows it (vec),
+// else one at a time.
+template <typename T>
+__device__ inline void store4(T* p, int64_t n, int64_t N, bool vec, const f32x4& v) {
+  T b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < g.N) p[i] = f32_to_bf16_rne(v[i]);
+  for (int i = 0; i < 4; ++i) store_out(b + i, v[i]);
+  if (vec && n + 4 <= N) {
+    __builtin_memcpy(__builtin_assume_aligned(p + n, 4 * sizeof(T)), b, sizeof(b));
   } else {
-    float* p = (float*)g.C + crow * g.ldc + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < g.N) p[i] = v[i];
+      if (n + i < N) p[n + i] = b[i];
   }
+}
+__device__ inline void store4(const Fp8Gemm& g, int64_t crow, int64_t n, const f32x4& v) {
+  const bool vec = g.ldc % 4 == 0 && (uintptr_t)g.C % (g.bf16_out ? 8 : 16) == 0;
+  if (g.bf16_out) store4((uint16_t*)g.C + crow * g.ldc, n, g.N, vec, v);
+  else store4((float*)g.C + crow * g.ldc, n, g.N, vec, v);
 }
 
 // General kernel: any sizes, strides and alignments.  64 x 64 tile, four waves of 32 x 32; each
@@ -158,7 +165,7 @@ __global__ __launch_bounds__(256) void fp8_gemm_general_kernel(Fp8Gemm g, bool v
   if (t.zero) t.kb1 = t.kb0;
 
   const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  float acc[2][2][4] = {};   // [m fragment][n fragment][n]
+  f32x4 acc[2][2] = {};   // [m fragment][n fragment], four n a lane
   auto stage = [&](unsigned char* dst, const uint8_t* X, int64_t ld, int64_t r0, int64_t r_end, int64_t k0, bool vec) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -232,8 +239,8 @@ hipError_t run_general(const Fp8Gemm& g, hipStream_t s) {
 // Tiled kernel: BM x BN tiles of C, 128-k stages of both operands in two LDS buffers filled by
 // direct-to-LDS loads, which for stage kt + 1 are in flight while stage kt is computed.
 //
-// An LDS row is 128 bytes of one row, its 16-byte chunk c at slot c ^ (row & 7): eight rows' reads of
-// the same chunk cover all banks.  A wave computes TM rows of A by TN rows of B as fragments of 16 x 16:
+// An LDS row is 128 bytes of one row, its 16-byte chunk c at slot c ^ (row / 2 % 8): sixteen rows' reads
+// of the same chunk cover all 64 banks once.  A wave computes TM rows of A by TN rows of B as fragments of 16 x 16:
 // it keeps the TM / 16 fragments of A for the stage and walks over B's, so that per B fragment TM / 16
 // matrix instructions run while the vector unit scales the previous fragment's results.  Two waves per
 // SIMD (their accumulators stay in vector registers: the scaling cannot read accumulation registers).
@@ -306,9 +313,10 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   const int KT = (int)(t.kb1 - t.kb0);
 
   // Load q of a wave: LDS rows 8 (LOADS wave + q) .. +7 of A's and then B's rows; lane -> row lane / 8
-  // of them, slot lane % 8, so source chunk (lane % 8) ^ (lane / 8).  Byte offsets from the tile's first
-  // row (rows past the last are read as the last).
-  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  // of them, slot lane % 8.  LOADS is even, so the slot's source chunk depends on the parity of q.  Byte
+  // offsets from the tile's first row (rows past the last are read as the last).
+  static_assert(Cfg::LOADS % 2 == 0, "");
+  const int chunk0 = ((lane & 7) ^ (lane >> 4)) * 16;   // of even loads; of odd ones chunk0 ^ 64
   uint32_t off[Cfg::LOADS];
 #pragma unroll
   for (int q = 0; q < Cfg::LOADS; ++q) {
@@ -316,7 +324,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
     const bool a = r < BM;
     const int64_t last = a ? g.M - 1 - t.m0 : g.N - 1 - t.n0;
     const int64_t row = a ? r : r - BM;
-    off[q] = (uint32_t)((row < last ? row : last) * (a ? g.lda : g.ldb) + chunk);
+    off[q] = (uint32_t)((row < last ? row : last) * (a ? g.lda : g.ldb) + (chunk0 ^ (q & 1 ? 64 : 0)));
   }
   // the 64 scales of this wave's part of a stage
   const float* sc;
@@ -338,14 +346,16 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   const uint32_t lds0 = lds_addr(smem);
   // past the last whole chunk of K the source is that chunk: those bytes are cleared below
   const int rem = (int)(g.K - (t.kb1 - 1) * 128);
-  const uint32_t back = chunk >= rem ? chunk - (rem - 1) / 16 * 16 : 0;
+  const int last_chunk = rem < 128 ? (rem - 1) / 16 * 16 : 112;
+  const uint32_t back0 = chunk0 > last_chunk ? chunk0 - last_chunk : 0;
+  const uint32_t back1 = (chunk0 ^ 64) > last_chunk ? (chunk0 ^ 64) - last_chunk : 0;
   auto issue = [&](int kt) {
     const uint32_t dst = lds0 + (kt & 1) * Cfg::STAGE;
-    const uint32_t cut = kt == KT - 1 ? back : 0;
+    const bool at_end = kt == KT - 1;
 #pragma unroll
     for (int q = 0; q < Cfg::LOADS; ++q) {
       const int blk = Cfg::LOADS * wave + q;
-      dma16s(off[q] - cut, (8 * blk < BM ? baseA : baseB) + (int64_t)kt * 128, uniform(dst + blk * 1024));
+      dma16s(off[q] - (at_end ? (q & 1 ? back1 : back0) : 0u), (8 * blk < BM ? baseA : baseB) + (int64_t)kt * 128, uniform(dst + blk * 1024));
     }
     dma4(sc + kt * sc_step, uniform(dst + Cfg::OPER + wave * 256));
   };
@@ -357,7 +367,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // a lane's 32 bytes of a fragment row: chunks 2 lq and 2 lq + 1
-  const int sl0 = ((2 * lq) ^ (l16 & 7)) * 16, sl1 = ((2 * lq + 1) ^ (l16 & 7)) * 16;
+  const int sl0 = ((2 * lq) ^ (l16 >> 1)) * 16, sl1 = ((2 * lq + 1) ^ (l16 >> 1)) * 16;
   const int a_row = (wm + l16) * 128, b_row = (BM + wn + l16) * 128;
   auto frag = [&](const unsigned char* st, int row) {
     i32x8 v;
@@ -369,32 +379,33 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   auto compute = [&](int kt) {
     const unsigned char* st = smem + (kt & 1) * Cfg::STAGE;
     const float* scales = reinterpret_cast<const float*>(st + Cfg::OPER);
-    i32x8 a[FM];
+    i32x8 a[FM], b[2];
     float s[FM];
+    f32x4 p[2][FM], sn;
+    b[0] = frag(st, b_row);
 #pragma unroll
     for (int i = 0; i < FM; ++i) a[i] = frag(st, a_row + i * 2048);
     const float sbw = scales[BM + wn];
 #pragma unroll
     for (int i = 0; i < FM; ++i) s[i] = scales[wm + 16 * i + l16] * (ROWB ? 1.f : sbw);
-    f32x4 p[2][FM];
-    i32x8 b = frag(st, b_row);
+    // fragment j's matrix instructions, and between them the scaling of fragment j - 1's results: a
+    // result is read FM matrix instructions after its own was issued
 #pragma unroll
     for (int j = 0; j <= FN; ++j) {
-      if (j < FN) {
+      if (j + 1 < FN) b[(j + 1) & 1] = frag(st, b_row + (j + 1) * 2048);
+      if (ROWB && j > 0) sn = *reinterpret_cast<const f32x4*>(scales + BM + wn + 16 * (j - 1) + 4 * lq);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) p[j & 1][i] = mfma128<FB, FA>(b, a[i]);
-        if (j + 1 < FN) b = frag(st, b_row + (j + 1) * 2048);
-      }
-      if (j > 0) {
-        f32x4 sn;
-        if (ROWB) sn = *reinterpret_cast<const f32x4*>(scales + BM + wn + 16 * (j - 1) + 4 * lq);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i) {
+        if (j < FN) p[j & 1][i] = mfma128<FB, FA>(b[j & 1], a[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j > 0) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float v = ROWB ? p[(j - 1) & 1][i][q] * sn[q] : p[(j - 1) & 1][i][q];
             acc[i][j - 1][q] = __builtin_fmaf(v, s[i], acc[i][j - 1][q]);
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -410,7 +421,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
       for (int r = tid; r < BM + BN; r += Cfg::NT) {
         unsigned char* row = smem + (kt & 1) * Cfg::STAGE + r * 128;
         for (int c = rem / 16; c < 8; ++c) {
-          u32x4* p = reinterpret_cast<u32x4*>(row + ((c ^ (r & 7)) * 16));
+          u32x4* p = reinterpret_cast<u32x4*>(row + ((c ^ (r >> 1 & 7)) * 16));
           u32x4 v = *p;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -432,8 +443,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
     if (m >= t.m_end) continue;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      store4(g, crow0 + m, t.n0 + wn + j * 16 + lq * 4, v);
+      store4(g, crow0 + m, t.n0 + wn + j * 16 + lq * 4, acc[i][j]);
     }
   }
 }

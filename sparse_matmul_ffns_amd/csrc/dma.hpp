@@ -43,6 +43,24 @@ __device__ __forceinline__ void dma16s(uint32_t voff, const void* sbase, uint32_
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory");
 }
+// Through a buffer descriptor: 16 bytes per lane from base + voff; a lane whose voff does not lie below
+// the descriptor's size reads nothing and writes zeros.
+__device__ __forceinline__ void dma16b(uint32_t voff, u32x4 desc, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(desc), "s"(lds) : "memory");
+}
+// Descriptor of `bytes` bytes from p (p wave-uniform): untyped, no stride, no swizzle.
+__device__ __forceinline__ u32x4 buffer_desc(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  u32x4 d;
+  d[0] = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
+  d[2] = __builtin_amdgcn_readfirstlane(bytes);
+  d[3] = 0x00020000u;
+  return d;
+}
+__device__ __forceinline__ void dma4s(uint32_t voff, const void* sbase, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");

@@ -12,6 +12,7 @@ namespace nms {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 // D[i][j] = sum_k X[i][k] Y[j][k] over 128 k; fx, fy: 0 e4m3, 1 e5m2.
 template <int FX, int FY>
@@ -111,8 +112,12 @@ __device__ inline void find_rows(const Fp8Gemm& g, const RowTiles& r, int64_t t,
 template <typename T>
 __device__ inline void store4(T* p, int64_t n, int64_t N, bool vec, const f32x4& v) {
   T b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) store_out(b + i, v[i]);
+  if constexpr (sizeof(T) == 2) {
+    const bf16x4 h = __builtin_convertvector(v, bf16x4);   // nearest even
+    __builtin_memcpy(b, &h, sizeof(b));
+  } else {
+    __builtin_memcpy(b, &v, sizeof(b));
+  }
   if (vec && n + 4 <= N) {
     __builtin_memcpy(__builtin_assume_aligned(p + n, 4 * sizeof(T)), b, sizeof(b));
   } else {
@@ -246,8 +251,9 @@ hipError_t run_general(const Fp8Gemm& g, hipStream_t s) {
 // SIMD (their accumulators stay in vector registers: the scaling cannot read accumulation registers).
 // The scales of a stage are a row of floats behind the operands, loaded the same way.
 // ---------------------------------------------------------------------------
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int D_>
 struct TileCfg {
+  static constexpr int D = D_;   // how many slots ahead B's fragments are read
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WM_, WAVES_N = WN_, WAVES = WM_ * WN_, NT = 64 * WAVES;
   static constexpr int TM = BM / WAVES_M, TN = BN / WAVES_N, FM = TM / 16, FN = TN / 16;
   static constexpr int OPER = (BM + BN) * 128, STAGE = OPER + (BM + BN) * 4, LDS = 2 * STAGE;
@@ -312,111 +318,56 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   const int wm = (wave / Cfg::WAVES_N) * Cfg::TM, wn = (wave % Cfg::WAVES_N) * Cfg::TN;
   const int KT = (int)(t.kb1 - t.kb0);
 
-  // Load q of a wave: LDS rows 8 (LOADS wave + q) .. +7 of A's and then B's rows; lane -> row lane / 8
-  // of them, slot lane % 8.  LOADS is even, so the slot's source chunk depends on the parity of q.  Byte
-  // offsets from the tile's first row (rows past the last are read as the last).
-  static_assert(Cfg::LOADS % 2 == 0, "");
-  const int chunk0 = ((lane & 7) ^ (lane >> 4)) * 16;   // of even loads; of odd ones chunk0 ^ 64
-  uint32_t off[Cfg::LOADS];
-#pragma unroll
-  for (int q = 0; q < Cfg::LOADS; ++q) {
-    const int r = 8 * (Cfg::LOADS * wave + q) + (lane >> 3);
-    const bool a = r < BM;
-    const int64_t last = a ? g.M - 1 - t.m0 : g.N - 1 - t.n0;
-    const int64_t row = a ? r : r - BM;
-    off[q] = (uint32_t)((row < last ? row : last) * (a ? g.lda : g.ldb) + (chunk0 ^ (q & 1 ? 64 : 0)));
-  }
-  // the 64 scales of this wave's part of a stage
+  // A wave fills 8 LOADS consecutive LDS rows, all of A's or all of B's: load q rows 8 q .. 8 q + 7 of
+  // them, lane -> row lane / 8, slot lane % 8 (LOADS is even, so the slot's source chunk depends on the
+  // parity of q).  The descriptor ends behind the wave's last row: lanes beyond it get zeros.
+  constexpr int ROWS = 8 * Cfg::LOADS;
+  static_assert(Cfg::LOADS % 2 == 0 && BM % ROWS == 0 && BN % ROWS == 0, "a wave's rows are of one operand");
+  const bool of_a = wave < BM / ROWS;
+  const int64_t ldx = of_a ? g.lda : g.ldb;
+  const int64_t row0 = of_a ? t.m0 + wave * ROWS : t.n0 + wave * ROWS - BM;
+  const int64_t left = (of_a ? g.M : g.N) - row0;
+  const int rows = left < 0 ? 0 : left < ROWS ? (int)left : ROWS;
+  const int rem = (int)(g.K - (t.kb1 - 1) * 128 < 128 ? g.K - (t.kb1 - 1) * 128 : 128);   // of the last block
+  const uint32_t span = uniform(rows > 0 && KT > 0 ? (uint32_t)((rows - 1) * ldx + (KT - 1) * 128 + (rem + 15) / 16 * 16) : 0u);
+  const u32x4 desc = buffer_desc((of_a ? g.A : B) + row0 * ldx + t.kb0 * 128, span);
+  const uint32_t voff0 = (uint32_t)((lane >> 3) * ldx) + ((lane & 7) ^ (lane >> 4)) * 16;
+  const uint32_t voff1 = (uint32_t)((lane >> 3) * ldx) + ((lane & 7) ^ (lane >> 4) ^ 4) * 16;
+  // and the 64 scales of 64 of the tile's rows (clamped to the last)
   const float* sc;
   int64_t sc_step;
-  {
-    const int r = 64 * wave + lane;
-    if (r < BM) {
-      const int64_t m = t.m0 + r < g.M ? t.m0 + r : g.M - 1;
-      sc = g.sa + t.kb0 * g.ldsa + m;
-      sc_step = g.ldsa;
-    } else {
-      const int64_t n = t.n0 + r - BM < g.N ? t.n0 + r - BM : g.N - 1;
-      sc = ROWB ? sb + t.kb0 * g.ldsb + n : sb + n / 128 * g.ldsb + t.kb0;
-      sc_step = ROWB ? g.ldsb : 1;
-    }
+  uint32_t sc_off;
+  if (wave < BM / 64) {
+    const int64_t m = t.m0 + wave * 64 + lane;
+    sc = g.sa + t.kb0 * g.ldsa + t.m0;
+    sc_off = (uint32_t)((m < g.M ? m : g.M - 1) - t.m0) * 4;
+    sc_step = g.ldsa;
+  } else {
+    int64_t n = t.n0 + wave * 64 - BM + lane;
+    n = n < g.N ? n : g.N - 1;
+    sc = ROWB ? sb + t.kb0 * g.ldsb + t.n0 : sb + t.n0 / 128 * g.ldsb + t.kb0;
+    sc_off = (uint32_t)(ROWB ? n - t.n0 : (n / 128 - t.n0 / 128) * g.ldsb) * 4;
+    sc_step = ROWB ? g.ldsb : 1;
   }
-  const uint8_t* baseA = g.A + t.m0 * g.lda + t.kb0 * 128;
-  const uint8_t* baseB = B + t.n0 * g.ldb + t.kb0 * 128;
   const uint32_t lds0 = lds_addr(smem);
-  // past the last whole chunk of K the source is that chunk: those bytes are cleared below
-  const int rem = (int)(g.K - (t.kb1 - 1) * 128);
-  const int last_chunk = rem < 128 ? (rem - 1) / 16 * 16 : 112;
-  const uint32_t back0 = chunk0 > last_chunk ? chunk0 - last_chunk : 0;
-  const uint32_t back1 = (chunk0 ^ 64) > last_chunk ? (chunk0 ^ 64) - last_chunk : 0;
-  auto issue = [&](int kt) {
+  // load q < LOADS of stage kt, or (q == LOADS) its scales; past the last stage nothing is read: the
+  // descriptor is empty (the scales are the last stage's again)
+  auto dma = [&](int kt, int q) {
     const uint32_t dst = lds0 + (kt & 1) * Cfg::STAGE;
-    const bool at_end = kt == KT - 1;
-#pragma unroll
-    for (int q = 0; q < Cfg::LOADS; ++q) {
-      const int blk = Cfg::LOADS * wave + q;
-      dma16s(off[q] - (at_end ? (q & 1 ? back1 : back0) : 0u), (8 * blk < BM ? baseA : baseB) + (int64_t)kt * 128, uniform(dst + blk * 1024));
-    }
-    dma4(sc + kt * sc_step, uniform(dst + Cfg::OPER + wave * 256));
-  };
-
-  f32x4 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // a lane's 32 bytes of a fragment row: chunks 2 lq and 2 lq + 1
-  const int sl0 = ((2 * lq) ^ (l16 >> 1)) * 16, sl1 = ((2 * lq + 1) ^ (l16 >> 1)) * 16;
-  const int a_row = (wm + l16) * 128, b_row = (BM + wn + l16) * 128;
-  auto frag = [&](const unsigned char* st, int row) {
-    i32x8 v;
-    u32x4* h = reinterpret_cast<u32x4*>(&v);
-    h[0] = *reinterpret_cast<const u32x4*>(st + row + sl0);
-    h[1] = *reinterpret_cast<const u32x4*>(st + row + sl1);
-    return v;
-  };
-  auto compute = [&](int kt) {
-    const unsigned char* st = smem + (kt & 1) * Cfg::STAGE;
-    const float* scales = reinterpret_cast<const float*>(st + Cfg::OPER);
-    i32x8 a[FM], b[2];
-    float s[FM];
-    f32x4 p[2][FM], sn;
-    b[0] = frag(st, b_row);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) a[i] = frag(st, a_row + i * 2048);
-    const float sbw = scales[BM + wn];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) s[i] = scales[wm + 16 * i + l16] * (ROWB ? 1.f : sbw);
-    // fragment j's matrix instructions, and between them the scaling of fragment j - 1's results: a
-    // result is read FM matrix instructions after its own was issued
-#pragma unroll
-    for (int j = 0; j <= FN; ++j) {
-      if (j + 1 < FN) b[(j + 1) & 1] = frag(st, b_row + (j + 1) * 2048);
-      if (ROWB && j > 0) sn = *reinterpret_cast<const f32x4*>(scales + BM + wn + 16 * (j - 1) + 4 * lq);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if (j < FN) p[j & 1][i] = mfma128<FB, FA>(b[j & 1], a[i]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (j > 0) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float v = ROWB ? p[(j - 1) & 1][i][q] * sn[q] : p[(j - 1) & 1][i][q];
-            acc[i][j - 1][q] = __builtin_fmaf(v, s[i], acc[i][j - 1][q]);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    if (q == Cfg::LOADS) {
+      dma4s(sc_off, sc + (kt < KT ? kt : KT - 1) * sc_step, uniform(dst + Cfg::OPER + wave * 256));
+    } else {
+      u32x4 d = desc;
+      d[2] = kt < KT ? span : 0u;
+      dma16b((q & 1 ? voff1 : voff0) + uniform((uint32_t)(q * 8 * ldx) + kt * 128), d,
+             uniform(dst + (Cfg::LOADS * wave + q) * 1024));
     }
   };
-
-  if (KT > 0) issue(0);
-  for (int kt = 0; kt < KT; ++kt) {
-    wait_vmcnt<0>();   // this wave's loads of stage kt have landed
-    lds_barrier();     // ... every wave's, and every wave has read stage kt - 1 (the other buffer)
-    if (kt + 1 < KT) {
-      issue(kt + 1);
-    } else if (rem < 128) {
+  // this wave's loads of stage kt have landed and its reads of the stage before are done; then every wave's
+  auto land = [&](int kt) {
+    wait_vmcnt<0>();
+    lds_barrier();
+    if (kt == KT - 1 && rem < 128) {
       // K ends inside the block: clear the bytes behind it in every row of both operands
       for (int r = tid; r < BM + BN; r += Cfg::NT) {
         unsigned char* row = smem + (kt & 1) * Cfg::STAGE + r * 128;
@@ -433,7 +384,102 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
       }
       lds_barrier();
     }
-    compute(kt);
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // a lane's 32 bytes of a fragment row: chunks 2 lq and 2 lq + 1
+  const int sl0 = ((2 * lq) ^ (l16 >> 1)) * 16, sl1 = ((2 * lq + 1) ^ (l16 >> 1)) * 16;
+  const int a_row = (wm + l16) * 128, b_row = (BM + wn + l16) * 128;
+  auto frag = [&](int kt, int row) {
+    const unsigned char* st = smem + (kt & 1) * Cfg::STAGE + row;
+    i32x8 v;
+    u32x4* h = reinterpret_cast<u32x4*>(&v);
+    h[0] = *reinterpret_cast<const u32x4*>(st + sl0);
+    h[1] = *reinterpret_cast<const u32x4*>(st + sl1);
+    return v;
+  };
+  auto scales = [&](int kt) { return reinterpret_cast<const float*>(smem + (kt & 1) * Cfg::STAGE + Cfg::OPER); };
+
+  constexpr int D = Cfg::D;
+  i32x8 a[FM], b[D + 1];
+  f32x4 p[2][FM], sn = {0.f, 0.f, 0.f, 0.f};
+  float s[FM], sprev[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    p[1][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s[i] = 0.f;
+  }
+  auto load_scales = [&](int kt) {
+    const float sbw = scales(kt)[BM + wn];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) s[i] = scales(kt)[wm + 16 * i + l16] * (ROWB ? 1.f : sbw);
+  };
+  auto scale = [&](int i, int j, const float (&sc_)[FM]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float v = ROWB ? p[j & 1][i][q] * sn[q] : p[j & 1][i][q];
+      acc[i][j][q] = __builtin_fmaf(v, sc_[i], acc[i][j][q]);
+    }
+    asm volatile("" : "+v"(acc[i][j]));   // here, not sunk to the end of the loop
+  };
+  // Stage kt.  Slot j: fragment j's FM matrix instructions, and between them the scaling of the slot
+  // before (a result is read FM matrix instructions after its own was issued; slot 0 finishes the stage
+  // before).  B's fragments are read two slots ahead, so slot FN - 2 holds none of this stage's reads:
+  // there the waves meet, and the two last slots read the next stage's first fragments and issue the
+  // loads of the stage after it into the buffer just left.
+  auto stage = [&](int kt) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sprev[i] = s[i];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      if (j == FN - D) land(kt + 1);
+      if (j + D < FN) b[(j + D) % (D + 1)] = frag(kt, b_row + (j + D) * 2048);
+      else b[(j + D) % (D + 1)] = frag(kt + 1, b_row + (j + D - FN) * 2048);
+      if (j == 0) load_scales(kt);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        p[j & 1][i] = mfma128<FB, FA>(b[j % (D + 1)], a[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j == 0) scale(i, FN - 1, sprev); else scale(i, j - 1, s);
+        if (j == FN - 1) a[i] = frag(kt + 1, a_row + i * 2048);
+        if (j >= FN - D) {
+          constexpr int PER = Cfg::LOADS / (D * FM);
+#pragma unroll
+          for (int u = 0; u < PER; ++u) dma(kt + 2, ((j - (FN - D)) * FM + i) * PER + u);
+        }
+      }
+      if (ROWB) sn = *reinterpret_cast<const f32x4*>(scales(kt) + BM + wn + 16 * j + 4 * lq);
+    }
+    dma(kt + 2, Cfg::LOADS);
+    if constexpr (FN % (D + 1) != 0) {
+      i32x8 r[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) r[d] = b[(FN + d) % (D + 1)];
+#pragma unroll
+      for (int d = 0; d < D; ++d) b[d] = r[d];
+    }
+  };
+  static_assert(Cfg::LOADS % (D * FM) == 0, "the last slots issue all loads");
+  if (KT > 0) {
+#pragma unroll
+    for (int q = 0; q <= Cfg::LOADS; ++q) dma(0, q);
+    land(0);
+#pragma unroll
+    for (int q = 0; q <= Cfg::LOADS; ++q) dma(1, q);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a[i] = frag(0, a_row + i * 2048);
+#pragma unroll
+    for (int d = 0; d < D; ++d) b[d] = frag(0, b_row + d * 2048);
+    for (int kt = 0; kt < KT; ++kt) stage(kt);
+    wait_vmcnt<0>();   // no load may land in LDS after the workgroup ends
+#pragma unroll
+    for (int i = 0; i < FM; ++i) scale(i, FN - 1, s);
   }
 
   const int64_t crow0 = g.mode == G_RED ? (int64_t)t.e * g.M : 0;
@@ -464,11 +510,11 @@ hipError_t run_tile(const Fp8Gemm& g, hipStream_t s) {
 // The tiled kernel's conditions: 16-byte loads of both operands, 32-bit offsets inside a tile.
 bool tile_ok(const Fp8Gemm& g) {
   return (uintptr_t)g.A % 16 == 0 && (uintptr_t)g.B % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 &&
-         g.lda < (1 << 23) && g.ldb < (1 << 23);
+         g.lda < (1 << 23) && g.ldb < (1 << 23) && g.ldsb < (1 << 28);
 }
 
-using Tile256 = TileCfg<256, 256, 4, 2>;
-using Tile128 = TileCfg<128, 128, 2, 2>;
+using Tile256 = TileCfg<256, 256, 4, 2, 1>;
+using Tile128 = TileCfg<128, 128, 2, 2, 2>;
 
 template <int FA, int FB>
 hipError_t run(const Fp8Gemm& g, hipStream_t s) {

@@ -132,6 +132,81 @@ __device__ inline void store4(const Fp8Gemm& g, int64_t crow, int64_t n, const f
   else store4((float*)g.C + crow * g.ldc, n, g.N, vec, v);
 }
 
+// A wave's FM x FN fragments to rows 0 .. rows - 1 and columns n .. of C.  A fragment's row is 16
+// columns in four lanes (64 bytes of fp32).  Stored as they lie, a wave's store touches 16 half lines;
+// two exchanges make it eight whole 128-byte lines, which (stored non-temporally: half lines and ordinary
+// stores gain nothing alone) took the experts' fp32 weight gradients from 255 to 173 us:
+//   - bf16: the 16-lane rows of two neighbouring fragments are swapped so that a lane holds eight
+//     consecutive columns (16 bytes) of one of them;
+//   - lanes 0-7 and 8-15 of each 16 trade, so that one store holds rows 0-7 of two such 64-byte runs
+//     and the next rows 8-15.
+template <int FM, int FN, typename T>
+__device__ inline void store_tile(const f32x4 (&acc)[FM][FN], T* C, int64_t ldc, int rows, int64_t n, int64_t N, int lane) {
+  constexpr bool BF = sizeof(T) == 2;
+  constexpr int STEP = BF ? 4 : 2;   // fragments in a 128-byte run
+  static_assert(FN % STEP == 0, "");
+  const int l16 = lane & 15, lq = lane >> 4;
+  if ((uintptr_t)C % 16 == 0 && (ldc * (int64_t)sizeof(T)) % 16 == 0) {
+    const bool low = l16 < 8;
+    constexpr int PER = 16 / (int)sizeof(T);   // elements a store
+    // this lane's place in a run: its half, and its 16 bytes of that half
+    const int64_t col = n + (low ? 0 : 64 / (int)sizeof(T)) + (BF ? (lq & 1) * 2 + (lq >> 1) : lq) * PER;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int j = 0; j < FN; j += STEP) {
+        u32x4 u, v;
+        if constexpr (BF) {
+          auto pair = [&](const f32x4& x, const f32x4& y) {
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4));   // nearest even
+            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
+            const auto r0 = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+            const auto r1 = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+            return u32x4{r0[0], r1[0], r0[1], r1[1]};
+          };
+          u = pair(acc[i][j], acc[i][j + 1]);
+          v = pair(acc[i][j + STEP - 2], acc[i][j + STEP - 1]);
+        } else {
+          u = __builtin_bit_cast(u32x4, acc[i][j]);
+          v = __builtin_bit_cast(u32x4, acc[i][j + 1]);
+        }
+        u32x4 first, second;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t t = low ? v[q] : u[q];
+          const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)t, (int)t, 0x128, 0xF, 0xF, false);   // lane ^ 8
+          first[q] = low ? u[q] : o;
+          second[q] = low ? o : v[q];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * i + 8 * h + (l16 & 7);
+          const int64_t c = col + 16 * j;
+          if (r >= rows) continue;
+          const u32x4 w = h ? second : first;
+          T* p = C + r * ldc + c;
+          if (c + PER <= N) {
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
+          } else {
+            T e[PER];
+            __builtin_memcpy(e, &w, 16);
+#pragma unroll
+            for (int q = 0; q < PER; ++q)
+              if (c + q < N) p[q] = e[q];
+          }
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if (16 * i + l16 >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) store4(C + (16 * i + l16) * ldc, n + 16 * j + 4 * lq, N, false, acc[i][j]);
+  }
+}
+
 // General kernel: any sizes, strides and alignments.  64 x 64 tile, four waves of 32 x 32; each
 // 128-block of both operands goes through LDS byte by byte where the rows are not 16-byte aligned,
 // with zeros beyond the rows and beyond K.
@@ -326,7 +401,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   const bool of_a = wave < BM / ROWS;
   const int64_t ldx = of_a ? g.lda : g.ldb;
   const int64_t row0 = of_a ? t.m0 + wave * ROWS : t.n0 + wave * ROWS - BM;
-  const int64_t left = (of_a ? g.M : g.N) - row0;
+  const int64_t left = (of_a ? t.m_end : g.N) - row0;
   const int rows = left < 0 ? 0 : left < ROWS ? (int)left : ROWS;
   const int rem = (int)(g.K - (t.kb1 - 1) * 128 < 128 ? g.K - (t.kb1 - 1) * 128 : 128);   // of the last block
   const uint32_t span = uniform(rows > 0 && KT > 0 ? (uint32_t)((rows - 1) * ldx + (KT - 1) * 128 + (rem + 15) / 16 * 16) : 0u);
@@ -482,16 +557,11 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
     for (int i = 0; i < FM; ++i) scale(i, FN - 1, s);
   }
 
-  const int64_t crow0 = g.mode == G_RED ? (int64_t)t.e * g.M : 0;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = t.m0 + wm + i * 16 + l16;
-    if (m >= t.m_end) continue;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      store4(g, crow0 + m, t.n0 + wn + j * 16 + lq * 4, acc[i][j]);
-    }
-  }
+  const int64_t crow = (g.mode == G_RED ? (int64_t)t.e * g.M : 0) + t.m0 + wm;
+  const int rows_left = (int)(t.m_end - t.m0) - wm;
+  const int64_t n = t.n0 + wn;
+  if (g.bf16_out) store_tile<FM, FN>(acc, (uint16_t*)g.C + crow * g.ldc, g.ldc, rows_left, n, g.N, lane);
+  else store_tile<FM, FN>(acc, (float*)g.C + crow * g.ldc, g.ldc, rows_left, n, g.N, lane);
 }
 
 template <int FA, int FB, bool ROWB, typename Cfg>

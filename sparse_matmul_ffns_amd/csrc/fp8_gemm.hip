@@ -305,11 +305,18 @@ __global__ __launch_bounds__(256) void fp8_gemm_general_kernel(Fp8Gemm g, bool v
   }
 }
 
+// The most row tiles that M rows in E groups can make: a partial one per group and at both ends, and
+// never more than one per row.
+int64_t most_row_tiles(const Fp8Gemm& g, int bm) {
+  const int64_t n = g.M / bm + g.E + 2;
+  return n < g.M ? n : g.M;
+}
+
 template <int FA, int FB>
 hipError_t run_general(const Fp8Gemm& g, hipStream_t s) {
   const bool va = (uintptr_t)g.A % 16 == 0 && g.lda % 16 == 0, vb = (uintptr_t)g.B % 16 == 0 && g.ldb % 16 == 0;
   const int64_t ntn = (g.N + 63) / 64;
-  const int64_t ntm = g.mode == G_ROWS ? g.M / 64 + g.E + 2 : (g.M + 63) / 64;
+  const int64_t ntm = g.mode == G_ROWS ? most_row_tiles(g, 64) : (g.M + 63) / 64;
   hipLaunchKernelGGL((fp8_gemm_general_kernel<FA, FB>), dim3((unsigned)ntm, (unsigned)ntn, g.mode == G_RED ? g.E : 1),
                      dim3(256), 0, s, g, va, vb);
   return hipGetLastError();
@@ -570,10 +577,182 @@ hipError_t run_tile(const Fp8Gemm& g, hipStream_t s) {
   (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS);
   const int64_t ntn = (g.N + Cfg::BN - 1) / Cfg::BN, ntm = (g.M + Cfg::BM - 1) / Cfg::BM;
   int64_t wgs = ntm * ntn;
-  if (g.mode == G_ROWS) wgs = (g.M / Cfg::BM + g.E + 2 + 7) / 8 * 8 * ntn;   // at most so many row tiles
+  if (g.mode == G_ROWS) wgs = (most_row_tiles(g, Cfg::BM) + 7) / 8 * 8 * ntn;
   if (g.mode == G_RED) wgs *= g.E;
   if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(Cfg::NT), Cfg::LDS, s, g);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per group (or few rows at all): B is read once and that bounds the call, so its bytes go
+// straight from memory to the registers of the matrix instruction, with no LDS and no barrier on the
+// way.  A workgroup computes 16 FM rows of A by 32 rows of B; its KS waves take every KS-th chunk of
+// two 128-blocks, each with the next chunk's loads in flight, and add their sums through LDS in the
+// order of the waves.  The lanes of a row that does not exist load nothing.
+// ---------------------------------------------------------------------------
+template <int FA, int FB, bool ROWB, int FM, int KS>
+__global__ __launch_bounds__(64 * KS) void fp8_gemm_rows_kernel(Fp8Gemm g) {
+  constexpr int BM = 16 * FM, BN = 32, FN = 2, CH = 2;   // CH: 128-blocks a chunk
+  __shared__ f32x4 part[KS][FM * FN][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int ntn = (int)((g.N + BN - 1) / BN);
+  Tile t;
+  t.e = 0;
+  t.zero = false;
+  t.kb0 = 0;
+  t.kb1 = (g.K + 127) / 128;
+  const int64_t rt = blockIdx.x / ntn;
+  t.n0 = (int64_t)(blockIdx.x % ntn) * BN;
+  if (g.mode == G_ROWS) {
+    const RowTiles r = count_rows<BM>(g);
+    if (rt >= r.total) return;
+    find_rows<BM>(g, r, rt, t);
+    if (t.zero) t.kb1 = 0;
+  } else {
+    t.m0 = rt * BM;
+    t.m_end = t.m0 + BM < g.M ? t.m0 + BM : g.M;
+  }
+  t.m0 = (int)uniform((uint32_t)t.m0);
+  t.m_end = (int)uniform((uint32_t)t.m_end);
+  t.e = (int)uniform((uint32_t)t.e);
+  t.kb1 = (int)uniform((uint32_t)t.kb1);
+  const uint8_t* B = g.B;
+  const float* sb = g.sb;
+  if (g.mode == G_ROWS) {
+    B += (int64_t)t.e * g.N * g.ldb;
+    sb += (int64_t)t.e * ((g.N + 127) / 128) * g.ldsb;
+  }
+  const int kbs = (int)t.kb1, nchunks = (kbs + CH - 1) / CH;
+
+  // a lane's 32 bytes of a block: 16 at 16 lq and 16 at 64 + 16 lq (the same for both operands, so the
+  // order inside a block does not matter), which makes 64 contiguous bytes of each row per load
+  const uint8_t* arow[FM];
+  bool aon[FM], bon[FN];
+  const uint8_t* brow[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = t.m0 + 16 * i + l16;
+    aon[i] = m < t.m_end;
+    arow[i] = g.A + (aon[i] ? m : t.m0) * g.lda;
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int64_t n = t.n0 + 16 * j + l16;
+    bon[j] = n < g.N;
+    brow[j] = B + (bon[j] ? n : t.n0) * g.ldb;
+  }
+  auto load16 = [&](const uint8_t* row, bool on, int64_t k) {
+    u32x4 v = {0, 0, 0, 0};
+    if (on && k < g.K) v = *reinterpret_cast<const u32x4*>(row + k);
+    return v;
+  };
+  auto trim = [&](u32x4 v, int64_t k) {   // clear the bytes from K on
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int64_t keep = g.K - k - 4 * w;
+      v[w] = keep >= 4 ? v[w] : keep <= 0 ? 0u : v[w] & ((1u << (8 * keep)) - 1);
+    }
+    return v;
+  };
+  struct Chunk {
+    u32x4 a[CH][FM][2], b[CH][FN][2];
+    float sa[CH][FM], sb[CH][ROWB ? 4 * FN : 1];
+  };
+  auto load = [&](int c, Chunk& x) {
+#pragma unroll
+    for (int u = 0; u < CH; ++u) {
+      const int kb = c * CH + u;
+      const int64_t k = (int64_t)kb * 128 + 16 * lq;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        x.b[u][j][0] = load16(brow[j], bon[j], k);
+        x.b[u][j][1] = load16(brow[j], bon[j], k + 64);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        x.a[u][i][0] = load16(arow[i], aon[i], k);
+        x.a[u][i][1] = load16(arow[i], aon[i], k + 64);
+        x.sa[u][i] = aon[i] && kb < kbs ? g.sa[kb * g.ldsa + t.m0 + 16 * i + l16] : 0.f;
+      }
+      if constexpr (ROWB) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int64_t n = t.n0 + 16 * j + 4 * lq + q;
+            x.sb[u][4 * j + q] = n < g.N && kb < kbs ? sb[kb * g.ldsb + n] : 0.f;
+          }
+      } else {
+        x.sb[u][0] = kb < kbs ? sb[t.n0 / 128 * g.ldsb + kb] : 0.f;   // a tile's 32 rows lie in one block
+      }
+    }
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](int c, Chunk& x) {
+#pragma unroll
+    for (int u = 0; u < CH; ++u) {
+      const int64_t k = (int64_t)(c * CH + u) * 128 + 16 * lq;
+      if ((int64_t)(c * CH + u + 1) * 128 > g.K) {   // K ends in this block
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) x.b[u][j][h] = trim(x.b[u][j][h], k + 64 * h);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) x.a[u][i][h] = trim(x.a[u][i][h], k + 64 * h);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const i32x8 fb = __builtin_bit_cast(i32x8, x.b[u][j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const f32x4 p = mfma128<FB, FA>(fb, __builtin_bit_cast(i32x8, x.a[u][i]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[i][j][q] += p[q] * (x.sa[u][i] * (ROWB ? x.sb[u][4 * j + q] : x.sb[u][0]));
+        }
+      }
+    }
+  };
+  Chunk x, y;
+  int c = wave;
+  if (c < nchunks) load(c, x);
+  while (c < nchunks) {
+    if (c + KS < nchunks) load(c + KS, y);
+    compute(c, x);
+    c += KS;
+    if (c >= nchunks) break;
+    if (c + KS < nchunks) load(c + KS, x);
+    compute(c, y);
+    c += KS;
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) part[wave][i * FN + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int f = wave; f < FM * FN; f += KS) {
+    f32x4 sum = part[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < KS; ++w) sum += part[w][f][lane];
+    const int64_t m = t.m0 + 16 * (f / FN) + l16;
+    if (m < t.m_end) store4(g, m, t.n0 + 16 * (f % FN) + 4 * lq, sum);
+  }
+}
+
+template <int FA, int FB, bool ROWB, int FM, int KS>
+hipError_t run_rows(const Fp8Gemm& g, hipStream_t s) {
+  const int64_t ntn = (g.N + 31) / 32;
+  const int64_t ntm = g.mode == G_ROWS ? most_row_tiles(g, 16 * FM) : (g.M + 16 * FM - 1) / (16 * FM);
+  if (ntm * ntn > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((fp8_gemm_rows_kernel<FA, FB, ROWB, FM, KS>), dim3((unsigned)(ntm * ntn)), dim3(64 * KS), 0, s, g);
   return hipGetLastError();
 }
 
@@ -589,10 +768,22 @@ using Tile128 = TileCfg<128, 128, 2, 2, 2>;
 template <int FA, int FB>
 hipError_t run(const Fp8Gemm& g, hipStream_t s) {
   if (force_generic() || !tile_ok(g)) return run_general<FA, FB>(g, s);
-  const int64_t tiles = (g.M + 255) / 256 * ((g.N + 255) / 256) * (g.mode == G_RED ? g.E : 1);
-  if (g.b_block == 1)
-    return tiles >= 192 ? run_tile<FA, FB, true, Tile256>(g, s) : run_tile<FA, FB, true, Tile128>(g, s);
-  return tiles >= 192 ? run_tile<FA, FB, false, Tile256>(g, s) : run_tile<FA, FB, false, Tile128>(g, s);
+  auto tiles = [&](int64_t b) { return (g.M + b - 1) / b * ((g.N + b - 1) / b) * (g.mode == G_RED ? g.E : 1); };
+  // Few rows a group, and at most one 128 x 128 tile a CU: the kernel without LDS.  It and the tiled
+  // kernel, in us: 1 x 8192 x 2048 5.3 and 12; 64 x 8192 x 2048 11.0 and 12.5; 128 x 8192 x 2048 18.6 and
+  // 12.7; 1 x 16384 x 4096 14 and 24; experts of 1024 x 2048, 8 rows of 8 of them 6.2 and 13, 128 rows of 64
+  // of them 23.5 and 21.6.
+  const int64_t groups = g.mode == G_ROWS ? (g.E < g.M ? g.E : g.M) : 1, per_group = (g.M + groups - 1) / groups;
+  if (g.mode != G_RED && per_group <= 64 && groups * ((g.N + 127) / 128) <= 256) {
+    const bool two = per_group > 16;
+    if (g.b_block == 1)
+      return two ? run_rows<FA, FB, true, 2, 4>(g, s) : run_rows<FA, FB, true, 1, 4>(g, s);
+    return two ? run_rows<FA, FB, false, 2, 4>(g, s) : run_rows<FA, FB, false, 1, 4>(g, s);
+  }
+  // Time of a round of 256 large tiles : of 512 small ones (two a CU) = 5 : 3 (65 and 39 us at K 4096).
+  const bool large = (tiles(256) + 255) / 256 * 5 <= (tiles(128) + 511) / 512 * 3;
+  if (g.b_block == 1) return large ? run_tile<FA, FB, true, Tile256>(g, s) : run_tile<FA, FB, true, Tile128>(g, s);
+  return large ? run_tile<FA, FB, false, Tile256>(g, s) : run_tile<FA, FB, false, Tile128>(g, s);
 }
 
 }  // namespace

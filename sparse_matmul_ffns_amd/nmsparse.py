@@ -10,6 +10,7 @@ fallback -- a missing library or a CPU tensor is an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -161,7 +162,9 @@ def _flat(t: torch.Tensor, name: str) -> None:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """torch's current HIP stream on the current device, as its handle: what
+    torch.cuda.current_stream().cuda_stream gives (4 us) without building a Stream object (0.3 us)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _p(t):
@@ -674,7 +677,7 @@ def _of(t: torch.Tensor, shape, dtype, name: str) -> None:
     """A contiguous tensor of the given shape and dtype."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
 
 
@@ -691,9 +694,12 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, g
         _of(bias, (E,), torch.float32, "bias")
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    else:
+        _of(ids, (T, k), torch.int32, "ids")
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _of(ids, (T, k), torch.int32, "ids"), _of(weights, (T, k), torch.float32, "weights")
+    else:
+        _of(weights, (T, k), torch.float32, "weights")
     _check(lib().moe_route(_dt(logits), _p(logits), ldl, T, E, _score(score), _p(bias), groups, topk_groups, group_top,
                            k, int(bool(renorm)), scale, _p(ids), _p(weights), _stream()), "moe_route")
     return ids, weights
@@ -725,6 +731,13 @@ def moe_plan_rows(n: int, E: int, align: int = 1) -> int:
     return _up(n + min(n, E) * (align - 1), align)
 
 
+@functools.lru_cache(maxsize=256)
+def _plan_work_bytes(T: int, k: int, E: int) -> int:
+    need = _i64()
+    _check(lib().moe_plan_work_bytes(T, k, E, ctypes.byref(need)), "moe_plan_work_bytes")
+    return need.value
+
+
 def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=None, src=None, pos=None, work="auto"):
     """The order of the T * k slots by expert: returns (offsets [E + 1], counts [E], src [rows], pos
     [T, k]), int32.  `work`: an int32 device tensor, or "auto" (allocated with torch when the call uses
@@ -737,20 +750,25 @@ def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=Non
     dev = ids.device
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    else:
+        _of(offsets, (E + 1,), torch.int32, "offsets")
     if counts is None:
         counts = torch.empty(E, dtype=torch.int32, device=dev)
+    else:
+        _of(counts, (E,), torch.int32, "counts")
     if src is None:
         src = torch.empty(moe_plan_rows(T * k, E, align), dtype=torch.int32, device=dev)
+    else:
+        _of(src, (src.numel(),), torch.int32, "src")
     if pos is None:
         pos = torch.empty((T, k), dtype=torch.int32, device=dev)
-    _of(offsets, (E + 1,), torch.int32, "offsets"), _of(counts, (E,), torch.int32, "counts")
-    _of(src, (src.numel(),), torch.int32, "src"), _of(pos, (T, k), torch.int32, "pos")
+    else:
+        _of(pos, (T, k), torch.int32, "pos")
     if isinstance(work, str):
         if work != "auto":
             raise ValueError("work must be a tensor, None or 'auto'")
-        need = _i64()
-        _check(lib().moe_plan_work_bytes(T, k, E, ctypes.byref(need)), "moe_plan_work_bytes")
-        work = torch.empty(need.value // 4, dtype=torch.int32, device=dev) if need.value else None
+        need = _plan_work_bytes(T, k, E)
+        work = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
     if work is not None:
         _dev(work)
         _flat(work, "work")
@@ -948,9 +966,10 @@ def moe_combine_bwd(dY: torch.Tensor, O: torch.Tensor, src: torch.Tensor, pos: t
         dO = torch.empty((rows, D), dtype=O.dtype, device=O.device)
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=O.device)
+    else:
+        _of(dweights, (T, k), torch.float32, "dweights")
     if tuple(dO.shape) != (rows, D) or dO.dtype != O.dtype:
         raise ValueError("dO must be [rows, D] with O's dtype")
-    _of(dweights, (T, k), torch.float32, "dweights")
     _check(lib().moe_combine_bwd(_dt(O), _p(dY), _ld(dY, "dY"), _p(O), _ld(O, "O"), rows, _p(src), _p(pos),
                                  _p(weights), T, k, D, _p(dO), _ld(dO, "dO"), _p(dweights), _stream()),
            "moe_combine_bwd")

@@ -424,7 +424,7 @@ nm_status fp8_quantize(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, cons
   const nm_status st = quantize_check(dt, X, ldx, RX, src, div, gate, ldg, R, K, fmt, Q, S);
   if (st != NM_OK) return st;
   if (ldq < up128(K) || lds < R) return NM_ERR_SHAPE;
-  const nms::QuantArgs a{X, ldx, RX, src, div, gate, ldg, R, K, fmt == NM_E5M2, Q, ldq, S, lds};
+  const nms::QuantArgs a{X, ldx, RX, src, nms::fast_div(src ? div : 1), gate, ldg, R, K, fmt == NM_E5M2, Q, ldq, S, lds};
   return hip_status(nms::launch_fp8_quantize(dt, a, hs(stream)));
 }
 
@@ -434,7 +434,7 @@ nm_status fp8_quantize_t(nm_dtype dt, const void* X, int64_t ldx, int64_t RX, co
   const nm_status st = quantize_check(dt, X, ldx, RX, src, div, gate, ldg, R, K, fmt, Qt, St);
   if (st != NM_OK) return st;
   if (ldqt < up128(R) || ldst < K) return NM_ERR_SHAPE;
-  const nms::QuantArgs a{X, ldx, RX, src, div, gate, ldg, R, K, fmt == NM_E5M2, Qt, ldqt, St, ldst};
+  const nms::QuantArgs a{X, ldx, RX, src, nms::fast_div(src ? div : 1), gate, ldg, R, K, fmt == NM_E5M2, Qt, ldqt, St, ldst};
   return hip_status(nms::launch_fp8_quantize_t(dt, a, hs(stream)));
 }
 

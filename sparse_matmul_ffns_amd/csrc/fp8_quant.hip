@@ -5,80 +5,100 @@
 namespace nms {
 namespace {
 
-// Eight consecutive elements of a row from column c, 0 beyond K.
-template <typename T>
-__device__ inline void load8(const T* p, int64_t c, int64_t K, bool vec, float (&x)[8]) {
-  T b[8];
-  if (vec && c + 8 <= K) {
-    __builtin_memcpy(b, __builtin_assume_aligned(p + c, 16), sizeof(b));
+// Eight consecutive elements of a row from column c, 0 beyond K: 16-byte loads (VEC: the columns exist
+// and the row is aligned) or one at a time.
+template <bool VEC, typename T>
+__device__ inline void load8(const T* p, int64_t c, int64_t K, Raw8<T>& x) {
+  if constexpr (VEC) {
+    __builtin_memcpy(x.w, __builtin_assume_aligned(p + c, 16), sizeof(x.w));
   } else {
+    T b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = c + i < K ? p[c + i] : (T)0;
+    __builtin_memcpy(x.w, b, sizeof(x.w));
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = Elem<T>::to_f32(b[i]);
 }
 
-// Eight elements of row r of the quantisers' input: gathered, and gated.
-template <typename T>
-__device__ inline void input8(const QuantArgs& a, int64_t r, int64_t c, bool vec, float (&x)[8]) {
+// Source row of row r of the quantisers' input, -1 for a row of zeros.
+__device__ inline int64_t source_row(const QuantArgs& a, int64_t r) {
+  if (!a.src) return r;
+  const int sl = a.src[r];
+  const uint32_t t = __umulhi(a.div.mul, (uint32_t)sl);
+  const int64_t row = (t + (((uint32_t)sl - t) >> a.div.s1)) >> a.div.s2;
+  return sl >= 0 && row < a.RX ? row : -1;
+}
+// Eight elements of N rows of the input from column c (rows[i] their sources, -1: zeros; r[i] their own
+// numbers, for the gate).  All loads are issued before any is used; a row of zeros reads row 0.
+template <bool VEC, typename T, int N>
+__device__ inline void input_rows(const QuantArgs& a, const int64_t (&rows)[N], const int64_t (&r)[N], int64_t c,
+                                  Raw8<T> (&x)[N]) {
   const T* X = (const T*)a.X;
-  int64_t row = r;
-  if (a.src) {
-    const int sl = a.src[r];
-    row = sl < 0 ? -1 : sl / a.div;
-    if (row >= a.RX) row = -1;
-  }
-  if (row < 0) {
+  const T* G = (const T*)a.gate;
+  const bool own = G && (const void*)G == a.X && !a.src && a.ldg == a.ldx;   // the gate is the row itself
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    return;
-  }
-  load8(X + row * a.ldx, c, a.K, vec, x);
-  if (a.gate) {
-    float g[8];
-    load8((const T*)a.gate + r * a.ldg, c, a.K, vec, g);
+  for (int i = 0; i < N; ++i) load8<VEC>(X + (rows[i] < 0 ? 0 : rows[i]) * a.ldx, c, a.K, x[i]);
+  if (G && !own) {
+    Raw8<T> g[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = g[i] > 0.f ? x[i] : 0.f;
+    for (int i = 0; i < N; ++i) load8<VEC>(G + r[i] * a.ldg, c, a.K, g[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i].gate(g[i]);
+  } else if (own) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i].gate(Raw8<T>(x[i]));
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (rows[i] < 0) x[i].zero();
 }
 
-__device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int CTRL>
+__device__ inline uint32_t dpp_max(uint32_t m) {
+  return umax2(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, CTRL, 0xF, 0xF, false));
+}
+// Maximum over 16 consecutive lanes, in each of them (rotations by 8, 4, 2, 1).
+__device__ inline uint32_t row16_max(uint32_t m) { return dpp_max<0x121>(dpp_max<0x122>(dpp_max<0x124>(dpp_max<0x128>(m)))); }
 
-// Rows: 16 lanes hold a block (8 elements a lane), a wave four consecutive blocks of one row, a
-// workgroup 32 rows x 4 blocks; the scales leave through LDS so that a block's 32 are written
-// together.  One pass over the data; bound by its bytes.
-template <typename T, bool E5M2>
+// Rows: 16 lanes hold a block (8 elements a lane), a wave four consecutive blocks of N rows, a
+// workgroup 4 N rows x 4 blocks; the scales leave through LDS so that a block's are written together.
+// One pass over the data; bound by its bytes.  N = 8 keeps eight rows' loads in flight (36864 gathered
+// rows of 2048: TODO us); N = 1 spreads few rows over more CUs (128 rows of 1024: TODO us).
+template <typename T, bool E5M2, int N>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a, bool vec) {
-  __shared__ float sc[4][32];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t r0 = (int64_t)blockIdx.x * 32;
+  __shared__ float sc[4][4 * N];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t r0 = (int64_t)blockIdx.x * (4 * N);
   const int64_t kb0 = (int64_t)blockIdx.y * 4, nkb = (a.K + 127) / 128;
   const int64_t kb = kb0 + (lane >> 4);
   const int64_t c = kb * 128 + (lane & 15) * 8;
-#pragma unroll 4
-  for (int i = 0; i < 8; ++i) {
-    const int rl = wave + 4 * i;
-    const int64_t r = r0 + rl;
-    const bool on = r < a.R && kb < nkb;
-    float x[8];
-    if (on) {
-      input8<T>(a, r, c, vec, x);
-    } else {
+  int64_t r[N], rows[N];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = 0.f;
+  for (int i = 0; i < N; ++i) {
+    r[i] = r0 + wave * N + i;
+    if (r[i] >= a.R) r[i] = a.R - 1;   // repeats that are not stored
+    rows[i] = source_row(a, r[i]);
+  }
+  Raw8<T> x[N];
+  if (vec && (kb0 + 4) * 128 <= a.K) input_rows<true, T, N>(a, rows, r, c, x);
+  else input_rows<false, T, N>(a, rows, r, c, x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int rl = wave * N + i;
+    uint32_t m = row16_max(x[i].row_max());
+    if (__any(m >= 0x7F800000u)) {
+      x[i].clean();
+      Raw8<T> f = x[i];
+#pragma unroll
+      for (int q = 0; q < Raw8<T>::NMAX; ++q) {
+        const auto v = f.mag_finite(q);
+        __builtin_memcpy(&f.w[q], &v, 4);
+      }
+      m = row16_max(f.row_max());
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) m = umax(m, finite_bits(x[q]));
-#pragma unroll
-    for (int d = 8; d > 0; d /= 2) m = umax(m, __shfl_xor(m, d));
-    const int e = block_exponent(m, E5M2);
-    const float inv = power2(-e);
-    const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
-    const u32x2 q = {pack4<E5M2>(lo, inv), pack4<E5M2>(hi, inv)};
-    if (on) {
-      uint8_t* dst = a.Q + r * a.ldq + c;
+    const float scale = power2(block_exponent(m, E5M2));
+    const u32x2 q = pack_row<E5M2>(x[i], scale);
+    if (r0 + rl < a.R && kb < nkb) {
+      uint8_t* dst = a.Q + (r0 + rl) * a.ldq + c;
       if (((uintptr_t)dst & 7) == 0) {
         *reinterpret_cast<u32x2*>(dst) = q;
       } else {
@@ -86,11 +106,11 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a, bool vec
         for (int b = 0; b < 8; ++b) dst[b] = (uint8_t)(q[b >> 2] >> (8 * (b & 3)));
       }
     }
-    if ((lane & 15) == 0) sc[lane >> 4][rl] = power2(e);
+    if ((lane & 15) == 0) sc[lane >> 4][rl] = scale;
   }
   __syncthreads();
-  if (threadIdx.x < 128) {
-    const int kq = threadIdx.x >> 5, rl = threadIdx.x & 31;
+  if (threadIdx.x < 16 * N) {
+    const int kq = threadIdx.x / (4 * N), rl = threadIdx.x % (4 * N);
     if (kb0 + kq < nkb && r0 + rl < a.R) a.S[(kb0 + kq) * a.lds + r0 + rl] = sc[kq][rl];
   }
 }
@@ -125,40 +145,63 @@ __device__ inline void store_transposed(TileT& t, uint8_t* Qt, int64_t ldqt, int
 template <typename T, bool E5M2>
 __global__ __launch_bounds__(256) void fp8_quantize_t_kernel(QuantArgs a, bool vec) {
   __shared__ __align__(16) TileT tile;
-  __shared__ uint32_t cmax[4][128];
+  __shared__ typename Raw8<T>::Max cmax[4][16][Raw8<T>::NMAX];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t r0 = (int64_t)blockIdx.x * 128, k0 = (int64_t)blockIdx.y * 128;
   const int cg = tid & 15, rg = tid >> 4;
   const int64_t c = k0 + cg * 8;
-  float x[8][8];   // [row][column]
-  uint32_t m[8] = {};
+  constexpr int NM = Raw8<T>::NMAX;
+  Raw8<T> x[8];
+  int64_t r[8], rows[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + rg * 8 + i;
-    if (r < a.R && c < a.K) {
-      input8<T>(a, r, c, vec, x[i]);
-    } else {
+    r[i] = r0 + rg * 8 + i;
+    const bool in = r[i] < a.R;
+    if (!in) r[i] = a.R - 1;
+    rows[i] = source_row(a, r[i]);
+    if (!in) rows[i] = -1;   // the padding columns of the result are 0
+  }
+  if (vec && k0 + 128 <= a.K) input_rows<true, T, 8>(a, rows, r, c, x);
+  else input_rows<false, T, 8>(a, rows, r, c, x);
+  typename Raw8<T>::Max m[NM];
+  // the columns' maxima: over the thread's rows, the wave's four row groups, the four waves
+  auto maxima = [&](auto mag) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[i][q] = 0.f;
+    for (int q = 0; q < NM; ++q) {
+      m[q] = mag(x[0], q);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m[q] = vmax(m[q], mag(x[i], q));
+#pragma unroll
+      for (int d = 16; d <= 32; d *= 2) {
+        uint32_t o;
+        __builtin_memcpy(&o, &m[q], 4);
+        o = __shfl_xor(o, d);
+        typename Raw8<T>::Max om;
+        __builtin_memcpy(&om, &o, 4);
+        m[q] = vmax(m[q], om);
+      }
+      if (lane < 16) cmax[wave][cg][q] = m[q];
     }
+    __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) m[q] = umax(m[q], finite_bits(x[i][q]));
-  }
+    for (int q = 0; q < NM; ++q) m[q] = vmax(vmax(cmax[0][cg][q], cmax[1][cg][q]), vmax(cmax[2][cg][q], cmax[3][cg][q]));
+  };
+  maxima([](const Raw8<T>& v, int q) { return v.mag(q); });
+  bool odd = false;   // a column with an infinity or NaN
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    m[q] = umax(m[q], __shfl_xor(m[q], 16));
-    m[q] = umax(m[q], __shfl_xor(m[q], 32));
-    if (lane < 16) cmax[wave][cg * 8 + q] = m[q];
+  for (int q = 0; q < 8; ++q) odd |= Raw8<T>::column(m, q) >= 0x7F800000u;
+  if (__syncthreads_or(odd)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i].clean();
+    maxima([](const Raw8<T>& v, int q) { return v.mag_finite(q); });
   }
-  __syncthreads();
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const int col = cg * 8 + q;
-    const int e = block_exponent(umax(umax(cmax[0][col], cmax[1][col]), umax(cmax[2][col], cmax[3][col])), E5M2);
-    const float inv = power2(-e);
-    const float lo[4] = {x[0][q], x[1][q], x[2][q], x[3][q]}, hi[4] = {x[4][q], x[5][q], x[6][q], x[7][q]};
-    *tile_slot(tile, col, rg) = (uint64_t)pack4<E5M2>(lo, inv) | ((uint64_t)pack4<E5M2>(hi, inv) << 32);
-    if (rg == 0 && k0 + col < a.K) a.S[(int64_t)blockIdx.x * a.lds + k0 + col] = power2(e);
+    const float scale = power2(block_exponent(Raw8<T>::column(m, q), E5M2));
+    const u32x2 b = pack_column<E5M2>(x, q, scale);
+    *tile_slot(tile, col, rg) = (uint64_t)b[0] | ((uint64_t)b[1] << 32);
+    if (rg == 0 && k0 + col < a.K) a.S[(int64_t)blockIdx.x * a.lds + k0 + col] = scale;
   }
   __syncthreads();
   store_transposed(tile, a.Q, a.ldq, k0, a.K, r0);
@@ -179,36 +222,52 @@ __global__ __launch_bounds__(256) void fp8_quantize_weight_kernel(const T* W, in
   const int cg = tid & 15, rg = tid >> 4;
   const int64_t c = k0 + cg * 8;
   W += ex * N * ldw;
-  float x[8][8];
+  Raw8<T> x[8];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = n0 + rg * 8 + i;
+    x[i].zero();
     if (r < N && c < K) {
-      load8(W + r * ldw, c, K, vec, x[i]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[i][q] = 0.f;
+      if (vec && c + 8 <= K) load8<true>(W + r * ldw, c, K, x[i]);
+      else load8<false>(W + r * ldw, c, K, x[i]);
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) m = umax(m, finite_bits(x[i][q]));
+    m = umax2(m, x[i].row_max());
   }
+  auto block_max = [&](uint32_t v) {
 #pragma unroll
-  for (int d = 32; d > 0; d /= 2) m = umax(m, __shfl_xor(m, d));
-  if (lane == 0) bmax[wave] = m;
-  __syncthreads();
-  const int e = block_exponent(umax(umax(bmax[0], bmax[1]), umax(bmax[2], bmax[3])), E5M2);
-  const float inv = power2(-e);
+    for (int d = 32; d > 0; d /= 2) v = umax2(v, __shfl_xor(v, d));
+    if (lane == 0) bmax[wave] = v;
+    __syncthreads();
+    return umax2(umax2(bmax[0], bmax[1]), umax2(bmax[2], bmax[3]));
+  };
+  m = block_max(m);
+  if (m >= 0x7F800000u) {   // the same for the whole workgroup
+    __syncthreads();        // bmax has been read
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i].clean();
+      Raw8<T> f = x[i];
+#pragma unroll
+      for (int q = 0; q < Raw8<T>::NMAX; ++q) {
+        const auto v = f.mag_finite(q);
+        __builtin_memcpy(&f.w[q], &v, 4);
+      }
+      m = umax2(m, f.row_max());
+    }
+    m = block_max(m);
+  }
+  const float scale = power2(block_exponent(m, E5M2));
   if (tid == 0) {
-    S[(ex * nb + ib) * kbn + jb] = power2(e);
-    if (St) St[(ex * kbn + jb) * nb + ib] = power2(e);
+    S[(ex * nb + ib) * kbn + jb] = scale;
+    if (St) St[(ex * kbn + jb) * nb + ib] = scale;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = n0 + rg * 8 + i;
     if (r >= N) continue;
-    const float lo[4] = {x[i][0], x[i][1], x[i][2], x[i][3]}, hi[4] = {x[i][4], x[i][5], x[i][6], x[i][7]};
-    const u32x2 q = {pack4<E5M2>(lo, inv), pack4<E5M2>(hi, inv)};
+    const u32x2 q = pack_row<E5M2>(x[i], scale);
     uint8_t* dst = Q + (ex * N + r) * ldq + c;
     if (((uintptr_t)dst & 7) == 0) {
       *reinterpret_cast<u32x2*>(dst) = q;
@@ -220,8 +279,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_weight_kernel(const T* W, in
   if (!Qt) return;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const float lo[4] = {x[0][q], x[1][q], x[2][q], x[3][q]}, hi[4] = {x[4][q], x[5][q], x[6][q], x[7][q]};
-    *tile_slot(tile, cg * 8 + q, rg) = (uint64_t)pack4<E5M2>(lo, inv) | ((uint64_t)pack4<E5M2>(hi, inv) << 32);
+    const u32x2 b = pack_column<E5M2>(x, q, scale);
+    *tile_slot(tile, cg * 8 + q, rg) = (uint64_t)b[0] | ((uint64_t)b[1] << 32);
   }
   __syncthreads();
   store_transposed(tile, Qt + ex * K * ldqt, ldqt, k0, K, n0);
@@ -233,19 +292,21 @@ bool vec_ok(int es, const void* X, int64_t ldx, const void* gate, int64_t ldg) {
 
 }  // namespace
 
-hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s) {
-  const int64_t nkb = (a.K + 127) / 128;
-  const dim3 grid((unsigned)((a.R + 31) / 32), (unsigned)((nkb + 3) / 4));
-  if (dt == DT_BF16) {
-    const bool vec = vec_ok(2, a.X, a.ldx, a.gate, a.ldg);
-    if (a.e5m2) hipLaunchKernelGGL((fp8_quantize_kernel<uint16_t, true>), grid, dim3(256), 0, s, a, vec);
-    else hipLaunchKernelGGL((fp8_quantize_kernel<uint16_t, false>), grid, dim3(256), 0, s, a, vec);
-  } else {
-    const bool vec = vec_ok(4, a.X, a.ldx, a.gate, a.ldg);
-    if (a.e5m2) hipLaunchKernelGGL((fp8_quantize_kernel<uint32_t, true>), grid, dim3(256), 0, s, a, vec);
-    else hipLaunchKernelGGL((fp8_quantize_kernel<uint32_t, false>), grid, dim3(256), 0, s, a, vec);
-  }
+template <typename T, bool E5M2>
+static hipError_t quantize_rows(const QuantArgs& a, hipStream_t s) {
+  const bool vec = vec_ok(sizeof(T), a.X, a.ldx, a.gate, a.ldg);
+  const unsigned gy = (unsigned)((a.K + 511) / 512);
+  // eight rows a wave once that fills the chip's 256 CUs twice
+  if ((a.R + 31) / 32 * gy >= 512)
+    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 8>), dim3((unsigned)((a.R + 31) / 32), gy), dim3(256), 0, s, a, vec);
+  else
+    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 1>), dim3((unsigned)((a.R + 3) / 4), gy), dim3(256), 0, s, a, vec);
   return hipGetLastError();
+}
+
+hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s) {
+  if (dt == DT_BF16) return a.e5m2 ? quantize_rows<uint16_t, true>(a, s) : quantize_rows<uint16_t, false>(a, s);
+  return a.e5m2 ? quantize_rows<uint32_t, true>(a, s) : quantize_rows<uint32_t, false>(a, s);
 }
 
 hipError_t launch_fp8_quantize_t(int dt, const QuantArgs& a, hipStream_t s) {

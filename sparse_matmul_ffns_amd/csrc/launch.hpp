@@ -138,11 +138,23 @@ hipError_t launch_moe_combine(int dt, const void* O, int64_t ldo, int64_t rows, 
 hipError_t launch_moe_combine_bwd(int dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int64_t rows,
                                   const int32_t* src, const int32_t* pos, const float* w, int64_t T, int k, int64_t D,
                                   void* dO, int64_t lddo, float* dw, hipStream_t s);
+// n / d for 0 <= n < 2^31 as a product and shifts (d fixed by the host): q = (t + ((n - t) >> s1)) >> s2
+// with t the high half of mul * n, mul = floor(2^32 (2^l - d) / d) + 1, l = ceil(log2 d).
+struct FastDiv {
+  uint32_t mul;
+  int s1, s2;
+};
+inline FastDiv fast_div(int d) {
+  int l = 0;
+  while ((int64_t(1) << l) < d) ++l;
+  const uint64_t mul = ((uint64_t)((int64_t(1) << l) - d) << 32) / (uint64_t)d + 1;
+  return FastDiv{(uint32_t)mul, l < 1 ? l : 1, l < 1 ? 0 : l - 1};
+}
 struct QuantArgs {
   const void* X;
   int64_t ldx, RX;
   const int32_t* src;
-  int div;
+  FastDiv div;
   const void* gate;
   int64_t ldg, R, K;
   int e5m2;

@@ -40,7 +40,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const T* __restrict__ O, int64_t ldo, int64_t rows,
                                                           const int32_t* __restrict__ pos, const float* __restrict__ w,
                                                           int k, int64_t D, T* __restrict__ Y, int64_t ldy, bool vec) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), J = 8;   // J rows in flight
   const int64_t t = blockIdx.x;
   for (int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V; c < D;
        c += (int64_t)gridDim.y * blockDim.x * V) {
@@ -48,14 +48,20 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const T* __restrict__ 
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int64_t p = pos[t * k + j];
-      if (p < 0 || p >= rows) continue;
-      const float wj = w ? w[t * k + j] : 1.f;
-      float x[V];
-      load_row<T, V>(O + p * ldo, c, D, whole, x);
+    for (int j0 = 0; j0 < k; j0 += J) {
+      float x[J][V], wj[J];
+      bool on[J];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += wj * x[i];
+      for (int q = 0; q < J; ++q) {
+        const int64_t p = j0 + q < k ? pos[t * k + j0 + q] : -1;
+        on[q] = p >= 0 && p < rows;
+        wj[q] = on[q] && w ? w[t * k + j0 + q] : 1.f;
+        load_row<T, V>(O + (on[q] ? p : 0) * ldo, c, D, whole, x[q]);   // row 0 where there is none
+      }
+#pragma unroll
+      for (int q = 0; q < J; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = on[q] ? acc[i] + wj[q] * x[q][i] : acc[i];
     }
     store_row<T, V>(Y + t * ldy, c, D, whole, acc);
   }

@@ -5,8 +5,8 @@
 namespace nms {
 namespace {
 
-// Eight consecutive elements of a row from column c, 0 beyond K: 16-byte loads (VEC: the columns exist
-// and the row is aligned) or one at a time.
+// Eight consecutive elements of a row from column c: 16-byte loads (VEC: the row is aligned, and the
+// columns exist), or one at a time with 0 beyond K.
 template <bool VEC, typename T>
 __device__ inline void load8(const T* p, int64_t c, int64_t K, Raw8<T>& x) {
   if constexpr (VEC) {
@@ -20,27 +20,30 @@ __device__ inline void load8(const T* p, int64_t c, int64_t K, Raw8<T>& x) {
 }
 
 // Source row of row r of the quantisers' input, -1 for a row of zeros.
-__device__ inline int64_t source_row(const QuantArgs& a, int64_t r) {
+__device__ inline int source_row(const QuantArgs& a, int r) {
   if (!a.src) return r;
   const int sl = a.src[r];
   const uint32_t t = __umulhi(a.div.mul, (uint32_t)sl);
-  const int64_t row = (t + (((uint32_t)sl - t) >> a.div.s1)) >> a.div.s2;
+  const int row = (int)((t + (((uint32_t)sl - t) >> a.div.s1)) >> a.div.s2);
   return sl >= 0 && row < a.RX ? row : -1;
 }
 // Eight elements of N rows of the input from column c (rows[i] their sources, -1: zeros; r[i] their own
-// numbers, for the gate).  All loads are issued before any is used; a row of zeros reads row 0.
+// numbers, for the gate).  All loads are issued before any is used; what is zero reads a place that
+// exists.  VEC: K % 8 == 0 and aligned rows, so a lane's eight columns exist or do not, together.
 template <bool VEC, typename T, int N>
-__device__ inline void input_rows(const QuantArgs& a, const int64_t (&rows)[N], const int64_t (&r)[N], int64_t c,
+__device__ inline void input_rows(const QuantArgs& a, const int (&rows)[N], const int (&r)[N], int64_t c,
                                   Raw8<T> (&x)[N]) {
   const T* X = (const T*)a.X;
   const T* G = (const T*)a.gate;
   const bool own = G && (const void*)G == a.X && !a.src && a.ldg == a.ldx;   // the gate is the row itself
+  const bool in = c < a.K;
+  const int64_t at = in ? c : 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) load8<VEC>(X + (rows[i] < 0 ? 0 : rows[i]) * a.ldx, c, a.K, x[i]);
+  for (int i = 0; i < N; ++i) load8<VEC>(X + (rows[i] < 0 ? 0 : rows[i]) * a.ldx, at, a.K, x[i]);
   if (G && !own) {
     Raw8<T> g[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) load8<VEC>(G + r[i] * a.ldg, c, a.K, g[i]);
+    for (int i = 0; i < N; ++i) load8<VEC>(G + r[i] * a.ldg, at, a.K, g[i]);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i].gate(g[i]);
   } else if (own) {
@@ -49,7 +52,7 @@ __device__ inline void input_rows(const QuantArgs& a, const int64_t (&rows)[N], 
   }
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (rows[i] < 0) x[i].zero();
+    if (rows[i] < 0 || !in) x[i].zero();
 }
 
 template <int CTRL>
@@ -63,24 +66,23 @@ __device__ inline uint32_t row16_max(uint32_t m) { return dpp_max<0x121>(dpp_max
 // workgroup 4 N rows x 4 blocks; the scales leave through LDS so that a block's are written together.
 // One pass over the data; bound by its bytes.  N = 8 keeps eight rows' loads in flight (36864 gathered
 // rows of 2048: TODO us); N = 1 spreads few rows over more CUs (128 rows of 1024: TODO us).
-template <typename T, bool E5M2, int N>
-__global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a, bool vec) {
+template <typename T, bool E5M2, int N, bool VEC>
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a) {
   __shared__ float sc[4][4 * N];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t r0 = (int64_t)blockIdx.x * (4 * N);
   const int64_t kb0 = (int64_t)blockIdx.y * 4, nkb = (a.K + 127) / 128;
   const int64_t kb = kb0 + (lane >> 4);
   const int64_t c = kb * 128 + (lane & 15) * 8;
-  int64_t r[N], rows[N];
+  int r[N], rows[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    r[i] = r0 + wave * N + i;
-    if (r[i] >= a.R) r[i] = a.R - 1;   // repeats that are not stored
+    const int64_t row = r0 + wave * N + i;
+    r[i] = (int)(row < a.R ? row : a.R - 1);   // repeats that are not stored
     rows[i] = source_row(a, r[i]);
   }
   Raw8<T> x[N];
-  if (vec && (kb0 + 4) * 128 <= a.K) input_rows<true, T, N>(a, rows, r, c, x);
-  else input_rows<false, T, N>(a, rows, r, c, x);
+  input_rows<VEC, T, N>(a, rows, r, c, x);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int rl = wave * N + i;
@@ -142,29 +144,32 @@ __device__ inline void store_transposed(TileT& t, uint8_t* Qt, int64_t ldqt, int
   }
 }
 
-template <typename T, bool E5M2>
-__global__ __launch_bounds__(256) void fp8_quantize_t_kernel(QuantArgs a, bool vec) {
-  __shared__ __align__(16) TileT tile;
-  __shared__ typename Raw8<T>::Max cmax[4][16][Raw8<T>::NMAX];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t r0 = (int64_t)blockIdx.x * 128, k0 = (int64_t)blockIdx.y * 128;
-  const int cg = tid & 15, rg = tid >> 4;
-  const int64_t c = k0 + cg * 8;
+// Transposed: 256 rows (two blocks) x 64 columns a workgroup, so that a column of the result leaves as
+// 256 contiguous bytes (36864 x 2048: TODO us; 128 x 128 tiles, 128 bytes: 56 us).  Thread -> columns
+// 8 (tid % 8) .. +7, rows 8 (tid / 8) .. +7, in registers; the column maxima are reduced over a block's
+// two waves; the bytes pass through LDS, where column j is 32 slots of 8 rows, slot s at s ^ 4 (j / 8):
+// a wave's writes cover all banks twice, and 16-byte reads keep their order.
+template <typename T, bool E5M2, bool VEC>
+__global__ __launch_bounds__(256) void fp8_quantize_t_kernel(QuantArgs a) {
   constexpr int NM = Raw8<T>::NMAX;
+  __shared__ __align__(16) unsigned char tile[64][256];
+  __shared__ typename Raw8<T>::Max cmax[4][8][NM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t r0 = (int64_t)blockIdx.x * 256, k0 = (int64_t)blockIdx.y * 64;
+  const int cg = tid & 7, rg = tid >> 3;
+  const int64_t c = k0 + cg * 8;
   Raw8<T> x[8];
-  int64_t r[8], rows[8];
+  int r[8], rows[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    r[i] = r0 + rg * 8 + i;
-    const bool in = r[i] < a.R;
-    if (!in) r[i] = a.R - 1;
+    const int64_t row = r0 + rg * 8 + i;
+    const bool in = row < a.R;
+    r[i] = (int)(in ? row : a.R - 1);
     rows[i] = source_row(a, r[i]);
     if (!in) rows[i] = -1;   // the padding columns of the result are 0
   }
-  if (vec && k0 + 128 <= a.K) input_rows<true, T, 8>(a, rows, r, c, x);
-  else input_rows<false, T, 8>(a, rows, r, c, x);
+  input_rows<VEC, T, 8>(a, rows, r, c, x);
   typename Raw8<T>::Max m[NM];
-  // the columns' maxima: over the thread's rows, the wave's four row groups, the four waves
   auto maxima = [&](auto mag) {
 #pragma unroll
     for (int q = 0; q < NM; ++q) {
@@ -172,7 +177,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_t_kernel(QuantArgs a, bool v
 #pragma unroll
       for (int i = 1; i < 8; ++i) m[q] = vmax(m[q], mag(x[i], q));
 #pragma unroll
-      for (int d = 16; d <= 32; d *= 2) {
+      for (int d = 8; d <= 32; d *= 2) {
         uint32_t o;
         __builtin_memcpy(&o, &m[q], 4);
         o = __shfl_xor(o, d);
@@ -180,11 +185,11 @@ __global__ __launch_bounds__(256) void fp8_quantize_t_kernel(QuantArgs a, bool v
         __builtin_memcpy(&om, &o, 4);
         m[q] = vmax(m[q], om);
       }
-      if (lane < 16) cmax[wave][cg][q] = m[q];
+      if (lane < 8) cmax[wave][cg][q] = m[q];
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < NM; ++q) m[q] = vmax(vmax(cmax[0][cg][q], cmax[1][cg][q]), vmax(cmax[2][cg][q], cmax[3][cg][q]));
+    for (int q = 0; q < NM; ++q) m[q] = vmax(cmax[wave & 2][cg][q], cmax[(wave & 2) + 1][cg][q]);
   };
   maxima([](const Raw8<T>& v, int q) { return v.mag(q); });
   bool odd = false;   // a column with an infinity or NaN
@@ -195,16 +200,27 @@ __global__ __launch_bounds__(256) void fp8_quantize_t_kernel(QuantArgs a, bool v
     for (int i = 0; i < 8; ++i) x[i].clean();
     maxima([](const Raw8<T>& v, int q) { return v.mag_finite(q); });
   }
+  const int64_t rp = (a.R + 127) / 128 * 128;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const int col = cg * 8 + q;
     const float scale = power2(block_exponent(Raw8<T>::column(m, q), E5M2));
     const u32x2 b = pack_column<E5M2>(x, q, scale);
-    *tile_slot(tile, col, rg) = (uint64_t)b[0] | ((uint64_t)b[1] << 32);
-    if (rg == 0 && k0 + col < a.K) a.S[(int64_t)blockIdx.x * a.lds + k0 + col] = scale;
+    *reinterpret_cast<u32x2*>(&tile[cg * 8 + q][(rg ^ (cg * 4)) * 8]) = b;
+    if ((rg & 15) == 0 && c + q < a.K && r0 + rg * 8 < rp) a.S[(r0 / 128 + (rg >> 4)) * a.lds + c + q] = scale;
   }
   __syncthreads();
-  store_transposed(tile, a.Q, a.ldq, k0, a.K, r0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int id = tid + 256 * i, col = id >> 4, piece = id & 15;   // 16 rows a piece
+    if (k0 + col >= a.K || r0 + 16 * piece >= rp) continue;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(&tile[col][((2 * piece) ^ ((col >> 3) * 4)) * 8]);
+    uint8_t* dst = a.Q + (k0 + col) * a.ldq + r0 + 16 * piece;
+    if (((uintptr_t)dst & 15) == 0) {
+      *reinterpret_cast<u32x4*>(dst) = v;
+    } else {
+      for (int b = 0; b < 16; ++b) dst[b] = (uint8_t)(v[b >> 2] >> (8 * (b & 3)));
+    }
+  }
 }
 
 // One 128 x 128 block of a weight: its bytes row by row, and the same bytes transposed.
@@ -292,35 +308,42 @@ bool vec_ok(int es, const void* X, int64_t ldx, const void* gate, int64_t ldg) {
 
 }  // namespace
 
-template <typename T, bool E5M2>
+template <typename T, bool E5M2, bool VEC>
 static hipError_t quantize_rows(const QuantArgs& a, hipStream_t s) {
-  const bool vec = vec_ok(sizeof(T), a.X, a.ldx, a.gate, a.ldg);
   const unsigned gy = (unsigned)((a.K + 511) / 512);
   // eight rows a wave once that fills the chip's 256 CUs twice
   if ((a.R + 31) / 32 * gy >= 512)
-    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 8>), dim3((unsigned)((a.R + 31) / 32), gy), dim3(256), 0, s, a, vec);
+    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 8, VEC>), dim3((unsigned)((a.R + 31) / 32), gy), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 1>), dim3((unsigned)((a.R + 3) / 4), gy), dim3(256), 0, s, a, vec);
+    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 1, VEC>), dim3((unsigned)((a.R + 3) / 4), gy), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool E5M2, bool VEC>
+static hipError_t quantize_columns(const QuantArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((fp8_quantize_t_kernel<T, E5M2, VEC>), dim3((unsigned)((a.R + 255) / 256), (unsigned)((a.K + 63) / 64)),
+                     dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s) {
-  if (dt == DT_BF16) return a.e5m2 ? quantize_rows<uint16_t, true>(a, s) : quantize_rows<uint16_t, false>(a, s);
-  return a.e5m2 ? quantize_rows<uint32_t, true>(a, s) : quantize_rows<uint32_t, false>(a, s);
+  const bool vec = a.K % 8 == 0 && vec_ok(dt == DT_BF16 ? 2 : 4, a.X, a.ldx, a.gate, a.ldg);
+  if (dt == DT_BF16) {
+    if (a.e5m2) return vec ? quantize_rows<uint16_t, true, true>(a, s) : quantize_rows<uint16_t, true, false>(a, s);
+    return vec ? quantize_rows<uint16_t, false, true>(a, s) : quantize_rows<uint16_t, false, false>(a, s);
+  }
+  if (a.e5m2) return vec ? quantize_rows<uint32_t, true, true>(a, s) : quantize_rows<uint32_t, true, false>(a, s);
+  return vec ? quantize_rows<uint32_t, false, true>(a, s) : quantize_rows<uint32_t, false, false>(a, s);
 }
 
 hipError_t launch_fp8_quantize_t(int dt, const QuantArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.R + 127) / 128), (unsigned)((a.K + 127) / 128));
+  const bool vec = a.K % 8 == 0 && vec_ok(dt == DT_BF16 ? 2 : 4, a.X, a.ldx, a.gate, a.ldg);
   if (dt == DT_BF16) {
-    const bool vec = vec_ok(2, a.X, a.ldx, a.gate, a.ldg);
-    if (a.e5m2) hipLaunchKernelGGL((fp8_quantize_t_kernel<uint16_t, true>), grid, dim3(256), 0, s, a, vec);
-    else hipLaunchKernelGGL((fp8_quantize_t_kernel<uint16_t, false>), grid, dim3(256), 0, s, a, vec);
-  } else {
-    const bool vec = vec_ok(4, a.X, a.ldx, a.gate, a.ldg);
-    if (a.e5m2) hipLaunchKernelGGL((fp8_quantize_t_kernel<uint32_t, true>), grid, dim3(256), 0, s, a, vec);
-    else hipLaunchKernelGGL((fp8_quantize_t_kernel<uint32_t, false>), grid, dim3(256), 0, s, a, vec);
+    if (a.e5m2) return vec ? quantize_columns<uint16_t, true, true>(a, s) : quantize_columns<uint16_t, true, false>(a, s);
+    return vec ? quantize_columns<uint16_t, false, true>(a, s) : quantize_columns<uint16_t, false, false>(a, s);
   }
-  return hipGetLastError();
+  if (a.e5m2) return vec ? quantize_columns<uint32_t, true, true>(a, s) : quantize_columns<uint32_t, true, false>(a, s);
+  return vec ? quantize_columns<uint32_t, false, true>(a, s) : quantize_columns<uint32_t, false, false>(a, s);
 }
 
 hipError_t launch_fp8_quantize_weight(int dt, const void* W, int64_t ldw, int64_t E, int64_t N, int64_t K, int e5m2,

@@ -313,7 +313,7 @@ static hipError_t quantize_rows(const QuantArgs& a, hipStream_t s) {
   const unsigned gy = (unsigned)((a.K + 511) / 512);
   // eight rows a wave once that fills the chip's 256 CUs twice
   if ((a.R + 31) / 32 * gy >= 512)
-    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 8, VEC>), dim3((unsigned)((a.R + 31) / 32), gy), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 4, VEC>), dim3((unsigned)((a.R + 15) / 16), gy), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((fp8_quantize_kernel<T, E5M2, 1, VEC>), dim3((unsigned)((a.R + 3) / 4), gy), dim3(256), 0, s, a);
   return hipGetLastError();

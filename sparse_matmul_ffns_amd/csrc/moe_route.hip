@@ -36,29 +36,37 @@ __device__ inline float reduce_sum(float v, int lane) {
   v = reduce_f32<LPT>(v, [](float a, float b) { return a + b; });
   return __shfl(v, lane & ~(LPT - 1));
 }
-// Largest (key, then lowest index) pair; the index is held complemented.
+// A choice as one number: the order key in the high 32 of 62 bits, below it the complement of the
+// expert's index, so that the largest is the best and on equal keys the lowest index.  Read as a double
+// (positive and finite: the bits above are 0), so that one instruction takes the larger of two.
+__device__ inline double choice(uint32_t key, int e) {
+  const uint64_t b = ((uint64_t)key << 30) | (uint32_t)(1023 - e);
+  return __builtin_bit_cast(double, key ? b : 0);
+}
+__device__ inline double larger(double a, double b) { return __builtin_fmax(a, b); }
 template <int CTRL>
-__device__ inline void best_step(uint32_t& key, uint32_t& nidx) {
-  const uint32_t k2 = dpp_row<CTRL>(key), n2 = dpp_row<CTRL>(nidx);
-  const bool take = k2 > key || (k2 == key && n2 > nidx);
-  key = take ? k2 : key;
-  nidx = take ? n2 : nidx;
+__device__ inline double larger_step(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  const u32x2 o = {dpp_row<CTRL>(b[0]), dpp_row<CTRL>(b[1])};
+  return larger(v, __builtin_bit_cast(double, o));
 }
 template <int LPT>
-__device__ inline void reduce_best(uint32_t& key, uint32_t& nidx) {
-  best_step<0x128>(key, nidx);
-  best_step<0x124>(key, nidx);
-  best_step<0x122>(key, nidx);
-  best_step<0x121>(key, nidx);
+__device__ inline double reduce_larger(double v) {
+  v = larger_step<0x121>(larger_step<0x122>(larger_step<0x124>(larger_step<0x128>(v))));
   if constexpr (LPT == 64) {
-#pragma unroll
-    for (int d = 16; d <= 32; d *= 2) {
-      const uint32_t k2 = __shfl_xor(key, d), n2 = __shfl_xor(nidx, d);
-      const bool take = k2 > key || (k2 == key && n2 > nidx);
-      key = take ? k2 : key;
-      nidx = take ? n2 : nidx;
-    }
+    v = larger(v, __shfl_xor(v, 16));
+    v = larger(v, __shfl_xor(v, 32));
   }
+  return v;
+}
+
+// The two largest of two lanes' two largest.
+template <int CTRL>
+__device__ inline void merge_top2(float& t1, float& t2) {
+  const float o1 = __uint_as_float(dpp_row<CTRL>(__float_as_uint(t1)));
+  const float o2 = __uint_as_float(dpp_row<CTRL>(__float_as_uint(t2)));
+  t2 = fmaxf(fmaxf(t2, o2), fminf(t1, o1));
+  t1 = fmaxf(t1, o1);
 }
 
 // Unsigned key with the order of the floats (no NaN; +0 and -0 alike); every value but -infinity
@@ -139,15 +147,26 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, bool vec) {
   }
 
   uint32_t key[EPL];
+  float c[EPL];
   if (a.bias || grouped) {
+    float b[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) b[i] = a.bias ? a.bias[e0 + i < E ? e0 + i : E - 1] : 0.f;
+    // reciprocals of one unit in the last place
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = __builtin_amdgcn_rcpf(1.f + expf(-v[i]));
+    } else {
+      const float inv = 1.f / Z;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = expf(v[i] - m) * inv;
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const float s = a.sigmoid ? 1.f / (1.f + expf(-v[i])) : expf(v[i] - m) / Z;
-      float c = s;
-      if (a.bias) c += a.bias[e0 + i < E ? e0 + i : E - 1];
-      const bool ok = v[i] > kNegInf && c > kNegInf;   // false for a NaN bias
-      cs[slot_tok][e0 + i] = ok ? c : kNegInf;
-      key[i] = ok ? order_key(a.bias ? c : v[i]) : 0u;
+      c[i] += b[i];
+      const bool ok = v[i] > kNegInf && c[i] > kNegInf;   // false for a NaN bias
+      c[i] = ok ? c[i] : kNegInf;
+      key[i] = ok ? order_key(a.bias ? c[i] : v[i]) : 0u;
     }
   } else {
 #pragma unroll
@@ -157,47 +176,83 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, bool vec) {
 
   if (grouped) {
     const int size = E / a.groups;
-    for (int g = li; g < a.groups; g += LPT) {
+    const int lanes = size / EPL;   // of a group, if it is whole lanes and a power of two of them
+    if (LPT == 16 && size == lanes * EPL && (lanes & (lanes - 1)) == 0 && lanes * a.groups == 16) {
+      // in registers: a lane's two largest, merged over the group's lanes (xor 1, 2, then mirrors, which
+      // reach the other half once the halves agree); then every lane sees the 15 others by rotation
       float t1 = kNegInf, t2 = kNegInf;
-      for (int j = 0, q = g % size; j < size; ++j, q = q + 1 == size ? 0 : q + 1) {   // staggered: LDS banks
-        const float c = cs[slot_tok][g * size + q];
-        t2 = fmaxf(t2, fminf(t1, c));
-        t1 = fmaxf(t1, c);
-      }
-      gscore[slot_tok][g] = a.group_top == 2 && t2 > kNegInf ? t1 + t2 : t1;
-    }
-    __syncthreads();
-    for (int g = li; g < a.groups; g += LPT) {
-      const float mine = gscore[slot_tok][g];
-      int rank = 0;
-      for (int q = 0; q < a.groups; ++q) {
-        const float o = gscore[slot_tok][q];
-        rank += (o > mine || (o == mine && q < g)) ? 1 : 0;
-      }
-      gkeep[slot_tok][g] = rank < a.topk_groups;
-    }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (e0 + i < E && !gkeep[slot_tok][(e0 + i) / size]) key[i] = 0u;
+      for (int i = 0; i < EPL; ++i) {
+        t2 = fmaxf(t2, fminf(t1, c[i]));
+        t1 = fmaxf(t1, c[i]);
+      }
+      if (lanes >= 2) merge_top2<0xB1>(t1, t2);
+      if (lanes >= 4) merge_top2<0x4E>(t1, t2);
+      if (lanes >= 8) merge_top2<0x141>(t1, t2);
+      const float mine = a.group_top == 2 && t2 > kNegInf ? t1 + t2 : t1;
+      const int g = li / lanes;
+      float o = mine;
+      int og = g, rank = 0;
+      for (int r = 1; r < 16; ++r) {
+        o = __uint_as_float(dpp_row<0x121>(__float_as_uint(o)));
+        og = (int)dpp_row<0x121>((uint32_t)og);
+        rank += (o > mine || (o == mine && og < g)) ? 1 : 0;   // each better group once per lane of it
+      }
+      if (rank >= a.topk_groups * lanes) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) cs[slot_tok][e0 + i] = c[i];
+      __syncthreads();
+      for (int g = li; g < a.groups; g += LPT) {
+        float t1 = kNegInf, t2 = kNegInf;
+        for (int j = 0, q = g % size; j < size; ++j, q = q + 1 == size ? 0 : q + 1) {   // staggered: LDS banks
+          const float v1 = cs[slot_tok][g * size + q];
+          t2 = fmaxf(t2, fminf(t1, v1));
+          t1 = fmaxf(t1, v1);
+        }
+        gscore[slot_tok][g] = a.group_top == 2 && t2 > kNegInf ? t1 + t2 : t1;
+      }
+      __syncthreads();
+      for (int g = li; g < a.groups; g += LPT) {
+        const float mine = gscore[slot_tok][g];
+        int rank = 0;
+        for (int q = 0; q < a.groups; ++q) {
+          const float o = gscore[slot_tok][q];
+          rank += (o > mine || (o == mine && q < g)) ? 1 : 0;
+        }
+        gkeep[slot_tok][g] = rank < a.topk_groups;
+      }
+      __syncthreads();
+      int g = e0 / size, left = size - e0 % size;   // this expert's group, and how many of it are left
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (e0 + i < E && !gkeep[slot_tok][g]) key[i] = 0u;
+        if (--left == 0) {
+          ++g;
+          left = size;
+        }
+      }
+    }
   }
 
+  double pick[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) pick[i] = choice(key[i], e0 + i);
   int id = -1;
   for (int r = 0; r < a.k; ++r) {
-    uint32_t bk = 0;
-    int bi = 0;
+    double best = pick[0];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const bool take = key[i] > bk;
-      bk = take ? key[i] : bk;
-      bi = take ? i : bi;
-    }
-    uint32_t nidx = ~(uint32_t)(e0 + bi);
-    reduce_best<LPT>(bk, nidx);
-    const int won = (int)~nidx;
-    if (li == r) id = bk ? won : -1;
+    for (int i = 1; i < EPL; ++i) best = larger(best, pick[i]);
+    best = reduce_larger<LPT>(best);
+    const uint64_t b = __builtin_bit_cast(uint64_t, best);
+    const int won = b ? 1023 - (int)(b & 1023) : -1;
+    if (li == r) id = won;
+    const int mine = won - e0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = won == e0 + i ? 0u : key[i];
+    for (int i = 0; i < EPL; ++i) pick[i] = mine == i ? 0.0 : pick[i];
   }
 
   const bool has = li < a.k && id >= 0;
@@ -348,12 +403,14 @@ hipError_t bwd_t(const T* logits, int64_t ldl, int64_t Tn, int E, int sigmoid, i
 // such lanes below it.  Integer counts only: the result does not depend on the order of threads.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
-constexpr int64_t kPlanChunk = 4096;
+constexpr int64_t kPlanChunk = 4096;   // of a single workgroup
+constexpr int64_t kPlanSmall = 2048;   // of one of many
 
 int64_t plan_chunk(int64_t n) {
   // at most 256 chunks: a workgroup of the second kernel reads every chunk's counts
+  if (n <= kPlanChunk) return kPlanChunk;
   const int64_t c = (n + 255) / 256;
-  return c <= kPlanChunk ? kPlanChunk : (c + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  return c <= kPlanSmall ? kPlanSmall : (c + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
 }
 
 __global__ __launch_bounds__(kPlanThreads) void moe_plan_count_kernel(const int32_t* ids, int64_t n, int E,
@@ -377,7 +434,8 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_place_kernel(const int3
   extern __shared__ int32_t smem[];
   int32_t* hist = smem;                       // [waves][E]: a wave's counts, then its next rows
   int32_t* scan = hist + kPlanWaves * E;      // [1024] padded counts, summed up to and including e
-  int32_t* total = scan + kPlanThreads;       // [E]
+  int32_t* lows = scan + kPlanThreads;        // [1024]
+  int32_t* total = lows + kPlanThreads;       // [E]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < n ? lo + chunk : n;
   const int64_t part = chunk / kPlanWaves;    // a multiple of 64
@@ -391,20 +449,44 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_place_kernel(const int3
   }
   __syncthreads();
   int before = 0, mine = 0;
+  int own[kPlanWaves];   // the waves' counts of expert tid
   if (tid < E) {
-    if (nchunks > 1) {
-      int sum = 0;
-      for (int c = 0; c < nchunks; ++c) {
-        const int v = work[(int64_t)c * E + tid];
-        before += c < (int)blockIdx.x ? v : 0;
-        sum += v;
-      }
-      mine = sum;
-    } else {
-      for (int w = 0; w < kPlanWaves; ++w) mine += hist[w * E + tid];
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) own[w] = hist[w * E + tid];
+    if (nchunks == 1) {
+#pragma unroll
+      for (int w = 0; w < kPlanWaves; ++w) mine += own[w];
     }
-    total[tid] = mine;
   }
+  if (nchunks > 1) {
+    // the counts of all chunks and of those before this one: E experts x as many parts as threads allow,
+    // eight loads in flight each, added up through LDS (scan and the space behind it)
+    const int parts = kPlanThreads / E < 16 ? kPlanThreads / E : 16;   // E <= 1024
+    const int e = tid % E, part = tid / E;
+    int sum = 0, low = 0;
+    if (part < parts) {
+      for (int c0 = part; c0 < nchunks; c0 += 8 * parts) {
+        int v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = c0 + u * parts < nchunks ? work[(int64_t)(c0 + u * parts) * E + e] : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          sum += v[u];
+          low += c0 + u * parts < (int)blockIdx.x ? v[u] : 0;
+        }
+      }
+    }
+    scan[tid] = sum;
+    lows[tid] = low;
+    __syncthreads();
+    if (tid < E)
+      for (int q = 0; q < parts; ++q) {
+        mine += scan[q * E + tid];
+        before += lows[q * E + tid];
+      }
+    __syncthreads();
+  }
+  if (tid < E) total[tid] = mine;
   const int padded = (mine + align - 1) & ~(align - 1);
   // inclusive sum of the padded counts over the experts: within waves, then over the waves
   int inc = padded;
@@ -415,17 +497,19 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_place_kernel(const int3
   }
   scan[tid] = inc;
   __syncthreads();
-  int carry = 0;
-  for (int w = 0; w < wave; ++w) carry += scan[w * 64 + 63];
+  int carry = lane < wave ? scan[lane * 64 + 63] : 0;
+#pragma unroll
+  for (int d = 8; d > 0; d /= 2) carry += __shfl_xor(carry, d);
+  carry = __shfl(carry, 0);
   __syncthreads();
   inc += carry;
   scan[tid] = inc;
   if (tid < E) {
     int base = inc - padded + before;
+#pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) {
-      const int t = hist[w * E + tid];
       hist[w * E + tid] = base;
-      base += t;
+      base += own[w];
     }
     if (blockIdx.x == 0) {
       offsets[tid + 1] = inc;
@@ -495,7 +579,7 @@ hipError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int align, int3
     hipLaunchKernelGGL(moe_plan_count_kernel, dim3(nchunks), dim3(kPlanThreads), E * 4, s, ids, n, E, chunk, work);
   int bits = 0;
   while ((1 << bits) < E) ++bits;
-  const size_t lds = ((size_t)kPlanWaves * E + kPlanThreads + E) * 4;
+  const size_t lds = ((size_t)kPlanWaves * E + 2 * kPlanThreads + E) * 4;
   (void)hipFuncSetAttribute((const void*)moe_plan_place_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   hipLaunchKernelGGL(moe_plan_place_kernel, dim3(nchunks), dim3(kPlanThreads), lds, s, ids, n, E, bits,
                      align, chunk, nchunks, offsets, counts, src, rows, pos, work);

@@ -113,7 +113,7 @@ __device__ inline float sigmoid_shifted(float l, float shift) {
 // key cleared.  Slot j's id ends in lane j, which computes the weight.  What bounds it: a launch and
 // one round trip to memory for few tokens; for many, the rounds' vector instructions.
 template <typename T, int LPT, int EPL>
-__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, bool vec) {
+__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, bool vec, bool vec_bias) {
   constexpr int TPW = 64 / LPT, ROW = LPT * EPL;
   __shared__ float lg[4 * TPW][ROW];
   __shared__ float cs[4 * TPW][ROW];
@@ -151,7 +151,13 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, bool vec) {
   if (a.bias || grouped) {
     float b[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) b[i] = a.bias ? a.bias[e0 + i < E ? e0 + i : E - 1] : 0.f;
+    for (int i = 0; i < EPL; ++i) b[i] = 0.f;
+    if (vec_bias) {
+      if (e0 < E) __builtin_memcpy(b, __builtin_assume_aligned(a.bias + e0, 16), sizeof(b));
+    } else if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) b[i] = a.bias[e0 + i < E ? e0 + i : E - 1];
+    }
     // reciprocals of one unit in the last place
     if (a.sigmoid) {
 #pragma unroll
@@ -362,7 +368,8 @@ template <typename T, int LPT, int EPL>
 hipError_t run_route(const RouteArgs& a, hipStream_t s) {
   const int per = 4 * (64 / LPT);
   hipLaunchKernelGGL((moe_route_kernel<T, LPT, EPL>), dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, s, a,
-                     rows_vec(a.logits, a.ldl, sizeof(T), a.E, EPL));
+                     rows_vec(a.logits, a.ldl, sizeof(T), a.E, EPL),
+                     a.bias && a.E % EPL == 0 && (uintptr_t)a.bias % 16 == 0);
   return hipGetLastError();
 }
 

@@ -51,3 +51,4 @@ from .nmsparse import (  # noqa: F401
     spmm_venom,
     transpose,
 )
+from .moe import ExpertFFN  # noqa: E402,F401

@@ -1,8 +1,8 @@
 // Products of 8-bit matrices with a scale for each block of 128 along the reduction: one product,
 // one per group of A's rows, or one per run of the reduction.
 //
-// v_mfma_f32_16x16x128_f8f6f4 spans exactly one scale block: its result is the block's fp32 sum,
-// which the vector unit scales and adds to the accumulator.  B takes the instruction's row operand
+// v_mfma_f32_16x16x128_f8f6f4 spans exactly one scale block: its result is the block's sum, which the
+// vector unit scales and adds to the fp32 accumulator.  B takes the instruction's row operand
 // and A its column operand, so a lane holds four consecutive columns n of one row m of C.
 #include "common.hpp"
 #include "dma.hpp"
@@ -14,11 +14,39 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
-// D[i][j] = sum_k X[i][k] Y[j][k] over 128 k; fx, fy: 0 e4m3, 1 e5m2.
-template <int FX, int FY>
+// Eight 8-bit values (F: 0 e4m3, 1 e5m2) as bf16, exactly.
+template <int F>
+__device__ inline bf16x8 widen8(uint32_t lo, uint32_t hi) {
+  u32x4 w;
+  if constexpr (F) {
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.f, false));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.f, true));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.f, false));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.f, true));
+  } else {
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true));
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// D[i][j] = sum_k X[i][k] Y[j][k] over 128 k, a lane holding 32 k of row l % 16 of each (the same ones);
+// FX, FY: 0 e4m3, 1 e5m2.  The 8-bit matrix instruction adds its products aligned to the largest of
+// them, keeping 2^-13 of it: 1.5e-5 of the result (root mean square, normal operands), far below a bf16
+// result's 2^-9 but not fp32's accuracy.  EXACT (fp32 results): the bytes widened to bf16 and four bf16
+// instructions, whose products and sums are fp32, at half the rate.
+template <int FX, int FY, bool EXACT>
 __device__ inline f32x4 mfma128(i32x8 x, i32x8 y) {
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, zero, FX, FY, 0, 0, 0, 0);
+  if constexpr (!EXACT) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, zero, FX, FY, 0, 0, 0, 0);
+  f32x4 d = zero;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<FX>(x[2 * s], x[2 * s + 1]), widen8<FY>(y[2 * s], y[2 * s + 1]), d,
+                                               0, 0, 0);
+  return d;
 }
 
 // What a workgroup computes: rows m0 .. m_end - 1 (at most a tile of them) of A and C times B's rows
@@ -211,7 +239,7 @@ __device__ inline void store_tile(const f32x4 (&acc)[FM][FN], T* C, int64_t ldc,
 // 128-block of both operands goes through LDS byte by byte where the rows are not 16-byte aligned,
 // with zeros beyond the rows and beyond K.
 constexpr int GP = 144;   // LDS row pitch: 128 bytes and a shift of the banks per row
-template <int FA, int FB>
+template <int FA, int FB, bool EXACT>
 __global__ __launch_bounds__(256) void fp8_gemm_general_kernel(Fp8Gemm g, bool vec_a, bool vec_b) {
   __shared__ __align__(16) unsigned char sA[64 * GP], sB[64 * GP];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -286,7 +314,7 @@ __global__ __launch_bounds__(256) void fp8_gemm_general_kernel(Fp8Gemm g, bool v
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int64_t n = t.n0 + wn + j * 16 + lq * 4;
-        const f32x4 p = mfma128<FB, FA>(frag(sB, wn + j * 16 + l16), fa);
+        const f32x4 p = mfma128<FB, FA, EXACT>(frag(sB, wn + j * 16 + l16), fa);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float sbn = 0.f;
@@ -317,8 +345,9 @@ hipError_t run_general(const Fp8Gemm& g, hipStream_t s) {
   const bool va = (uintptr_t)g.A % 16 == 0 && g.lda % 16 == 0, vb = (uintptr_t)g.B % 16 == 0 && g.ldb % 16 == 0;
   const int64_t ntn = (g.N + 63) / 64;
   const int64_t ntm = g.mode == G_ROWS ? most_row_tiles(g, 64) : (g.M + 63) / 64;
-  hipLaunchKernelGGL((fp8_gemm_general_kernel<FA, FB>), dim3((unsigned)ntm, (unsigned)ntn, g.mode == G_RED ? g.E : 1),
-                     dim3(256), 0, s, g, va, vb);
+  const dim3 grid((unsigned)ntm, (unsigned)ntn, g.mode == G_RED ? g.E : 1);
+  if (g.bf16_out) hipLaunchKernelGGL((fp8_gemm_general_kernel<FA, FB, false>), grid, dim3(256), 0, s, g, va, vb);
+  else hipLaunchKernelGGL((fp8_gemm_general_kernel<FA, FB, true>), grid, dim3(256), 0, s, g, va, vb);
   return hipGetLastError();
 }
 
@@ -343,7 +372,7 @@ struct TileCfg {
   static_assert((BM + BN) / 64 == WAVES, "one load of 64 scales a wave");
 };
 
-template <int FA, int FB, bool ROWB, typename Cfg>
+template <int FA, int FB, bool ROWB, bool EXACT, typename Cfg>
 __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   constexpr int BM = Cfg::BM, BN = Cfg::BN, FM = Cfg::FM, FN = Cfg::FN;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -489,13 +518,19 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
 
   constexpr int D = Cfg::D;
   i32x8 a[FM], b[D + 1];
-  f32x4 p[2][FM], sn = {0.f, 0.f, 0.f, 0.f};
+  bf16x8 aw[EXACT ? FM : 1][4];   // EXACT: the stage's A fragments widened
+  f32x4 p[2][FM], sn = {0.f, 0.f, 0.f, 0.f}, late[D];   // late: the row scales of the last D slots
   float s[FM], sprev[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     p[1][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     s[i] = 0.f;
   }
+#pragma unroll
+  for (int d = 0; d < D; ++d) late[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto row_scales = [&](int kt, int j) {
+    return *reinterpret_cast<const f32x4*>(scales(kt) + BM + wn + 16 * j + 4 * lq);
+  };
   auto load_scales = [&](int kt) {
     const float sbw = scales(kt)[BM + wn];
 #pragma unroll
@@ -504,19 +539,25 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   auto scale = [&](int i, int j, const float (&sc_)[FM]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float v = ROWB ? p[j & 1][i][q] * sn[q] : p[j & 1][i][q];
+      const float v = ROWB ? p[j & 1][i][q] * (j < FN - D ? sn[q] : late[j < FN - D ? 0 : j - (FN - D)][q]) : p[j & 1][i][q];
       acc[i][j][q] = __builtin_fmaf(v, sc_[i], acc[i][j][q]);
     }
     asm volatile("" : "+v"(acc[i][j]));   // here, not sunk to the end of the loop
   };
   // Stage kt.  Slot j: fragment j's FM matrix instructions, and between them the scaling of the slot
   // before (a result is read FM matrix instructions after its own was issued; slot 0 finishes the stage
-  // before).  B's fragments are read two slots ahead, so slot FN - 2 holds none of this stage's reads:
-  // there the waves meet, and the two last slots read the next stage's first fragments and issue the
-  // loads of the stage after it into the buffer just left.
+  // before).  B's fragments are read D slots ahead, and the last D slots' row scales before slot FN - D,
+  // so from there on nothing of this stage is read: there the waves meet, and the last D slots read the
+  // next stage's first fragments and issue the loads of the stage after it into the buffer just left.
   auto stage = [&](int kt) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) sprev[i] = s[i];
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) aw[i][h] = widen8<FA>(a[i][2 * h], a[i][2 * h + 1]);
+    }
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       if (j == FN - D) land(kt + 1);
@@ -524,19 +565,35 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
       else b[(j + D) % (D + 1)] = frag(kt + 1, b_row + (j + D - FN) * 2048);
       if (j == 0) load_scales(kt);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
-        p[j & 1][i] = mfma128<FB, FA>(b[j % (D + 1)], a[i]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (j == 0) scale(i, FN - 1, sprev); else scale(i, j - 1, s);
-        if (j == FN - 1) a[i] = frag(kt + 1, a_row + i * 2048);
-        if (j >= FN - D) {
-          constexpr int PER = Cfg::LOADS / (D * FM);
+      for (int h = 0; h < (EXACT ? 4 : 1); ++h) {
+        bf16x8 bw;
+        if constexpr (EXACT) bw = widen8<FB>(b[j % (D + 1)][2 * h], b[j % (D + 1)][2 * h + 1]);
 #pragma unroll
-          for (int u = 0; u < PER; ++u) dma(kt + 2, ((j - (FN - D)) * FM + i) * PER + u);
+        for (int i = 0; i < FM; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (EXACT)
+            p[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                bw, aw[i][h], h == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : p[j & 1][i], 0, 0, 0);
+          else
+            p[j & 1][i] = mfma128<FB, FA, false>(b[j % (D + 1)], a[i]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (h > 0) continue;
+          if (j == 0) scale(i, FN - 1, sprev); else scale(i, j - 1, s);
+          if (j == FN - 1) a[i] = frag(kt + 1, a_row + i * 2048);
+          if (j >= FN - D) {
+            constexpr int PER = Cfg::LOADS / (D * FM);
+#pragma unroll
+            for (int u = 0; u < PER; ++u) dma(kt + 2, ((j - (FN - D)) * FM + i) * PER + u);
+          }
         }
       }
-      if (ROWB) sn = *reinterpret_cast<const f32x4*>(scales(kt) + BM + wn + 16 * j + 4 * lq);
+      if (ROWB) {
+        if (j < FN - D) sn = row_scales(kt, j);
+        if (j == FN - D - 1) {
+#pragma unroll
+          for (int d = 0; d < D; ++d) late[d] = row_scales(kt, FN - D + d);
+        }
+      }
     }
     dma(kt + 2, Cfg::LOADS);
     if constexpr (FN % (D + 1) != 0) {
@@ -571,9 +628,9 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   else store_tile<FM, FN>(acc, (float*)g.C + crow * g.ldc, g.ldc, rows_left, n, g.N, lane);
 }
 
-template <int FA, int FB, bool ROWB, typename Cfg>
+template <int FA, int FB, bool ROWB, bool EXACT, typename Cfg>
 hipError_t run_tile(const Fp8Gemm& g, hipStream_t s) {
-  auto kern = fp8_gemm_tile_kernel<FA, FB, ROWB, Cfg>;
+  auto kern = fp8_gemm_tile_kernel<FA, FB, ROWB, EXACT, Cfg>;
   (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS);
   const int64_t ntn = (g.N + Cfg::BN - 1) / Cfg::BN, ntm = (g.M + Cfg::BM - 1) / Cfg::BM;
   int64_t wgs = ntm * ntn;
@@ -591,7 +648,7 @@ hipError_t run_tile(const Fp8Gemm& g, hipStream_t s) {
 // two 128-blocks, each with the next chunk's loads in flight, and add their sums through LDS in the
 // order of the waves.  The lanes of a row that does not exist load nothing.
 // ---------------------------------------------------------------------------
-template <int FA, int FB, bool ROWB, int FM, int KS>
+template <int FA, int FB, bool ROWB, bool EXACT, int FM, int KS>
 __global__ __launch_bounds__(64 * KS) void fp8_gemm_rows_kernel(Fp8Gemm g) {
   constexpr int BM = 16 * FM, BN = 32, FN = 2, CH = 2;   // CH: 128-blocks a chunk
   __shared__ f32x4 part[KS][FM * FN][64];
@@ -713,7 +770,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_gemm_rows_kernel(Fp8Gemm g) {
         const i32x8 fb = __builtin_bit_cast(i32x8, x.b[u][j]);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-          const f32x4 p = mfma128<FB, FA>(fb, __builtin_bit_cast(i32x8, x.a[u][i]));
+          const f32x4 p = mfma128<FB, FA, EXACT>(fb, __builtin_bit_cast(i32x8, x.a[u][i]));
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             acc[i][j][q] += p[q] * (x.sa[u][i] * (ROWB ? x.sb[u][4 * j + q] : x.sb[u][0]));
@@ -752,7 +809,9 @@ hipError_t run_rows(const Fp8Gemm& g, hipStream_t s) {
   const int64_t ntn = (g.N + 31) / 32;
   const int64_t ntm = g.mode == G_ROWS ? most_row_tiles(g, 16 * FM) : (g.M + 16 * FM - 1) / (16 * FM);
   if (ntm * ntn > INT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((fp8_gemm_rows_kernel<FA, FB, ROWB, FM, KS>), dim3((unsigned)(ntm * ntn)), dim3(64 * KS), 0, s, g);
+  const dim3 grid((unsigned)(ntm * ntn)), wg(64 * KS);
+  if (g.bf16_out) hipLaunchKernelGGL((fp8_gemm_rows_kernel<FA, FB, ROWB, false, FM, KS>), grid, wg, 0, s, g);
+  else hipLaunchKernelGGL((fp8_gemm_rows_kernel<FA, FB, ROWB, true, FM, KS>), grid, wg, 0, s, g);
   return hipGetLastError();
 }
 
@@ -780,10 +839,14 @@ hipError_t run(const Fp8Gemm& g, hipStream_t s) {
       return two ? run_rows<FA, FB, true, 2, 4>(g, s) : run_rows<FA, FB, true, 1, 4>(g, s);
     return two ? run_rows<FA, FB, false, 2, 4>(g, s) : run_rows<FA, FB, false, 1, 4>(g, s);
   }
+  // fp32 results: the widened fragments fit beside the small tile's accumulators only
+  if (!g.bf16_out)
+    return g.b_block == 1 ? run_tile<FA, FB, true, true, Tile128>(g, s) : run_tile<FA, FB, false, true, Tile128>(g, s);
   // Time of a round of 256 large tiles : of 512 small ones (two a CU) = 5 : 3 (65 and 39 us at K 4096).
   const bool large = (tiles(256) + 255) / 256 * 5 <= (tiles(128) + 511) / 512 * 3;
-  if (g.b_block == 1) return large ? run_tile<FA, FB, true, Tile256>(g, s) : run_tile<FA, FB, true, Tile128>(g, s);
-  return large ? run_tile<FA, FB, false, Tile256>(g, s) : run_tile<FA, FB, false, Tile128>(g, s);
+  if (g.b_block == 1)
+    return large ? run_tile<FA, FB, true, false, Tile256>(g, s) : run_tile<FA, FB, true, false, Tile128>(g, s);
+  return large ? run_tile<FA, FB, false, false, Tile256>(g, s) : run_tile<FA, FB, false, false, Tile128>(g, s);
 }
 
 }  // namespace

@@ -1,0 +1,100 @@
+"""A mixture-of-experts FFN in 8-bit floating point over the library's calls.
+
+"To 2:4 Sparsity and Beyond" (abstract) states that its FFN method is orthogonal to quantisation and
+applies to mixture-of-experts; this module is the mixture-of-experts FFN itself, each expert the up-
+projection, ReLU and down-projection of the framework's FFN:
+
+    y[t] = sum_j w[t, j] W_down[e_j] relu(W_up[e_j] x[t]),   (e, w) = moe_route(logits)
+
+It only sequences the library's calls (and torch allocations); nothing here computes on tensors.
+
+    python -c "from sparse_matmul_ffns_amd import moe; moe.main()"
+
+runs one forward and backward pass of a layer of 64 experts and prints its time.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import nmsparse as _nm
+
+
+class ExpertFFN:
+    """The experts' weights W_up [E, F, D] and W_down [E, D, F] (bf16 or fp32, device) held in 8 bits,
+    and the calls of a forward and a backward pass.
+
+    `train` keeps the weights' transposed bytes too, orders the rows by expert in runs of 128 (what the
+    weight gradients' blocks need) and saves what backward() reads; without it a pass keeps nothing.
+    Routing options as for moe_route; activations and weights are e4m3, gradients `grad_fmt`."""
+
+    def __init__(self, W_up: torch.Tensor, W_down: torch.Tensor, k: int, score: str = "softmax", bias=None,
+                 groups: int = 1, topk_groups: int = 1, group_top: int = 2, renorm: bool = True, scale: float = 1.0,
+                 train: bool = False, grad_fmt: torch.dtype = torch.float8_e5m2):
+        E, F, D = W_up.shape
+        if tuple(W_down.shape) != (E, D, F):
+            raise ValueError("W_up must be [E, F, D] and W_down [E, D, F]")
+        self.E, self.k, self.train, self.grad_fmt = E, k, train, grad_fmt
+        self.choice = dict(bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)
+        self.score = dict(score=score, renorm=renorm, scale=scale)
+        self.saved = None
+        self.set_weights(W_up, W_down)
+
+    def set_weights(self, W_up: torch.Tensor, W_down: torch.Tensor) -> None:
+        """Quantise the weights (again, after an optimizer step)."""
+        self.up = _nm.fp8_quantize_weight(W_up, transposed=self.train)
+        self.down = _nm.fp8_quantize_weight(W_down, transposed=self.train)
+
+    def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+        """y [T, D] of tokens x [T, D] (bf16) and router logits [T, E]."""
+        ids, w = _nm.moe_route(logits, self.k, **self.choice, **self.score)
+        offsets, _, src, pos = _nm.moe_plan(ids, self.E, align=128 if self.train else 1)
+        q, s = _nm.fp8_quantize(x, src=src, div=self.k)
+        h = _nm.fp8_gemm_nt_grouped(q, s, self.up[0], self.up[1], offsets, out_dtype=x.dtype)
+        q, s = _nm.fp8_quantize(h, gate=h)
+        o = _nm.fp8_gemm_nt_grouped(q, s, self.down[0], self.down[1], offsets, out_dtype=x.dtype)
+        if self.train:
+            self.saved = (x, logits, ids, w, offsets, src, pos, h, o)
+        return _nm.moe_combine(o, pos, w)
+
+    def backward(self, dy: torch.Tensor):
+        """Gradients of the last forward pass: (dx [T, D], dlogits [T, E], dW_up [E, F, D] and dW_down
+        [E, D, F] in fp32)."""
+        if self.saved is None:
+            raise RuntimeError("backward() needs a forward pass with train=True")
+        x, logits, ids, w, offsets, src, pos, h, o = self.saved
+        g = self.grad_fmt
+        do, dw = _nm.moe_combine_bwd(dy, o, src, pos, w)
+        dlogits = _nm.moe_route_bwd(logits, ids, w, dw, **self.score)
+        q, s = _nm.fp8_quantize(do, g)
+        dh = _nm.fp8_gemm_nt_grouped(q, s, self.down[2], self.down[3], offsets, out_dtype=x.dtype)
+        dW_down = _nm.fp8_gemm_nt_grouped_k(*_nm.fp8_quantize_t(do, g), *_nm.fp8_quantize_t(h, gate=h), offsets)
+        q, s = _nm.fp8_quantize(dh, g, gate=h)
+        dx = _nm.moe_combine(_nm.fp8_gemm_nt_grouped(q, s, self.up[2], self.up[3], offsets, out_dtype=x.dtype), pos)
+        dW_up = _nm.fp8_gemm_nt_grouped_k(*_nm.fp8_quantize_t(dh, g, gate=h),
+                                          *_nm.fp8_quantize_t(x, src=src, div=self.k), offsets)
+        return dx, dlogits, dW_up, dW_down
+
+
+def main(tokens: int = 4096) -> None:
+    E, D, F, k = 64, 2048, 1024, 8
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *shape, std=1.0: (torch.randn(*shape, generator=gen, device="cuda") * std).bfloat16()
+    layer = ExpertFFN(rand(E, F, D, std=0.02), rand(E, D, F, std=0.02), k, train=True)
+    x, dy, logits = rand(tokens, D), rand(tokens, D), rand(tokens, E).float()
+    times = []
+    for _ in range(5):
+        marks = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+        marks[0].record()
+        y = layer.forward(x, logits)
+        marks[1].record()
+        grads = layer.backward(dy)
+        marks[2].record()
+        torch.cuda.synchronize()
+        times.append((marks[0].elapsed_time(marks[1]), marks[1].elapsed_time(marks[2])))
+    fwd, bwd = (min(t) for t in zip(*times))
+    assert all(bool(torch.isfinite(t).all()) for t in (y, *grads))
+    flops = 4 * tokens * k * D * F
+    print(f"{tokens} tokens, {k} of {E} experts, {D} x {F}: forward {fwd:.3f} ms ({flops / fwd / 1e9:.0f} TFLOP/s), "
+          f"backward {bwd:.3f} ms ({2 * flops / bwd / 1e9:.0f} TFLOP/s)")
+

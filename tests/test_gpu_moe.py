@@ -4,9 +4,10 @@ Tolerances, from the arithmetic: routing weights are quotients of fp32 exponenti
 differences |l - max| < 64 (relative error below 64 * 2^-24 * 2 in each) and sums of at most 1024 terms
 in at most 26 rounded steps: 1e-5 relative.  The gradient's terms are products of those: 2e-5 of the sum
 of their magnitudes, plus half a unit in the last place of a bf16 result (2^-8 relative).  An 8-bit
-product adds 128 terms in the matrix instruction, each aligned to the block's largest, which keeps at
-least 12 bits below it per term, then scales and adds fp32 blocks: |C - C*| <= 2^-12 sum_kb (|A| |B|)_kb,
-plus half a unit of a bf16 result; products of small integers are exact.  Quantisation, orders and ids
+product with a bf16 result adds 128 terms in the matrix instruction, each aligned to the block's largest,
+which keeps at least 12 bits below it per term, then scales and adds fp32 blocks: |C - C*| <= 2^-12
+sum_kb (|A| |B|)_kb plus half a unit of the result.  With an fp32 result the 128 products and their sums
+are fp32: 128 * 2^-24 + (blocks + 2) * 2^-24 of sum_kb (|A| |B|)_kb.  Products of small integers are exact.  Quantisation, orders and ids
 are exact.  The combine adds k <= 64 fp32 products: 64 * 2^-24 of the sum of magnitudes.
 """
 
@@ -291,11 +292,11 @@ def _ref(A, B, lo=0, hi=None):
     return A @ B.T, np.abs(A) @ np.abs(B).T
 
 
-def _check_product(got, ref, mag, dtype, kind, what):
+def _check_product(got, ref, mag, dtype, kind, what, blocks=64):
     if kind == "ints" and dtype == "f32":
         assert np.array_equal(got, ref), what
     else:
-        tol = mag * 2.0 ** -12 + half_ulp(ref, dtype) + 1e-30
+        tol = mag * (2.0 ** -12 if dtype == "bf16" else (130 + blocks) * 2.0 ** -24) + half_ulp(ref, dtype) + 1e-30
         assert (np.abs(got - ref) <= tol).all(), (what, (np.abs(got - ref) / tol).max())
 
 
@@ -320,6 +321,29 @@ def test_gemm(M, N, K, fa, fb):
         C = nm.fp8_gemm_nt(fp8_dev(qa, fa, pad, off), dev(sa)[0], fp8_dev(qb, fb, pad, off), dev(sb)[0], b_block=block,
                            out_dtype=TD[out])
         _check_product(host(C), *_ref(a, b), out, kind, (kind, out, block, pad, off))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("fa", ["e4m3", "e5m2"])
+def test_gemm_many_stages_and_tiles(fa, block, out):
+    """Hundreds of workgroups over 64 stages whose scales differ from stage to stage: a scale or an operand
+    read after its buffer was refilled changes integers that are compared exactly (bf16: powers of two
+    small enough that the sums are within 2^-8)."""
+    rng = np.random.default_rng(9)
+    M, N, K = 2048, 2304, 8192
+    qa, qb = _bytes(rng, M, K, fa, "ints"), _bytes(rng, N, K, "e4m3", "ints")
+    sa = _scale_of(rng, (K // 128, M), "ints")
+    sb = _scale_of(rng, (K // 128, N) if block == 1 else (N // 128, K // 128), "ints")
+    a, b = MO.values_rows(qa, sa, fa), MO.values_rows(qb, sb, "e4m3") if block == 1 else MO.values_blocks(qb, sb, "e4m3")
+    ref = (torch.from_numpy(a).cuda() @ torch.from_numpy(b).cuda().t()).cpu().numpy()
+    args = fp8_dev(qa, fa), dev(sa)[0], fp8_dev(qb, "e4m3"), dev(sb)[0]
+    for _ in range(3):
+        C = host(nm.fp8_gemm_nt(*args, b_block=block, out_dtype=TD[out]))
+        if out == "f32":
+            assert np.array_equal(C, ref)
+        else:
+            assert (np.abs(C - ref) <= np.abs(ref) * 2.0 ** -8).all()
 
 
 def test_gemm_strided_output_and_scales():

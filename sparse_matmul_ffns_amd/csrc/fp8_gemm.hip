@@ -402,8 +402,8 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
       const int wg = xcd_remap(blockIdx.x, gridDim.x);
       t.e = wg / (ntm * ntn);
       const int within = wg % (ntm * ntn);
-      tm = within % ntm;
-      tn = within / ntm;
+      tm = within / ntn;
+      tn = within % ntn;
       t.kb0 = clamp_off(g.offsets[t.e], g.K) / 128;
       t.kb1 = clamp_off(g.offsets[t.e + 1], g.K) / 128;
     } else {

@@ -615,10 +615,19 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
     for (int i = 0; i < FM; ++i) a[i] = frag(0, a_row + i * 2048);
 #pragma unroll
     for (int d = 0; d < D; ++d) b[d] = frag(0, b_row + d * 2048);
-    for (int kt = 0; kt < KT; ++kt) stage(kt);
-    wait_vmcnt<0>();   // no load may land in LDS after the workgroup ends
+    if (t.m0 + wm < t.m_end) {
+      for (int kt = 0; kt < KT; ++kt) stage(kt);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) scale(i, FN - 1, s);
+      for (int i = 0; i < FM; ++i) scale(i, FN - 1, s);
+    } else {
+      // a wave whose rows lie behind the group's last (a group's partial tile) only loads
+      for (int kt = 0; kt < KT; ++kt) {
+        land(kt + 1);
+#pragma unroll
+        for (int q = 0; q <= Cfg::LOADS; ++q) dma(kt + 2, q);
+      }
+    }
+    wait_vmcnt<0>();   // no load may land in LDS after the workgroup ends
   }
 
   const int64_t crow = (g.mode == G_RED ? (int64_t)t.e * g.M : 0) + t.m0 + wm;

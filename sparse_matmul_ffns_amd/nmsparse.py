@@ -655,9 +655,10 @@ def _up(n: int, m: int) -> int:
 def _ld(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor whose rows are contiguous; strides of dimensions of one element are
     whatever torch left there and do not count."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+    stride = t.stride()
+    if len(stride) != 2 or (stride[1] != 1 and t.shape[1] != 1):
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return stride[0] if t.shape[0] > 1 else max(stride[0], t.shape[1])
 
 
 def _fp8(t: torch.Tensor, name: str) -> int:
@@ -693,11 +694,11 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, g
     if bias is not None:
         _of(bias, (E,), torch.float32, "bias")
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        ids = logits.new_empty((T, k), dtype=torch.int32)
     else:
         _of(ids, (T, k), torch.int32, "ids")
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        weights = logits.new_empty((T, k), dtype=torch.float32)
     else:
         _of(weights, (T, k), torch.float32, "weights")
     _check(lib().moe_route(_dt(logits), _p(logits), ldl, T, E, _score(score), _p(bias), groups, topk_groups, group_top,
@@ -717,8 +718,8 @@ def moe_route_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     _of(ids, (T, k), torch.int32, "ids"), _of(weights, (T, k), torch.float32, "weights")
     _of(dweights, (T, k), torch.float32, "dweights")
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    if tuple(dlogits.shape) != (T, E) or dlogits.dtype != logits.dtype:
+        dlogits = logits.new_empty((T, E))
+    elif dlogits.shape != (T, E) or dlogits.dtype != logits.dtype:
         raise ValueError("dlogits must be [T, E] with the logits' dtype")
     _check(lib().moe_route_bwd(_dt(logits), _p(logits), ldl, T, E, _score(score), k, int(bool(renorm)), scale, _p(ids),
                                _p(weights), _p(dweights), _p(dlogits), _ld(dlogits, "dlogits"), _stream()),
@@ -747,28 +748,23 @@ def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=Non
         raise ValueError("ids must be [T, k]")
     T, k = ids.shape
     _of(ids, (T, k), torch.int32, "ids")
-    dev = ids.device
-    if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    if offsets is None and counts is None and src is None and pos is None:
+        # one allocation, four contiguous parts: a call for one token, 8 of 64 experts, is bound by the host
+        parts = [E + 1, E, T * k, moe_plan_rows(T * k, E, align)]
+        offsets, counts, pos, src = ids.new_empty(sum(parts)).split_with_sizes(parts)
+        pos = pos.view(T, k)
     else:
-        _of(offsets, (E + 1,), torch.int32, "offsets")
-    if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
-    else:
-        _of(counts, (E,), torch.int32, "counts")
-    if src is None:
-        src = torch.empty(moe_plan_rows(T * k, E, align), dtype=torch.int32, device=dev)
-    else:
-        _of(src, (src.numel(),), torch.int32, "src")
-    if pos is None:
-        pos = torch.empty((T, k), dtype=torch.int32, device=dev)
-    else:
-        _of(pos, (T, k), torch.int32, "pos")
+        offsets = ids.new_empty(E + 1) if offsets is None else offsets
+        counts = ids.new_empty(E) if counts is None else counts
+        src = ids.new_empty(moe_plan_rows(T * k, E, align)) if src is None else src
+        pos = ids.new_empty((T, k)) if pos is None else pos
+        _of(offsets, (E + 1,), torch.int32, "offsets"), _of(counts, (E,), torch.int32, "counts")
+        _of(src, (src.numel(),), torch.int32, "src"), _of(pos, (T, k), torch.int32, "pos")
     if isinstance(work, str):
         if work != "auto":
             raise ValueError("work must be a tensor, None or 'auto'")
         need = _plan_work_bytes(T, k, E)
-        work = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
+        work = ids.new_empty(need // 4) if need else None
     if work is not None:
         _dev(work)
         _flat(work, "work")
@@ -785,7 +781,7 @@ def _quantize_args(X, src, gate):
     if src is not None:
         R = src.numel()
         _of(src, (R,), torch.int32, "src")
-    if gate is not None and (tuple(gate.shape) != (R, K) or gate.dtype != X.dtype):
+    if gate is not None and (gate.shape != (R, K) or gate.dtype != X.dtype):
         raise ValueError("gate must be [rows, K] with X's dtype")
     return ldx, RX, R, K, 0 if gate is None else _ld(gate, "gate")
 
@@ -799,10 +795,10 @@ def fp8_quantize(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=No
     _dev(Q, S)
     Kp = _up(K, 128)
     if Q is None:
-        Q = torch.empty((R, Kp), dtype=fmt, device=X.device)
+        Q = X.new_empty((R, Kp), dtype=fmt)
     if S is None:
-        S = torch.empty((Kp // 128, R), dtype=torch.float32, device=X.device)
-    if tuple(Q.shape) != (R, Kp) or tuple(S.shape) != (Kp // 128, R) or S.dtype != torch.float32:
+        S = X.new_empty((Kp // 128, R), dtype=torch.float32)
+    if Q.shape != (R, Kp) or S.shape != (Kp // 128, R) or S.dtype != torch.float32:
         raise ValueError("Q must be [rows, Kp] and S an fp32 [Kp / 128, rows] tensor")
     _check(lib().fp8_quantize(_dt(X), _p(X), ldx, RX, _p(src), div, _p(gate), ldg, R, K, _fp8(Q, "Q"), _p(Q),
                               _ld(Q, "Q"), _p(S), _ld(S, "S"), _stream()), "fp8_quantize")
@@ -817,10 +813,10 @@ def fp8_quantize_t(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=
     _dev(Q, S)
     Rp = _up(R, 128)
     if Q is None:
-        Q = torch.empty((K, Rp), dtype=fmt, device=X.device)
+        Q = X.new_empty((K, Rp), dtype=fmt)
     if S is None:
-        S = torch.empty((Rp // 128, K), dtype=torch.float32, device=X.device)
-    if tuple(Q.shape) != (K, Rp) or tuple(S.shape) != (Rp // 128, K) or S.dtype != torch.float32:
+        S = X.new_empty((Rp // 128, K), dtype=torch.float32)
+    if Q.shape != (K, Rp) or S.shape != (Rp // 128, K) or S.dtype != torch.float32:
         raise ValueError("Q must be [K, Rp] and S an fp32 [Rp / 128, K] tensor")
     _check(lib().fp8_quantize_t(_dt(X), _p(X), ldx, RX, _p(src), div, _p(gate), ldg, R, K, _fp8(Q, "Q"), _p(Q),
                                 _ld(Q, "Q"), _p(S), _ld(S, "S"), _stream()), "fp8_quantize_t")
@@ -851,10 +847,10 @@ def fp8_quantize_weight(W: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn,
     return tuple(t[0] for t in out) if W.dim() == 2 else out
 
 
-def _gemm_out(out, shape, out_dtype, dev):
+def _gemm_out(out, shape, out_dtype, sa):
     if out is None:
-        return torch.empty(shape, dtype=out_dtype, device=dev)
-    if tuple(out.shape) != tuple(shape):
+        return sa.new_empty(shape, dtype=out_dtype)
+    if out.shape != shape:
         raise ValueError(f"out must be {list(shape)}")
     return out
 
@@ -879,7 +875,7 @@ def fp8_gemm_nt(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Te
     if b_block not in (1, 128):
         raise ValueError("b_block must be 1 or 128")
     Kb = _up(K, 128) // 128
-    out = _gemm_out(out, (M, N), out_dtype, A.device)
+    out = _gemm_out(out, (M, N), out_dtype, sa)
     ldsa = _scales(sa, (Kb, M), "sa")
     ldsb = _scales(sb, (Kb, N) if b_block == 1 else (_up(N, 128) // 128, Kb), "sb")
     _check(lib().fp8_gemm_nt(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), ldsa, _fp8(B, "B"), _p(B), _ld(B, "B"),
@@ -902,7 +898,7 @@ def fp8_gemm_nt_grouped(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: 
     if (B.stride(2) != 1 and K > 1) or (E > 1 and B.stride(0) != N * ldb):
         raise ValueError("B must have contiguous rows and evenly spaced experts")
     _of(offsets, (E + 1,), torch.int32, "offsets"), _of(sb, (E, Nb, Kb), torch.float32, "sb")
-    out = _gemm_out(out, (rows, N), out_dtype, A.device)
+    out = _gemm_out(out, (rows, N), out_dtype, sa)
     _check(lib().fp8_gemm_nt_grouped(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), _scales(sa, (Kb, rows), "sa"),
                                      _fp8(B, "B"), _p(B), ldb, _p(sb), Kb, _p(offsets), E, rows, N, K, _dt(out), _p(out),
                                      _ld(out, "out"), _stream()), "fp8_gemm_nt_grouped")
@@ -922,7 +918,7 @@ def fp8_gemm_nt_grouped_k(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb
     E = offsets.numel() - 1
     _of(offsets, (E + 1,), torch.int32, "offsets")
     Rb = _up(rows, 128) // 128
-    out = _gemm_out(out, (E, M, N), out_dtype, A.device)
+    out = _gemm_out(out, (E, M, N), out_dtype, sa)
     _flat(out, "out")
     _check(lib().fp8_gemm_nt_grouped_k(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), _scales(sa, (Rb, M), "sa"),
                                        _fp8(B, "B"), _p(B), _ld(B, "B"), _p(sb), _scales(sb, (Rb, N), "sb"),
@@ -942,8 +938,8 @@ def moe_combine(O: torch.Tensor, pos: torch.Tensor, weights=None, out=None) -> t
     if weights is not None:
         _of(weights, (T, k), torch.float32, "weights")
     if out is None:
-        out = torch.empty((T, D), dtype=O.dtype, device=O.device)
-    if tuple(out.shape) != (T, D) or out.dtype != O.dtype:
+        out = O.new_empty((T, D))
+    elif out.shape != (T, D) or out.dtype != O.dtype:
         raise ValueError("out must be [T, D] with O's dtype")
     _check(lib().moe_combine(_dt(O), _p(O), _ld(O, "O"), rows, _p(pos), _p(weights), T, k, D, _p(out),
                              _ld(out, "out"), _stream()), "moe_combine")
@@ -958,17 +954,17 @@ def moe_combine_bwd(dY: torch.Tensor, O: torch.Tensor, src: torch.Tensor, pos: t
     if pos.dim() != 2:
         raise ValueError("pos must be [T, k]")
     T, k = pos.shape
-    if tuple(dY.shape) != (T, D) or dY.dtype != O.dtype:
+    if dY.shape != (T, D) or dY.dtype != O.dtype:
         raise ValueError("dY must be [T, D] with O's dtype")
     _of(src, (rows,), torch.int32, "src"), _of(pos, (T, k), torch.int32, "pos")
     _of(weights, (T, k), torch.float32, "weights")
     if dO is None:
-        dO = torch.empty((rows, D), dtype=O.dtype, device=O.device)
+        dO = O.new_empty((rows, D))
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=O.device)
+        dweights = O.new_empty((T, k), dtype=torch.float32)
     else:
         _of(dweights, (T, k), torch.float32, "dweights")
-    if tuple(dO.shape) != (rows, D) or dO.dtype != O.dtype:
+    if dO.shape != (rows, D) or dO.dtype != O.dtype:
         raise ValueError("dO must be [rows, D] with O's dtype")
     _check(lib().moe_combine_bwd(_dt(O), _p(dY), _ld(dY, "dY"), _p(O), _ld(O, "O"), rows, _p(src), _p(pos),
                                  _p(weights), T, k, D, _p(dO), _ld(dO, "dO"), _p(dweights), _stream()),

@@ -665,7 +665,9 @@ nm_status fp8_quantize_weight(nm_dtype dt, const void* W, int64_t ldw, int64_t E
  *   B [N][ldb] format fb; sb by blocks (b_block 128): [ceil(N / 128)][ldsb], ldsb >= ceil(K / 128),
  *     or by rows (b_block 1): [ceil(K / 128)][ldsb], ldsb >= N
  *   C [M][ldc] fp32 or bf16 (out)
- * Each 128-block's sum is scaled and added in fp32; the result is rounded once.  The sum itself:
+ * Each 128-block's sum is scaled and added in fp32; the result is rounded once.  The product of a block's
+ * two scales is formed first, in fp32, and has to be finite (scales of magnitude below 2^64 always
+ * do; an infinite product gives NaN where the sum is 0).  The sum itself:
  *   out NM_F32   products and sums are fp32.
  *   out NM_BF16  the 8-bit matrix instruction.  Of every eight products k = 8 i .. 8 i + 7 each is cut
  *     towards zero to a multiple of 2^-13 u, u the largest 2^(ea + eb) among the eight that are not 0

@@ -542,8 +542,10 @@ __global__ __launch_bounds__(Cfg::NT, 2) void fp8_gemm_tile_kernel(Fp8Gemm g) {
   auto scale = [&](int i, int j, const float (&sc_)[FM]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float v = ROWB ? p[j & 1][i][q] * (j < FN - D ? sn[q] : late[j < FN - D ? 0 : j - (FN - D)][q]) : p[j & 1][i][q];
-      acc[i][j][q] = __builtin_fmaf(v, sc_[i], acc[i][j][q]);
+      // the block's scale is formed first, as in the other kernels: a sum times one scale alone can pass
+      // fp32's range where the result does not
+      const float f = ROWB ? sc_[i] * (j < FN - D ? sn[q] : late[j < FN - D ? 0 : j - (FN - D)][q]) : sc_[i];
+      acc[i][j][q] = __builtin_fmaf(p[j & 1][i][q], f, acc[i][j][q]);
     }
     asm volatile("" : "+v"(acc[i][j]));   // here, not sunk to the end of the loop
   };

@@ -31,22 +31,30 @@ class ExpertFFN:
     def __init__(self, W_up: torch.Tensor, W_down: torch.Tensor, k: int, score: str = "softmax", bias=None,
                  groups: int = 1, topk_groups: int = 1, group_top: int = 2, renorm: bool = True, scale: float = 1.0,
                  train: bool = False, grad_fmt: torch.dtype = torch.float8_e5m2):
-        E, F, D = W_up.shape
-        if tuple(W_down.shape) != (E, D, F):
-            raise ValueError("W_up must be [E, F, D] and W_down [E, D, F]")
-        self.E, self.k, self.train, self.grad_fmt = E, k, train, grad_fmt
+        if W_up.dim() != 3:
+            raise ValueError("W_up must be [E, F, D]")
+        self.E, self.F, self.D = W_up.shape
+        self.k, self.train, self.grad_fmt = k, train, grad_fmt
         self.choice = dict(bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)
         self.score = dict(score=score, renorm=renorm, scale=scale)
         self.saved = None
         self.set_weights(W_up, W_down)
 
     def set_weights(self, W_up: torch.Tensor, W_down: torch.Tensor) -> None:
-        """Quantise the weights (again, after an optimizer step)."""
+        """Quantise the weights (again, after an optimizer step); their shapes stay those of the layer."""
+        E, F, D = self.E, self.F, self.D
+        if tuple(W_up.shape) != (E, F, D) or tuple(W_down.shape) != (E, D, F):
+            raise ValueError(f"W_up must be [E, F, D] = {[E, F, D]} and W_down [E, D, F]")
         self.up = _nm.fp8_quantize_weight(W_up, transposed=self.train)
         self.down = _nm.fp8_quantize_weight(W_down, transposed=self.train)
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """y [T, D] of tokens x [T, D] (bf16) and router logits [T, E]."""
+        # the products pad D to 128 and the plan drops choices of no expert: neither would notice
+        if x.dim() != 2 or x.shape[1] != self.D:
+            raise ValueError(f"x must be [T, {self.D}]")
+        if logits.shape != (x.shape[0], self.E):
+            raise ValueError(f"logits must be [T, {self.E}] with x's number of tokens")
         ids, w = _nm.moe_route(logits, self.k, **self.choice, **self.score)
         offsets, _, src, pos = _nm.moe_plan(ids, self.E, align=128 if self.train else 1)
         q, s = _nm.fp8_quantize(x, src=src, div=self.k)

@@ -20,12 +20,20 @@ import torch
 from . import nmsparse as _nm
 
 
+def _version(t: torch.Tensor):
+    """torch's count of the in-place changes of t (tensors made in inference mode have none)."""
+    return None if t.is_inference() else t._version
+
+
 class ExpertFFN:
     """The experts' weights W_up [E, F, D] and W_down [E, D, F] (bf16 or fp32, device) held in 8 bits,
     and the calls of a forward and a backward pass.
 
     `train` keeps the weights' transposed bytes too, orders the rows by expert in runs of 128 (what the
     weight gradients' blocks need) and saves what backward() reads; without it a pass keeps nothing.
+    The layer keeps the last pass only, and with it x and logits themselves, not copies.  Passes that wait
+    for their gradients together (micro-batches, threads) are kept by the caller: forward(...,
+    return_saved=True) and backward(dy, saved).
     Routing options as for moe_route; activations and weights are e4m3, gradients `grad_fmt`."""
 
     def __init__(self, W_up: torch.Tensor, W_down: torch.Tensor, k: int, score: str = "softmax", bias=None,
@@ -38,6 +46,8 @@ class ExpertFFN:
         self.choice = dict(bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)
         self.score = dict(score=score, renorm=renorm, scale=scale)
         self.saved = None
+        self.used = self.replaced = False   # the saved pass has had a backward pass; it replaced one that had none
+        self.generation = 0                 # of the weights
         self.set_weights(W_up, W_down)
 
     def set_weights(self, W_up: torch.Tensor, W_down: torch.Tensor) -> None:
@@ -45,11 +55,15 @@ class ExpertFFN:
         E, F, D = self.E, self.F, self.D
         if tuple(W_up.shape) != (E, F, D) or tuple(W_down.shape) != (E, D, F):
             raise ValueError(f"W_up must be [E, F, D] = {[E, F, D]} and W_down [E, D, F]")
+        self.generation += 1
         self.up = _nm.fp8_quantize_weight(W_up, transposed=self.train)
         self.down = _nm.fp8_quantize_weight(W_down, transposed=self.train)
 
-    def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
-        """y [T, D] of tokens x [T, D] (bf16) and router logits [T, E]."""
+    def forward(self, x: torch.Tensor, logits: torch.Tensor, return_saved: bool = False):
+        """y [T, D] of tokens x [T, D] (bf16) and router logits [T, E]; with `return_saved` (y, what
+        backward() reads), and the layer itself keeps nothing of the pass."""
+        if return_saved and not self.train:
+            raise ValueError("return_saved needs a layer with train=True")
         # the products pad D to 128 and the plan drops choices of no expert: neither would notice
         if x.dim() != 2 or x.shape[1] != self.D:
             raise ValueError(f"x must be [T, {self.D}]")
@@ -61,16 +75,35 @@ class ExpertFFN:
         h = _nm.fp8_gemm_nt_grouped(q, s, self.up[0], self.up[1], offsets, out_dtype=x.dtype)
         q, s = _nm.fp8_quantize(h, gate=h)
         o = _nm.fp8_gemm_nt_grouped(q, s, self.down[0], self.down[1], offsets, out_dtype=x.dtype)
-        if self.train:
-            self.saved = (x, logits, ids, w, offsets, src, pos, h, o)
-        return _nm.moe_combine(o, pos, w)
+        y = _nm.moe_combine(o, pos, w)
+        if not self.train:
+            return y
+        saved = (x, logits, ids, w, offsets, src, pos, h, o, self.generation, _version(x), _version(logits))
+        if return_saved:
+            return y, saved
+        self.replaced = self.saved is not None and not self.used
+        self.saved, self.used = saved, False
+        return y
 
-    def backward(self, dy: torch.Tensor):
-        """Gradients of the last forward pass: (dx [T, D], dlogits [T, E], dW_up [E, F, D] and dW_down
-        [E, D, F] in fp32)."""
-        if self.saved is None:
-            raise RuntimeError("backward() needs a forward pass with train=True")
-        x, logits, ids, w, offsets, src, pos, h, o = self.saved
+    def backward(self, dy: torch.Tensor, saved=None):
+        """Gradients of the last forward pass, or of the one that returned `saved`: (dx [T, D], dlogits
+        [T, E], dW_up [E, F, D] and dW_down [E, D, F] in fp32).
+
+        Refused (RuntimeError): a second backward() of a pass that took the place of one without
+        a backward pass, as two forwards and then two backwards make it; x, logits (as torch sees it) or
+        the weights changed since the pass."""
+        if saved is None:
+            saved = self.saved
+            if saved is None:
+                raise RuntimeError("backward() needs a forward pass with train=True")
+            if self.used and self.replaced:
+                raise RuntimeError("the layer keeps the last pass only, and an earlier one had no backward(): keep the "
+                                   "passes with forward(..., return_saved=True) and give each to backward(dy, saved)")
+        x, logits, ids, w, offsets, src, pos, h, o, generation, *versions = saved
+        if generation != self.generation:
+            raise RuntimeError("the weights have been set since this forward pass")
+        if versions != [_version(x), _version(logits)]:
+            raise RuntimeError("x or logits has been changed in place since this forward pass")
         g = self.grad_fmt
         do, dw = _nm.moe_combine_bwd(dy, o, src, pos, w)
         dlogits = _nm.moe_route_bwd(logits, ids, w, dw, **self.score)
@@ -81,6 +114,8 @@ class ExpertFFN:
         dx = _nm.moe_combine(_nm.fp8_gemm_nt_grouped(q, s, self.up[2], self.up[3], offsets, out_dtype=x.dtype), pos)
         dW_up = _nm.fp8_gemm_nt_grouped_k(*_nm.fp8_quantize_t(dh, g, gate=h),
                                           *_nm.fp8_quantize_t(x, src=src, div=self.k), offsets)
+        if saved is self.saved:
+            self.used = True
         return dx, dlogits, dW_up, dW_down
 
 

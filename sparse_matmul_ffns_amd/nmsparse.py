@@ -857,7 +857,7 @@ def _gemm_out(out, shape, out_dtype, sa):
 
 def _scales(s: torch.Tensor, shape, name: str) -> int:
     """Row stride of fp32 scales of at least the given shape."""
-    if s.dtype != torch.float32 or s.shape[0] != shape[0] or s.shape[1] < shape[1]:
+    if s.dtype != torch.float32 or s.dim() != 2 or s.shape[0] != shape[0] or s.shape[1] < shape[1]:
         raise ValueError(f"{name} must be an fp32 tensor of shape {list(shape)}")
     return _ld(s, name)
 
@@ -869,9 +869,9 @@ def fp8_gemm_nt(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Te
     row (b_block 1).  C is bf16 or fp32."""
     _dev(A, sa, B, sb, out)
     M, K = A.shape
+    if B.dim() != 2 or B.shape[1] != K:
+        raise ValueError("A and B must be 2-D with the same number of columns")
     N = B.shape[0]
-    if B.shape[1] != K:
-        raise ValueError("A and B must have the same number of columns")
     if b_block not in (1, 128):
         raise ValueError("b_block must be 1 or 128")
     Kb = _up(K, 128) // 128
@@ -912,10 +912,12 @@ def fp8_gemm_nt_grouped_k(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb
     128 (moe_plan with align 128)."""
     _dev(A, sa, B, sb, offsets, out)
     M, rows = A.shape
+    if B.dim() != 2 or B.shape[1] != rows:
+        raise ValueError("A and B must be 2-D with the same number of columns")
     N = B.shape[0]
-    if B.shape[1] != rows:
-        raise ValueError("A and B must have the same number of columns")
     E = offsets.numel() - 1
+    if E < 1:
+        raise ValueError("offsets must have an entry for every expert and one more")
     _of(offsets, (E + 1,), torch.int32, "offsets")
     Rb = _up(rows, 128) // 128
     out = _gemm_out(out, (E, M, N), out_dtype, sa)

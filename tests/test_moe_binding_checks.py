@@ -42,3 +42,12 @@ def test_products_refuse_other_ranks(bad):
                 call(**dict(args, **{bad: other}))
     with pytest.raises(AssertionError):
         nm.fp8_gemm_nt(**good)
+
+
+@pytest.mark.parametrize("bad", ["sa", "sb"])
+def test_scales_of_one_dimension(bad):
+    """As many entries as the scales have rows."""
+    args = dict(A=_q(4, 256), sa=torch.ones(2, 4), B=_q(128, 256), sb=torch.ones(2, 128), b_block=1)
+    args[bad] = torch.ones(2)
+    with pytest.raises(ValueError):
+        nm.fp8_gemm_nt(**args)

@@ -623,7 +623,8 @@ nm_status moe_plan_work_bytes(int64_t T, int k, int64_t E, int64_t* bytes);
  * fp8_quantize -- rows to 8 bits in blocks of 128 along K, with a power-of-two scale:
  *   x[r][c] = X[src[r] / div][c] (src NULL: X[r][c]); 0 where src[r] / div is not a row of X;
  *             0 where gate is given and gate[r][c] is not > 0 (gate = X: ReLU; gate = the
- *             forward's pre-activations: the gradient of ReLU)
+ *             forward's pre-activations: the gradient of ReLU); a NaN gate is not > 0, so ReLU
+ *             takes a NaN to 0, and keeps +infinity
  *   S[kb][r] = the smallest power of two (at least 2^-126) that is >= amax / 448 (e4m3) or
  *             amax / 57344 (e5m2), amax the largest finite |x| of the block; 1 when that is 0
  *   Q[r][c] = x[r][c] / S[kb][r] rounded to nearest even (the division is exact)

@@ -39,7 +39,7 @@ __device__ inline void store_row(T* p, int64_t c, int64_t D, bool vec, const flo
 }
 
 // One workgroup per token and run of blockDim.x * V columns, eight of the k rows' loads in flight.  Bound
-// by its bytes: 8192 tokens of 8 rows of 2048 bf16 (302 MB) in 56 us, 5.4 TB/s.
+// by its bytes: 8192 tokens of 8 rows of 2048 bf16 (302 MB) in 52 us, 5.8 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const T* __restrict__ O, int64_t ldo, int64_t rows,
                                                           const int32_t* __restrict__ pos, const float* __restrict__ w,
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const T* __restrict__ 
 // Workgroups 0 .. T-1: one token each: dY's row is read once for its k rows of dO and k dot products
 // (summed per thread, then over the wave and the four waves in a fixed order).  Workgroups from T
 // on: 16 rows of dO each, those of no slot are cleared.  Bound by its bytes: the same tokens (588 MB with
-// 4096 rows of padding) in 107 us, 5.5 TB/s.
+// 4096 rows of padding) in 104 us, 5.7 TB/s.
 constexpr int kPadRows = 16;
 template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_bwd_kernel(const T* __restrict__ dY, int64_t lddy,

@@ -741,8 +741,8 @@ def _plan_work_bytes(T: int, k: int, E: int) -> int:
 
 def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=None, src=None, pos=None, work="auto"):
     """The order of the T * k slots by expert: returns (offsets [E + 1], counts [E], src [rows], pos
-    [T, k]), int32.  `work`: an int32 device tensor, or "auto" (allocated with torch when the call uses
-    it)."""
+    [T, k]), int32, parts of one allocation when none is given.  `work`: an int32 device tensor, or "auto"
+    (allocated with torch when the call uses it)."""
     _dev(ids, offsets, counts, src, pos)
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")

@@ -7,6 +7,7 @@
 #include "common.hpp"
 #include "dma.hpp"
 #include "launch.hpp"
+#include "pieces.hpp"
 
 namespace nms {
 namespace {
@@ -349,6 +350,7 @@ hipError_t run_general(const Fp8Gemm& g, hipStream_t s) {
   const bool va = (uintptr_t)g.A % 16 == 0 && g.lda % 16 == 0, vb = (uintptr_t)g.B % 16 == 0 && g.ldb % 16 == 0;
   const int64_t ntn = (g.N + 63) / 64;
   const int64_t ntm = g.mode == G_ROWS ? most_row_tiles(g, 64) : (g.M + 63) / 64;
+  if (!grid_ok(ntm, 256)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)ntm, (unsigned)ntn, g.mode == G_RED ? g.E : 1);
   if (g.bf16_out) hipLaunchKernelGGL((fp8_gemm_general_kernel<FA, FB, false>), grid, dim3(256), 0, s, g, va, vb);
   else hipLaunchKernelGGL((fp8_gemm_general_kernel<FA, FB, true>), grid, dim3(256), 0, s, g, va, vb);
@@ -653,7 +655,7 @@ hipError_t run_tile(const Fp8Gemm& g, hipStream_t s) {
   int64_t wgs = ntm * ntn;
   if (g.mode == G_ROWS) wgs = (most_row_tiles(g, Cfg::BM) + 7) / 8 * 8 * ntn;
   if (g.mode == G_RED) wgs *= g.E;
-  if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (!grid_ok(wgs, Cfg::NT)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(Cfg::NT), Cfg::LDS, s, g);
   return hipGetLastError();
 }
@@ -825,7 +827,7 @@ template <int FA, int FB, bool ROWB, int FM, int KS>
 hipError_t run_rows(const Fp8Gemm& g, hipStream_t s) {
   const int64_t ntn = (g.N + 31) / 32;
   const int64_t ntm = g.mode == G_ROWS ? most_row_tiles(g, 16 * FM) : (g.M + 16 * FM - 1) / (16 * FM);
-  if (ntm * ntn > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (!grid_ok(ntm * ntn, 64 * KS)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(ntm * ntn)), wg(64 * KS);
   if (g.bf16_out) hipLaunchKernelGGL((fp8_gemm_rows_kernel<FA, FB, ROWB, false, FM, KS>), grid, wg, 0, s, g);
   else hipLaunchKernelGGL((fp8_gemm_rows_kernel<FA, FB, ROWB, true, FM, KS>), grid, wg, 0, s, g);
@@ -872,9 +874,21 @@ hipError_t run(const Fp8Gemm& g, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
+static hipError_t gemm_piece(const Fp8Gemm& g, hipStream_t s) {
   if (g.a_e5m2) return g.b_e5m2 ? run<1, 1>(g, s) : run<1, 0>(g, s);
   return g.b_e5m2 ? run<0, 1>(g, s) : run<0, 0>(g, s);
+}
+
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s) {
+  if (g.mode != G_DENSE) return gemm_piece(g, s);
+  return in_pieces(g.M, kPieceRows, [&](int64_t m0, int64_t n) {
+    Fp8Gemm p = g;
+    p.A += m0 * g.lda;
+    p.sa += m0;
+    p.M = n;
+    p.C = (uint8_t*)g.C + m0 * g.ldc * (g.bf16_out ? 2 : 4);
+    return gemm_piece(p, s);
+  });
 }
 
 }  // namespace nms

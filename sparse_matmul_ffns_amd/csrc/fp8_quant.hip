@@ -1,6 +1,7 @@
 // Quantisation to 8-bit floating point in blocks of 128 with a power-of-two scale.
 #include "fp8.hpp"
 #include "launch.hpp"
+#include "pieces.hpp"
 
 namespace nms {
 namespace {
@@ -328,7 +329,19 @@ static hipError_t quantize_columns(const QuantArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s) {
+// Rows r0 .. r0 + n - 1 of a.
+static QuantArgs rows_of(const QuantArgs& a, int es, int64_t r0, int64_t n) {
+  QuantArgs p = a;
+  if (a.src) p.src += r0;
+  else p.X = (const uint8_t*)a.X + r0 * a.ldx * es;
+  if (a.gate) p.gate = (const uint8_t*)a.gate + r0 * a.ldg * es;
+  p.R = n;
+  p.Q += r0 * a.ldq;
+  p.S += r0;
+  return p;
+}
+
+static hipError_t quantize_piece(int dt, const QuantArgs& a, hipStream_t s) {
   const bool vec = a.K % 8 == 0 && vec_ok(dt == DT_BF16 ? 2 : 4, a.X, a.ldx, a.gate, a.ldg);
   if (dt == DT_BF16) {
     if (a.e5m2) return vec ? quantize_rows<uint16_t, true, true>(a, s) : quantize_rows<uint16_t, true, false>(a, s);
@@ -336,6 +349,12 @@ hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s) {
   }
   if (a.e5m2) return vec ? quantize_rows<uint32_t, true, true>(a, s) : quantize_rows<uint32_t, true, false>(a, s);
   return vec ? quantize_rows<uint32_t, false, true>(a, s) : quantize_rows<uint32_t, false, false>(a, s);
+}
+
+hipError_t launch_fp8_quantize(int dt, const QuantArgs& a, hipStream_t s) {
+  return in_pieces(a.R, kPieceRows, [&](int64_t r0, int64_t n) {
+    return quantize_piece(dt, rows_of(a, dt == DT_BF16 ? 2 : 4, r0, n), s);
+  });
 }
 
 hipError_t launch_fp8_quantize_t(int dt, const QuantArgs& a, hipStream_t s) {
@@ -351,7 +370,9 @@ hipError_t launch_fp8_quantize_t(int dt, const QuantArgs& a, hipStream_t s) {
 hipError_t launch_fp8_quantize_weight(int dt, const void* W, int64_t ldw, int64_t E, int64_t N, int64_t K, int e5m2,
                                       uint8_t* Q, int64_t ldq, float* S, uint8_t* Qt, int64_t ldqt, float* St,
                                       hipStream_t s) {
-  const dim3 grid((unsigned)(((N + 127) / 128) * ((K + 127) / 128)), (unsigned)E);
+  const int64_t blocks = ((N + 127) / 128) * ((K + 127) / 128);
+  if (!grid_ok(blocks, 256)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)E);
   const int es = dt == DT_BF16 ? 2 : 4;
   const bool vec = vec_ok(es, W, ldw, nullptr, 0);
   auto go = [&](auto kern, auto* w) {

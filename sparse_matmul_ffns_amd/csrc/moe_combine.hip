@@ -1,6 +1,7 @@
 // The weighted sum of each token's expert rows, and its gradients.
 #include "common.hpp"
 #include "launch.hpp"
+#include "pieces.hpp"
 
 namespace nms {
 namespace {
@@ -153,9 +154,12 @@ hipError_t combine_t(const T* O, int64_t ldo, int64_t rows, const int32_t* pos, 
   const int64_t need = (D + V - 1) / V;
   const int nt = need <= 64 ? 64 : need <= 128 ? 128 : 256;
   const int64_t runs = (need + nt - 1) / nt;
-  hipLaunchKernelGGL(moe_combine_kernel<T>, dim3((unsigned)Tn, (unsigned)(runs < 65535 ? runs : 65535)), dim3(nt), 0, s,
-                     O, ldo, rows, pos, w, k, D, Y, ldy, vec_rows<T>(O, ldo) && vec_rows<T>(Y, ldy));
-  return hipGetLastError();
+  const bool vec = vec_rows<T>(O, ldo) && vec_rows<T>(Y, ldy);
+  return in_pieces(Tn, kPieceRows256, [&](int64_t t0, int64_t n) {
+    hipLaunchKernelGGL(moe_combine_kernel<T>, dim3((unsigned)n, (unsigned)(runs < 65535 ? runs : 65535)), dim3(nt), 0, s, O,
+                       ldo, rows, pos + t0 * k, w ? w + t0 * k : nullptr, k, D, Y + t0 * ldy, ldy, vec);
+    return hipGetLastError();
+  });
 }
 
 template <typename T>
@@ -163,10 +167,21 @@ hipError_t combine_bwd_t(const T* dY, int64_t lddy, const T* O, int64_t ldo, int
                          const int32_t* pos, const float* w, int64_t Tn, int k, int64_t D, T* dO, int64_t lddo, float* dw,
                          hipStream_t s) {
   const int64_t pads = (rows + kPadRows - 1) / kPadRows;
-  hipLaunchKernelGGL(moe_combine_bwd_kernel<T>, dim3((unsigned)(Tn + pads)), dim3(256), 0, s, dY, lddy, O, ldo, rows, src,
-                     pos, w, Tn, k, D, dO, lddo, dw,
-                     vec_rows<T>(dY, lddy) && vec_rows<T>(O, ldo) && vec_rows<T>(dO, lddo));
-  return hipGetLastError();
+  const bool vec = vec_rows<T>(dY, lddy) && vec_rows<T>(O, ldo) && vec_rows<T>(dO, lddo);
+  // the rows to clear go with the last tokens, unless those and they are too many for one launch
+  const bool together = pads <= kPieceRows256;
+  const hipError_t e = in_pieces(Tn, kPieceRows256, [&](int64_t t0, int64_t n) {
+    const int64_t clear = together && t0 + n == Tn ? pads : 0;
+    hipLaunchKernelGGL(moe_combine_bwd_kernel<T>, dim3((unsigned)(n + clear)), dim3(256), 0, s, dY + t0 * lddy, lddy, O, ldo,
+                       rows, src, pos + t0 * k, w + t0 * k, n, k, D, dO, lddo, dw + t0 * k, vec);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || together) return e;
+  return in_pieces(rows, kPieceRows256 * kPadRows, [&](int64_t r0, int64_t n) {
+    hipLaunchKernelGGL(moe_combine_bwd_kernel<T>, dim3((unsigned)((n + kPadRows - 1) / kPadRows)), dim3(256), 0, s, dY, lddy, O,
+                       ldo, n, src + r0, pos, w, (int64_t)0, k, D, dO + r0 * lddo, lddo, dw, vec);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace

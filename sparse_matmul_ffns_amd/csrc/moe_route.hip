@@ -2,6 +2,7 @@
 // (token, choice) slots by expert.
 #include "common.hpp"
 #include "launch.hpp"
+#include "pieces.hpp"
 
 namespace nms {
 namespace {
@@ -378,11 +379,23 @@ hipError_t run_route(const RouteArgs& a, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t route_t(const RouteArgs& a, hipStream_t s) {
+hipError_t route_piece(const RouteArgs& a, hipStream_t s) {
   if (a.k <= 16 && a.E <= 64) return run_route<T, 16, 4>(a, s);
   if (a.k <= 16 && a.E <= 256) return run_route<T, 16, 16>(a, s);
   if (a.E <= 256) return run_route<T, 64, 4>(a, s);
   return run_route<T, 64, 16>(a, s);
+}
+
+template <typename T>
+hipError_t route_t(const RouteArgs& a, hipStream_t s) {
+  return in_pieces(a.T, kPieceRows, [&](int64_t t0, int64_t n) {
+    RouteArgs p = a;
+    p.logits = (const T*)a.logits + t0 * a.ldl;
+    p.T = n;
+    p.ids += t0 * a.k;
+    p.weights += t0 * a.k;
+    return route_piece<T>(p, s);
+  });
 }
 
 template <typename T, int LPT, int EPL>
@@ -396,13 +409,22 @@ hipError_t run_bwd(const T* logits, int64_t ldl, int64_t Tn, int E, int sigmoid,
 }
 
 template <typename T>
-hipError_t bwd_t(const T* logits, int64_t ldl, int64_t Tn, int E, int sigmoid, int k, int renorm, float scale,
+hipError_t bwd_piece(const T* logits, int64_t ldl, int64_t Tn, int E, int sigmoid, int k, int renorm, float scale,
                  const int32_t* ids, const float* w, const float* dw, T* dl, int64_t lddl, hipStream_t s) {
   if (k <= 16 && E <= 64) return run_bwd<T, 16, 4>(logits, ldl, Tn, E, sigmoid, k, renorm, scale, ids, w, dw, dl, lddl, s);
   if (k <= 16 && E <= 256)
     return run_bwd<T, 16, 16>(logits, ldl, Tn, E, sigmoid, k, renorm, scale, ids, w, dw, dl, lddl, s);
   if (E <= 256) return run_bwd<T, 64, 4>(logits, ldl, Tn, E, sigmoid, k, renorm, scale, ids, w, dw, dl, lddl, s);
   return run_bwd<T, 64, 16>(logits, ldl, Tn, E, sigmoid, k, renorm, scale, ids, w, dw, dl, lddl, s);
+}
+
+template <typename T>
+hipError_t bwd_t(const T* logits, int64_t ldl, int64_t Tn, int E, int sigmoid, int k, int renorm, float scale,
+                 const int32_t* ids, const float* w, const float* dw, T* dl, int64_t lddl, hipStream_t s) {
+  return in_pieces(Tn, kPieceRows, [&](int64_t t0, int64_t n) {
+    return bwd_piece<T>(logits + t0 * ldl, ldl, n, E, sigmoid, k, renorm, scale, ids + t0 * k, w + t0 * k, dw + t0 * k,
+                        dl + t0 * lddl, lddl, s);
+  });
 }
 
 // ---------------------------------------------------------------------------

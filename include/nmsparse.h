@@ -5,7 +5,9 @@
  * the FFN forward pass and of the double-pruned backward pass.  The last part
  * is the mixture-of-experts FFN in 8-bit floating point: routing, the rows'
  * order by expert, quantisation to blocks of 128, products with a scale per
- * block, and the weighted combine.
+ * block, and the weighted combine; and the dense FFN block around the products:
+ * the norm in front, the dense product with its epilogue and gradients, and the
+ * gradients' norm and clipping.
  *
  * Sources (page title, section):
  *   "Success story: ESPLAG" (inno4scale) -- Highlights, Research Topic,
@@ -731,6 +733,159 @@ nm_status moe_combine(nm_dtype dt, const void* O, int64_t ldo, int64_t rows, con
 nm_status moe_combine_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int64_t rows,
                           const int32_t* src, const int32_t* pos, const float* weights, int64_t T, int k, int64_t D,
                           void* dO, int64_t lddo, float* dweights, nm_stream stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The dense FFN block ("To 2:4 Sparsity and Beyond", abstract: sparse steps
+ * for most of the training, "regular dense training steps towards the end"):
+ * the norm in front of the block, the dense products with what surrounds them,
+ * their gradients, and the gradients' norm and clipping.  A block's forward is
+ *   rms_norm -> linear_fwd (up: bias, activation) -> linear_fwd (down: bias, residual)
+ * and its backward linear_bwd_w and linear_bwd_x of both products (the latter
+ * with the activation's derivative between them), linear_bwd_act for the
+ * biases, rms_norm_bwd, then grad_clip over all gradients.
+ *
+ * An output of these calls may be one of the call's own inputs, at the same
+ * address with the same row stride and type, where that is stated; no other
+ * overlap is allowed.
+ * ---------------------------------------------------------------------------
+ */
+
+typedef enum { NM_ACT_NONE = 0, NM_ACT_RELU = 1, NM_ACT_GELU_TANH = 2, NM_ACT_SILU = 3 } nm_act;
+
+/*
+ * rms_norm -- the residual's addition and the root-mean-square norm of each row:
+ *   h[t][c] = X[t][c] + residual[t][c]      (residual NULL: X)
+ *   rstd[t] = 1 / sqrt(mean over c of h[t][c]^2 + eps)
+ *   Y[t][c] = h[t][c] * rstd[t] * w[c]
+ *   X, residual, Y [T][..] dtype dt, w [D] dtype wdt, rstd fp32 [T] (NULL: not stored)
+ *   H [T][ldh] dtype dt: h rounded, the next block's residual (NULL: not stored)
+ * Sums and products are fp32 and taken from h before its rounding; every output is rounded once.
+ * H may be X or the residual, Y may be X.  Squares are fp32: rows beyond 1e19 overflow.  0 < eps, finite, and
+ * D <= 32768 (NM_ERR_UNSUPPORTED).
+ */
+nm_status rms_norm(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
+                   const void* w, float eps, int64_t T, int64_t D, void* H, int64_t ldh, void* Y, int64_t ldy,
+                   float* rstd, nm_stream stream);
+
+/*
+ * rms_norm_fp8 -- rms_norm whose result is the operand of an 8-bit product: the fp32 rows
+ * h * rstd * w to 8 bits in blocks of 128 with a power-of-two scale, by fp8_quantize's rule (the fp32 values are
+ * rounded once, to 8 bits).
+ *   Q [T][ldq] bytes, ldq >= Dp = D rounded up to 128: columns D .. Dp-1 are written 0
+ *   S fp32 [Dp / 128][lds], lds >= T
+ *   Y as for rms_norm (NULL: not stored); the rest as for rms_norm.
+ */
+nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
+                       const void* w, float eps, int64_t T, int64_t D, nm_fp8 fmt, uint8_t* Q, int64_t ldq, float* S,
+                       int64_t lds, void* H, int64_t ldh, void* Y, int64_t ldy, float* rstd, nm_stream stream);
+
+/*
+ * rms_norm_bwd -- the gradients of rms_norm.  With xh = H * rstd and g = dY * w:
+ *   dX[t][c] = dH[t][c] + rstd[t] (g[t][c] - xh[t][c] mean over c of g[t] xh[t])
+ *   dw[c]    = sum over t of dY[t][c] xh[t][c]
+ *   dY, H (what rms_norm stored, or its X without a residual), dH (the gradient that reaches h by other ways: the
+ *   residual's; NULL: none), dX [T][..] dtype dt; w [D] dtype wdt; rstd fp32 [T]; dw fp32 [D]
+ *   work  device memory, 4-byte aligned, of rms_norm_bwd_work_bytes bytes (NULL when that is 0;
+ *         NM_ERR_SHAPE when work_bytes is less)
+ * dX is the gradient of X and of the residual.  It may be dY or dH.  Sums are fp32; dw's are added in an order that
+ * depends on T and D alone.  D <= 32768 (NM_ERR_UNSUPPORTED).
+ */
+nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H, int64_t ldh, nm_dtype wdt,
+                       const void* w, const float* rstd, const void* dH, int64_t lddh, int64_t T, int64_t D, void* dX,
+                       int64_t lddx, float* dw, void* work, int64_t work_bytes, nm_stream stream);
+
+/* Host only: the work bytes rms_norm_bwd uses (*bytes; 0 for few rows). */
+nm_status rms_norm_bwd_work_bytes(int64_t T, int64_t D, int64_t* bytes);
+
+/*
+ * linear_fwd -- the dense product of an FFN layer with what follows it:
+ *   z[m][n] = sum over k of X[m][k] W[n][k] + bias[n]
+ *   Y[m][n] = act(z[m][n]) + residual[m][n]
+ *   NM_ACT_NONE        z
+ *   NM_ACT_RELU        z where z > 0, else +0.0 (a NaN becomes 0, as in prune_act_venom's and fp8_quantize's ReLU)
+ *   NM_ACT_GELU_TANH   0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
+ *   NM_ACT_SILU        z / (1 + exp(-z))
+ *   X [M][ldx], W [N][ldw], residual [M][ldr] (NULL: none) bf16; bias [N] dtype bdt (NULL: none)
+ *   Y [M][ldy] bf16 or fp32 (out); pre [M][ldp] bf16: z, what the backward pass reads (NULL: not stored)
+ * Sums, z and the activation are fp32; Y and pre are rounded once each.  bf16 only (NM_ERR_UNSUPPORTED).  Y may be
+ * the residual (bf16).  The tiled kernels run when K, ldx and ldw are multiples of 8 and X and W are
+ * 16-byte aligned; other calls take a slower general kernel.
+ */
+nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
+                     const void* bias, nm_act act, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K,
+                     nm_dtype out, void* Y, int64_t ldy, void* pre, int64_t ldp, nm_stream stream);
+
+/*
+ * linear_bwd_act -- the gradient of an activation and of the bias in front of it:
+ *   dZ[m][n] = dY[m][n] act'(pre[m][n]),  db[n] = sum over m of dY[m][n] act'(pre[m][n])
+ *   dY [M][lddy], pre [M][ldp] (linear_fwd's; NULL with NM_ACT_NONE), dZ [M][lddz] bf16 (NULL: not stored);
+ *   db fp32 [N] (NULL: not wanted; not both).  dZ may be dY or pre.
+ *   work  device memory, 4-byte aligned, of linear_bwd_act_work_bytes bytes (NULL when that is 0 or db is NULL;
+ *         NM_ERR_SHAPE when work_bytes is less)
+ * The derivative of ReLU at 0 is 0.  db adds the fp32 products before dZ's rounding, in an order that depends on M and
+ * N alone.  bf16 only (NM_ERR_UNSUPPORTED).
+ */
+nm_status linear_bwd_act(nm_dtype dt, const void* dY, int64_t lddy, const void* pre, int64_t ldp, nm_act act, int64_t M,
+                         int64_t N, void* dZ, int64_t lddz, float* db, void* work, int64_t work_bytes,
+                         nm_stream stream);
+
+/* Host only: the work bytes linear_bwd_act uses for db (*bytes; 0 for few rows). */
+nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes);
+
+/*
+ * linear_bwd_x -- the gradient of linear_fwd's input, with the derivative of the activation that made it:
+ *   dX[m][k] = (sum over n of dZ[m][n] W[n][k]) act'(pre[m][k])
+ *   dZ [M][lddz], W [N][ldw] bf16; pre [M][ldp] bf16, the pre-activations X came from (NULL with NM_ACT_NONE)
+ *   dX [M][lddx] bf16 or fp32 (out); it may be pre (bf16).
+ * With ReLU, X itself gives the same derivative as its pre-activations.  Sums are fp32, the result is rounded once.
+ * bf16 only.  The tiled kernels run when N, K and the leading dimensions of dZ and W are multiples
+ * of 8 and dZ and W are 16-byte aligned.
+ */
+nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W, int64_t ldw, const void* pre,
+                       int64_t ldp, nm_act act, int64_t M, int64_t N, int64_t K, nm_dtype out, void* dX, int64_t lddx,
+                       nm_stream stream);
+
+/*
+ * linear_bwd_w -- the gradient of linear_fwd's weight:
+ *   dW[n][k] = sum over m of dZ[m][n] X[m][k]      (accumulate: added to dW)
+ *   dZ [M][lddz], X [M][ldx] bf16; dW [N][lddw] fp32 or bf16 (out; accumulate needs fp32, NM_ERR_UNSUPPORTED)
+ * Sums are fp32.  bf16 operands only.  The tiled kernels run when N, K and the leading dimensions of dZ and X
+ * are multiples of 8 and dZ and X are 16-byte aligned.
+ */
+nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
+                       int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, nm_stream stream);
+
+/*
+ * grad_norm -- the norm of n tensors together: norm = sqrt(sum over all elements of g^2), one fp32 value.
+ *   dt, grads, counts  HOST arrays of n entries (read before the call returns): each tensor's dtype, device address
+ *                      and number of contiguous elements; an entry of 0 elements is left out, whatever its address
+ *   norm   device fp32, one value
+ *   work   device memory, 8-byte aligned, of grad_work_bytes bytes (NM_ERR_SHAPE when work_bytes is less)
+ * Squares and sums are 64-bit, in an order that depends on the counts alone; the result is rounded once (a norm
+ * beyond fp32 is infinity; a NaN or infinite element makes it NaN or infinite).  1 <= n <= 65536.
+ */
+nm_status grad_norm(int64_t n, const nm_dtype* dt, const void* const* grads, const int64_t* counts, float* norm,
+                    void* work, int64_t work_bytes, nm_stream stream);
+
+/*
+ * grad_clip -- n tensors scaled so that their norm is at most max_norm:
+ *   f = max_norm / norm where max_norm < norm < infinity, else 1;  out = f * grad, rounded once
+ *   have_norm 0: *norm is grad_norm's result, written by this call (work as for grad_norm)
+ *   have_norm 1: *norm is the caller's (the norm of gradients that lie on several GPUs, say) and is read; work may be
+ *                NULL
+ *   out  HOST array of device addresses with dtypes odt, counts as the gradients'.  out[i] may be grads[i] with the
+ *        same dtype (in place; nothing is written where f is 1).  No other overlap of an output with another
+ *        output or a gradient is allowed: NM_ERR_SHAPE, so a tensor that is listed twice in place is refused.
+ * A norm that is not finite leaves the values as they are.  0 <= max_norm, infinity allowed (NM_ERR_UNSUPPORTED for a
+ * NaN or negative one).
+ */
+nm_status grad_clip(int64_t n, const nm_dtype* dt, const void* const* grads, const int64_t* counts, float max_norm,
+                    int have_norm, float* norm, const nm_dtype* odt, void* const* out, void* work, int64_t work_bytes,
+                    nm_stream stream);
+
+/* Host only: the work bytes grad_norm and grad_clip use (*bytes). */
+nm_status grad_work_bytes(int64_t n, const int64_t* counts, int64_t* bytes);
 
 /*
  * nm_sizes -- host-only helper: element count of values, bytes of meta and of

@@ -1,6 +1,7 @@
 """MI355X (gfx950) semi-structured sparse FFN matmuls: N:M and V:N:M pruning,
-compression and sparse x dense products, and the mixture-of-experts FFN in
-8-bit floating point, behind the libnmsparse C ABI.
+compression and sparse x dense products, the mixture-of-experts FFN in 8-bit
+floating point, and the dense FFN block around the products, behind the
+libnmsparse C ABI.
 
 The binding functions live in `sparse_matmul_ffns_amd.nmsparse`; the library
 is loaded on first use and must have been built with
@@ -16,7 +17,13 @@ from .nmsparse import (  # noqa: F401
     fp8_quantize,
     fp8_quantize_t,
     fp8_quantize_weight,
+    grad_clip,
+    grad_norm,
     lib,
+    linear_bwd_act,
+    linear_bwd_w,
+    linear_bwd_x,
+    linear_fwd,
     mfma_rate_probe,
     moe_combine,
     moe_combine_bwd,
@@ -34,6 +41,9 @@ from .nmsparse import (  # noqa: F401
     nm_to_panels,
     nm_reprune_t,
     prune_act_venom,
+    rms_norm,
+    rms_norm_bwd,
+    rms_norm_fp8,
     sddmm_nm,
     sizes,
     spmm_nm,

@@ -5,6 +5,9 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+#include <new>
+
 #include "../../include/nmsparse.h"
 #include "launch.hpp"
 
@@ -55,6 +58,66 @@ nm_status fp8_gemm_check(nm_fp8 fa, const void* A, int64_t lda, const void* sa, 
       ldc < N)
     return NM_ERR_SHAPE;
   if (!aligned(sa, 4) || !aligned(sb, 4) || !aligned(C, esize(out))) return NM_ERR_ALIGN;
+  return NM_OK;
+}
+
+bool act_ok(nm_act a) { return a >= NM_ACT_NONE && a <= NM_ACT_SILU; }
+// A number of rows and a width that an int holds.
+bool rows_ok(int64_t R, int64_t C) { return R > 0 && C > 0 && R <= INT32_MAX && C <= INT32_MAX; }
+bool same(const void* a, int64_t lda, const void* b, int64_t ldb) { return a == b && lda == ldb; }
+constexpr int64_t kNormWidth = 32768;   // a row stays in the registers of a workgroup
+
+// the checks rms_norm and rms_norm_fp8 share
+nm_status norm_check(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
+                     const void* w, float eps, int64_t T, int64_t D, const void* H, int64_t ldh, const void* Y,
+                     int64_t ldy, const float* rstd) {
+  if (!X || !w) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || !dtype_ok(wdt) || !(eps > 0.f) || eps - eps != 0.f) return NM_ERR_UNSUPPORTED;
+  if (!rows_ok(T, D) || ldx < D || (residual && ldr < D) || (H && ldh < D) || (Y && ldy < D)) return NM_ERR_SHAPE;
+  if (D > kNormWidth) return NM_ERR_UNSUPPORTED;
+  if (!aligned(X, esize(dt)) || !aligned(residual, esize(dt)) || !aligned(w, esize(wdt)) || !aligned(H, esize(dt)) ||
+      !aligned(Y, esize(dt)) || !aligned(rstd, 4))
+    return NM_ERR_ALIGN;
+  return NM_OK;
+}
+
+// A contiguous range of device memory that a call over many tensors reads, or writes (out).
+struct Range {
+  uintptr_t lo, hi;
+  bool out;
+};
+
+// Whether an output meets another range (in place, an output is its own gradient).
+bool outputs_overlap(const Range* r, int64_t n) {
+  // sorted by address: the ranges that started before and reach furthest, among the outputs and among all
+  uintptr_t hi_out = 0, hi_any = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (r[i].lo < hi_out || (r[i].out && r[i].lo < hi_any)) return true;
+    if (r[i].out && r[i].hi > hi_out) hi_out = r[i].hi;
+    if (r[i].hi > hi_any) hi_any = r[i].hi;
+  }
+  return false;
+}
+
+// the checks grad_norm and grad_clip share
+nm_status grads_check(int64_t n, const nm_dtype* dt, const void* const* grads, const int64_t* counts,
+                      const float* norm, const void* work, int64_t work_bytes, bool need_work) {
+  if (n <= 0 || n > 65536) return NM_ERR_SHAPE;
+  if (!dt || !grads || !counts || !norm) return NM_ERR_NULL;
+  for (int64_t i = 0; i < n; ++i) {
+    if (!dtype_ok(dt[i])) return NM_ERR_UNSUPPORTED;
+    if (counts[i] < 0 || counts[i] > INT64_MAX / 8 / n) return NM_ERR_SHAPE;
+    if (counts[i] == 0) continue;
+    if (!grads[i]) return NM_ERR_NULL;
+    if (!aligned(grads[i], esize(dt[i]))) return NM_ERR_ALIGN;
+  }
+  if (!aligned(norm, 4)) return NM_ERR_ALIGN;
+  if (need_work) {
+    const int64_t need = nms::grad_partials(counts, n) * 8;
+    if (need > 0 && !work) return NM_ERR_NULL;
+    if (work_bytes < need) return NM_ERR_SHAPE;
+    if (!aligned(work, 8)) return NM_ERR_ALIGN;
+  }
   return NM_OK;
 }
 
@@ -515,6 +578,176 @@ nm_status moe_combine_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void*
     return NM_ERR_ALIGN;
   return hip_status(nms::launch_moe_combine_bwd(dt, dY, lddy, O, ldo, rows, src, pos, weights, T, k, D, dO, lddo,
                                                 dweights, hs(stream)));
+}
+
+nm_status rms_norm(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
+                   const void* w, float eps, int64_t T, int64_t D, void* H, int64_t ldh, void* Y, int64_t ldy,
+                   float* rstd, nm_stream stream) {
+  if (!Y) return NM_ERR_NULL;
+  const nm_status st = norm_check(dt, X, ldx, residual, ldr, wdt, w, eps, T, D, H, ldh, Y, ldy, rstd);
+  if (st != NM_OK) return st;
+  const nms::NormArgs a{X, ldx, residual, ldr, w, eps, T, D, H, ldh, Y, ldy, rstd, nullptr, 0, nullptr, 0, 0};
+  return hip_status(nms::launch_rms_norm(dt, wdt, a, hs(stream)));
+}
+
+nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
+                       const void* w, float eps, int64_t T, int64_t D, nm_fp8 fmt, uint8_t* Q, int64_t ldq, float* S,
+                       int64_t lds, void* H, int64_t ldh, void* Y, int64_t ldy, float* rstd, nm_stream stream) {
+  if (!Q || !S) return NM_ERR_NULL;
+  if (!fp8_ok(fmt)) return NM_ERR_UNSUPPORTED;
+  const nm_status st = norm_check(dt, X, ldx, residual, ldr, wdt, w, eps, T, D, H, ldh, Y, ldy, rstd);
+  if (st != NM_OK) return st;
+  if (ldq < up128(D) || lds < T) return NM_ERR_SHAPE;
+  if (!aligned(S, 4)) return NM_ERR_ALIGN;
+  const nms::NormArgs a{X, ldx, residual, ldr, w, eps, T, D, H, ldh, Y, ldy, rstd, Q, ldq, S, lds, fmt == NM_E5M2};
+  return hip_status(nms::launch_rms_norm(dt, wdt, a, hs(stream)));
+}
+
+nm_status rms_norm_bwd_work_bytes(int64_t T, int64_t D, int64_t* bytes) {
+  if (!bytes) return NM_ERR_NULL;
+  if (!rows_ok(T, D)) return NM_ERR_SHAPE;
+  if (D > kNormWidth) return NM_ERR_UNSUPPORTED;
+  const int64_t g = nms::norm_bwd_groups(T, D);
+  *bytes = g > 1 ? g * D * 4 : 0;
+  return NM_OK;
+}
+
+nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H, int64_t ldh, nm_dtype wdt,
+                       const void* w, const float* rstd, const void* dH, int64_t lddh, int64_t T, int64_t D, void* dX,
+                       int64_t lddx, float* dw, void* work, int64_t work_bytes, nm_stream stream) {
+  if (!dY || !H || !w || !rstd || !dX || !dw) return NM_ERR_NULL;
+  if (!dtype_ok(dt) || !dtype_ok(wdt)) return NM_ERR_UNSUPPORTED;
+  if (!rows_ok(T, D) || lddy < D || ldh < D || (dH && lddh < D) || lddx < D) return NM_ERR_SHAPE;
+  int64_t need;
+  const nm_status st = rms_norm_bwd_work_bytes(T, D, &need);
+  if (st != NM_OK) return st;
+  if (need > 0 && !work) return NM_ERR_NULL;
+  if (work_bytes < need) return NM_ERR_SHAPE;
+  if (!aligned(dY, esize(dt)) || !aligned(H, esize(dt)) || !aligned(w, esize(wdt)) || !aligned(rstd, 4) ||
+      !aligned(dH, esize(dt)) || !aligned(dX, esize(dt)) || !aligned(dw, 4) || !aligned(work, 4))
+    return NM_ERR_ALIGN;
+  const nms::NormBwdArgs a{dY, lddy, H, ldh, w, rstd, dH, lddh, T, D, dX, lddx, dw, (float*)work};
+  return hip_status(nms::launch_rms_norm_bwd(dt, wdt, a, hs(stream)));
+}
+
+nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
+                     const void* bias, nm_act act, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K,
+                     nm_dtype out, void* Y, int64_t ldy, void* pre, int64_t ldp, nm_stream stream) {
+  if (!X || !W || !Y) return NM_ERR_NULL;
+  if (dt != NM_BF16 || !dtype_ok(out) || (bias && !dtype_ok(bdt)) || !act_ok(act)) return NM_ERR_UNSUPPORTED;
+  if (!rows_ok(M, N) || !rows_ok(K, 1) || ldx < K || ldw < K || (residual && ldr < N) || ldy < N || (pre && ldp < N))
+    return NM_ERR_SHAPE;
+  if (!aligned(X, 2) || !aligned(W, 2) || (bias && !aligned(bias, esize(bdt))) || !aligned(residual, 2) ||
+      !aligned(Y, esize(out)) || !aligned(pre, 2))
+    return NM_ERR_ALIGN;
+  const nms::Linear g{(const uint16_t*)X, ldx, (const uint16_t*)W, ldw, 0, 0, M, N, K, Y, ldy, out == NM_BF16,
+                      nms::EPI_FWD, bias, bdt == NM_BF16, act, (const uint16_t*)residual, ldr, (uint16_t*)pre, ldp,
+                      nullptr, 0, 0};
+  return hip_status(nms::launch_linear(g, hs(stream)));
+}
+
+nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes) {
+  if (!bytes) return NM_ERR_NULL;
+  if (!rows_ok(M, N)) return NM_ERR_SHAPE;
+  const int64_t g = nms::act_bwd_groups(M, N);
+  *bytes = g > 1 ? g * N * 4 : 0;
+  return NM_OK;
+}
+
+nm_status linear_bwd_act(nm_dtype dt, const void* dY, int64_t lddy, const void* pre, int64_t ldp, nm_act act, int64_t M,
+                         int64_t N, void* dZ, int64_t lddz, float* db, void* work, int64_t work_bytes,
+                         nm_stream stream) {
+  if (!dY || (!pre && act != NM_ACT_NONE) || (!dZ && !db)) return NM_ERR_NULL;
+  if (dt != NM_BF16 || !act_ok(act)) return NM_ERR_UNSUPPORTED;
+  if (!rows_ok(M, N) || lddy < N || (act != NM_ACT_NONE && ldp < N) || (dZ && lddz < N)) return NM_ERR_SHAPE;
+  int64_t need = 0;
+  if (db) (void)linear_bwd_act_work_bytes(M, N, &need);
+  if (need > 0 && !work) return NM_ERR_NULL;
+  if (work_bytes < need) return NM_ERR_SHAPE;
+  if (!aligned(dY, 2) || !aligned(pre, 2) || !aligned(dZ, 2) || !aligned(db, 4) || !aligned(work, 4)) return NM_ERR_ALIGN;
+  const nms::ActBwdArgs a{dY, lddy, pre, ldp, act, M, N, dZ, lddz, db, (float*)work};
+  return hip_status(nms::launch_linear_bwd_act(a, hs(stream)));
+}
+
+nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W, int64_t ldw, const void* pre,
+                       int64_t ldp, nm_act act, int64_t M, int64_t N, int64_t K, nm_dtype out, void* dX, int64_t lddx,
+                       nm_stream stream) {
+  if (!dZ || !W || !dX || (!pre && act != NM_ACT_NONE)) return NM_ERR_NULL;
+  if (dt != NM_BF16 || !dtype_ok(out) || !act_ok(act)) return NM_ERR_UNSUPPORTED;
+  if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldw < K || (act != NM_ACT_NONE && ldp < K) || lddx < K)
+    return NM_ERR_SHAPE;
+  if (!aligned(dZ, 2) || !aligned(W, 2) || !aligned(pre, 2) || !aligned(dX, esize(out))) return NM_ERR_ALIGN;
+  // rows of dZ times columns of W: the product's columns are W's, its reduction runs over W's rows
+  const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)W, ldw, 0, 1, M, K, N, dX, lddx, out == NM_BF16,
+                      act == NM_ACT_NONE ? nms::EPI_PLAIN : nms::EPI_GATE, nullptr, 0, act, nullptr, 0, nullptr, 0,
+                      (const uint16_t*)pre, ldp, 0};
+  return hip_status(nms::launch_linear(g, hs(stream)));
+}
+
+nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
+                       int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, nm_stream stream) {
+  if (!dZ || !X || !dW) return NM_ERR_NULL;
+  if (dt != NM_BF16 || !dtype_ok(out) || (accumulate && out != NM_F32)) return NM_ERR_UNSUPPORTED;
+  if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldx < K || lddw < K) return NM_ERR_SHAPE;
+  if (!aligned(dZ, 2) || !aligned(X, 2) || !aligned(dW, esize(out))) return NM_ERR_ALIGN;
+  const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)X, ldx, 1, 1, N, K, M, dW, lddw, out == NM_BF16,
+                      nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0, accumulate != 0};
+  return hip_status(nms::launch_linear(g, hs(stream)));
+}
+
+nm_status grad_work_bytes(int64_t n, const int64_t* counts, int64_t* bytes) {
+  if (!bytes || !counts) return NM_ERR_NULL;
+  if (n <= 0 || n > 65536) return NM_ERR_SHAPE;
+  for (int64_t i = 0; i < n; ++i)
+    if (counts[i] < 0 || counts[i] > INT64_MAX / 8 / n) return NM_ERR_SHAPE;
+  *bytes = nms::grad_partials(counts, n) * 8;
+  return NM_OK;
+}
+
+nm_status grad_norm(int64_t n, const nm_dtype* dt, const void* const* grads, const int64_t* counts, float* norm,
+                    void* work, int64_t work_bytes, nm_stream stream) {
+  const nm_status st = grads_check(n, dt, grads, counts, norm, work, work_bytes, true);
+  if (st != NM_OK) return st;
+  const nms::Grads g{n, (const int*)dt, grads, counts, nullptr, nullptr};
+  return hip_status(nms::launch_grad_norm(g, norm, (double*)work, hs(stream)));
+}
+
+nm_status grad_clip(int64_t n, const nm_dtype* dt, const void* const* grads, const int64_t* counts, float max_norm,
+                    int have_norm, float* norm, const nm_dtype* odt, void* const* out, void* work, int64_t work_bytes,
+                    nm_stream stream) {
+  if (!odt || !out) return NM_ERR_NULL;
+  const nm_status st = grads_check(n, dt, grads, counts, norm, work, work_bytes, !have_norm);
+  if (st != NM_OK) return st;
+  if (!(max_norm >= 0.f)) return NM_ERR_UNSUPPORTED;
+  for (int64_t i = 0; i < n; ++i) {
+    if (!dtype_ok(odt[i])) return NM_ERR_UNSUPPORTED;
+    if (counts[i] == 0) continue;
+    if (!out[i]) return NM_ERR_NULL;
+    if (!aligned(out[i], esize(odt[i]))) return NM_ERR_ALIGN;
+  }
+  Range* r = new (std::nothrow) Range[2 * n + 2];
+  if (!r) return hip_status(hipErrorOutOfMemory);
+  int64_t k = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (counts[i] == 0) continue;
+    const uintptr_t o = (uintptr_t)out[i], p = (uintptr_t)grads[i];
+    r[k++] = Range{o, o + (uintptr_t)(counts[i] * esize(odt[i])), true};
+    if (o != p || odt[i] != dt[i]) r[k++] = Range{p, p + (uintptr_t)(counts[i] * esize(dt[i])), false};
+  }
+  // the norm and the work memory are written too
+  r[k++] = Range{(uintptr_t)norm, (uintptr_t)norm + 4, true};
+  if (!have_norm && work)
+    r[k++] = Range{(uintptr_t)work, (uintptr_t)work + (uintptr_t)(nms::grad_partials(counts, n) * 8), true};
+  std::sort(r, r + k, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  const bool bad = outputs_overlap(r, k);
+  delete[] r;
+  if (bad) return NM_ERR_SHAPE;
+  const nms::Grads g{n, (const int*)dt, grads, counts, (const int*)odt, out};
+  if (!have_norm) {
+    const hipError_t e = nms::launch_grad_norm(g, norm, (double*)work, hs(stream));
+    if (e != hipSuccess) return hip_status(e);
+  }
+  return hip_status(nms::launch_grad_scale(g, norm, max_norm, hs(stream)));
 }
 
 void nm_sizes(int64_t R, int64_t K, int N, int M, int V, int64_t* n_values, int64_t* meta_bytes,

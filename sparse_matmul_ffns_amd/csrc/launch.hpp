@@ -188,4 +188,93 @@ struct Fp8Gemm {
 };
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t s);
 
+// The dense FFN block: norms, products with their epilogue and gradients, the gradients' norm.
+struct NormArgs {
+  const void* X;
+  int64_t ldx;
+  const void* R;            // null: nothing is added
+  int64_t ldr;
+  const void* w;
+  float eps;
+  int64_t T, D;
+  void* H;                  // null: the sum is not stored
+  int64_t ldh;
+  void* Y;                  // null with Q only
+  int64_t ldy;
+  float* rstd;              // null: not stored
+  uint8_t* Q;               // null: no 8-bit result
+  int64_t ldq;
+  float* S;
+  int64_t lds;
+  int e5m2;
+};
+hipError_t launch_rms_norm(int dt, int wdt, const NormArgs& a, hipStream_t s);
+struct NormBwdArgs {
+  const void* dY;
+  int64_t lddy;
+  const void* H;
+  int64_t ldh;
+  const void* w;
+  const float* rstd;
+  const void* dH;           // null: nothing comes through the residual
+  int64_t lddh, T, D;
+  void* dX;
+  int64_t lddx;
+  float* dw;
+  float* work;
+};
+int64_t norm_bwd_groups(int64_t T, int64_t D);
+hipError_t launch_rms_norm_bwd(int dt, int wdt, const NormBwdArgs& a, hipStream_t s);
+// out[c] = sum of part[0 .. G - 1][c], in fp32 in a fixed order.
+hipError_t launch_sum_partials(const float* part, int64_t G, int64_t N, float* out, hipStream_t s);
+struct ActBwdArgs {
+  const void* dY;
+  int64_t lddy;
+  const void* pre;
+  int64_t ldp;
+  int act;
+  int64_t M, N;
+  void* dZ;                 // null: only the sums
+  int64_t lddz;
+  float* db;                // null: no sums
+  float* work;
+};
+int64_t act_bwd_groups(int64_t M, int64_t N);
+hipError_t launch_linear_bwd_act(const ActBwdArgs& a, hipStream_t s);
+// C[m][n] = sum over k of A(m, k) B(n, k), bf16 operands: A(m, k) at A[m * lda + k], or with a_t at
+// A[k * lda + m]; B alike.
+enum { EPI_FWD = 0, EPI_GATE = 1, EPI_PLAIN = 2 };
+struct Linear {
+  const uint16_t* A;
+  int64_t lda;
+  const uint16_t* B;
+  int64_t ldb;
+  int a_t, b_t;
+  int64_t M, N, K;
+  void* C;
+  int64_t ldc;
+  int bf16_out, epi;
+  const void* bias;         // EPI_FWD; null: none
+  int bias_bf16, act;
+  const uint16_t* R;        // EPI_FWD: added behind the activation; null: none
+  int64_t ldr;
+  uint16_t* Z;              // EPI_FWD: the sum before the activation; null: not stored
+  int64_t ldz;
+  const uint16_t* P;        // EPI_GATE: the activation's derivative at P
+  int64_t ldp;
+  int accumulate;           // EPI_PLAIN: added to C (fp32)
+};
+hipError_t launch_linear(const Linear& g, hipStream_t s);
+struct Grads {
+  int64_t n;
+  const int* dt;
+  const void* const* in;
+  const int64_t* count;
+  const int* odt;           // with out
+  void* const* out;         // null for the norm alone
+};
+int64_t grad_partials(const int64_t* count, int64_t n);
+hipError_t launch_grad_norm(const Grads& g, float* norm, double* work, hipStream_t s);
+hipError_t launch_grad_scale(const Grads& g, const float* norm, float max_norm, hipStream_t s);
+
 }  // namespace nms

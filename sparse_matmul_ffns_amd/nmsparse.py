@@ -24,6 +24,7 @@ NM_OK, NM_ERR_NULL, NM_ERR_SHAPE, NM_ERR_UNSUPPORTED, NM_ERR_ALIGN, NM_ERR_HIP, 
 NM_F32, NM_BF16 = 0, 1
 NM_E4M3, NM_E5M2 = 0, 1
 NM_SOFTMAX, NM_SIGMOID = 0, 1
+NM_ACT_NONE, NM_ACT_RELU, NM_ACT_GELU_TANH, NM_ACT_SILU = range(4)
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -75,6 +76,21 @@ _SIGNATURES = {
                               _int, _vp, _i64, _vp],
     "moe_combine": [_int, _vp, _i64, _i64, _vp, _vp, _i64, _int, _i64, _vp, _i64, _vp],
     "moe_combine_bwd": [_int, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _int, _i64, _vp, _i64, _vp, _vp],
+    "rms_norm": [_int, _vp, _i64, _vp, _i64, _int, _vp, _f32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp],
+    "rms_norm_fp8": [_int, _vp, _i64, _vp, _i64, _int, _vp, _f32, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64,
+                     _vp, _i64, _vp, _vp],
+    "rms_norm_bwd": [_int, _vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64,
+                     _vp],
+    "rms_norm_bwd_work_bytes": [_i64, _i64, ctypes.POINTER(_i64)],
+    "linear_fwd": [_int, _vp, _i64, _vp, _i64, _int, _vp, _int, _vp, _i64, _i64, _i64, _i64, _int, _vp, _i64, _vp,
+                   _i64, _vp],
+    "linear_bwd_act": [_int, _vp, _i64, _vp, _i64, _int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp],
+    "linear_bwd_act_work_bytes": [_i64, _i64, ctypes.POINTER(_i64)],
+    "linear_bwd_x": [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp],
+    "linear_bwd_w": [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp],
+    "grad_norm": [_i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
+    "grad_clip": [_i64, _vp, _vp, _vp, _f32, _int, _vp, _vp, _vp, _vp, _i64, _vp],
+    "grad_work_bytes": [_i64, _vp, ctypes.POINTER(_i64)],
 }
 
 _lib = None
@@ -972,3 +988,304 @@ def moe_combine_bwd(dY: torch.Tensor, O: torch.Tensor, src: torch.Tensor, pos: t
                                  _p(weights), T, k, D, _p(dO), _ld(dO, "dO"), _p(dweights), _stream()),
            "moe_combine_bwd")
     return dO, dweights
+
+
+# ---------------------------------------------------------------------------
+# The dense FFN block: the norm, the dense products with their gradients, the gradients' norm
+# ---------------------------------------------------------------------------
+_ACTS = {"none": NM_ACT_NONE, "relu": NM_ACT_RELU, "gelu_tanh": NM_ACT_GELU_TANH, "silu": NM_ACT_SILU}
+
+
+def _act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError("act must be 'none', 'relu', 'gelu_tanh' or 'silu'")
+    return _ACTS[act]
+
+
+def _here(*ts) -> None:
+    """Device tensors (None is skipped) of the current device, on whose stream the call runs."""
+    _dev(*ts)
+    here = torch._C._cuda_getDevice()
+    for t in ts:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor lies on cuda:{t.get_device()}, but the current device is cuda:{here}")
+
+
+def _matrix(t: torch.Tensor, shape, dtype, name: str) -> int:
+    """Row stride of a tensor of the given shape and dtype (None: bf16 or fp32) with contiguous rows."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return _ld(t, name)
+
+
+def _opt(t, shape, dtype, name: str) -> int:
+    return 0 if t is None else _matrix(t, shape, dtype, name)
+
+
+def _two(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape
+
+
+def _new_or(t, shape, dtype, like, name: str):
+    """t, checked, or a new tensor; and its row stride."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype), shape[1]
+    return t, _matrix(t, shape, dtype, name)
+
+
+def _new_vector(t, n: int, like, name: str):
+    if t is None:
+        return like.new_empty(n, dtype=torch.float32)
+    _of(t, (n,), torch.float32, name)
+    return t
+
+
+def _workspace(work, need: int, like):
+    """A caller's contiguous device tensor, or with "auto" a new one of `need` bytes; and its bytes."""
+    if isinstance(work, str):
+        if work != "auto":
+            raise ValueError("work must be a tensor, None or 'auto'")
+        if need == 0:
+            return None, 0
+        return like.new_empty(need, dtype=torch.uint8), need
+    if work is None:
+        return None, 0
+    _here(work), _flat(work, "work")
+    return work, work.numel() * work.element_size()
+
+
+def _norm_args(X, w, residual, H, rstd):
+    T, D = _two(X, "X")
+    _here(X, w, residual, H, rstd)
+    if w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [{D}] tensor")
+    ldx = _ld(X, "X")
+    ldr = _opt(residual, (T, D), X.dtype, "residual")
+    if H is None and residual is not None:
+        H = X.new_empty((T, D))
+    ldh = _opt(H, (T, D), X.dtype, "H")
+    return T, D, ldx, ldr, H, ldh, _new_vector(rstd, T, X, "rstd")
+
+
+def rms_norm(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=None, H=None, Y=None, rstd=None):
+    """h = X [T, D] + residual, Y = h / sqrt(mean(h^2) + eps) * w: returns (Y, H, rstd), H the rounded sum
+    (without a residual X itself, unless H is given) and rstd [T] fp32, what rms_norm_bwd reads.  In place: H may be
+    X or the residual, Y may be X."""
+    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd)
+    _here(Y)
+    Y, ldy = _new_or(Y, (T, D), X.dtype, X, "Y")
+    _check(lib().rms_norm(_dt(X), _p(X), ldx, _p(residual), ldr, _dt(w), _p(w), eps, T, D, _p(H), ldh, _p(Y), ldy,
+                          _p(rstd), _stream()), "rms_norm")
+    return Y, X if H is None else H, rstd
+
+
+def rms_norm_fp8(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=None,
+                 fmt: torch.dtype = torch.float8_e4m3fn, H=None, Q=None, S=None, Y=None, rstd=None):
+    """rms_norm with its result in 8 bits and a power-of-two scale per row and 128 columns, as fp8_gemm_nt takes it:
+    returns (Q [T, Dp], S [Dp / 128, T], H, rstd), Dp = D rounded up to 128, the columns beyond D 0.  With a tensor Y
+    [T, D] the result is stored there in X's dtype too."""
+    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd)
+    _here(Q, S, Y)
+    Dp = _up(D, 128)
+    if Q is None:
+        Q = X.new_empty((T, Dp), dtype=fmt)
+    ldq = _matrix(Q, (T, Dp), None, "Q")
+    S, lds = _new_or(S, (Dp // 128, T), torch.float32, X, "S")
+    ldy = _opt(Y, (T, D), X.dtype, "Y")
+    _check(lib().rms_norm_fp8(_dt(X), _p(X), ldx, _p(residual), ldr, _dt(w), _p(w), eps, T, D, _fp8(Q, "Q"), _p(Q),
+                              ldq, _p(S), lds, _p(H), ldh, _p(Y), ldy, _p(rstd), _stream()), "rms_norm_fp8")
+    return Q, S, X if H is None else H, rstd
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_work_bytes(T: int, D: int) -> int:
+    need = _i64()
+    _check(lib().rms_norm_bwd_work_bytes(T, D, ctypes.byref(need)), "rms_norm_bwd_work_bytes")
+    return need.value
+
+
+def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, dH=None, dX=None, dw=None,
+                 work="auto"):
+    """The gradients of rms_norm at its stored H and rstd: (dX [T, D], the gradient of X and of the residual; dw [D]
+    fp32).  `dH` is the gradient that reaches H by other ways (through the residual); dX may be dY or dH."""
+    T, D = _two(H, "H")
+    _here(dY, H, w, rstd, dH, dX, dw)
+    if w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [{D}] tensor")
+    _of(rstd, (T,), torch.float32, "rstd")
+    ldh, lddy = _ld(H, "H"), _matrix(dY, (T, D), H.dtype, "dY")
+    lddh = _opt(dH, (T, D), H.dtype, "dH")
+    dX, lddx = _new_or(dX, (T, D), H.dtype, H, "dX")
+    dw = _new_vector(dw, D, H, "dw")
+    work, nbytes = _workspace(work, _norm_work_bytes(T, D), H)
+    _check(lib().rms_norm_bwd(_dt(H), _p(dY), lddy, _p(H), ldh, _dt(w), _p(w), _p(rstd), _p(dH), lddh, T, D, _p(dX),
+                              lddx, _p(dw), _p(work), nbytes, _stream()), "rms_norm_bwd")
+    return dX, dw
+
+
+def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", residual=None,
+               out_dtype: torch.dtype = torch.bfloat16, out=None, pre=None, return_pre: bool = False):
+    """Y = act(X [M, K] @ W [N, K].T + bias) + residual, bf16 operands and fp32 sums; act is 'none', 'relu',
+    'gelu_tanh' or 'silu'.  With `pre` (a tensor) or `return_pre` returns (Y, pre), pre [M, N] bf16 the sum before the
+    activation, what linear_bwd_act and linear_bwd_x read.  In place: out may be the residual."""
+    M, K = _two(X, "X")
+    N = _two(W, "W")[0]
+    _here(X, W, bias, residual, out, pre)
+    ldx, ldw = _ld(X, "X"), _matrix(W, (N, K), X.dtype, "W")
+    if bias is not None and (bias.shape != (N,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous [{N}] tensor")
+    ldr = _opt(residual, (M, N), X.dtype, "residual")
+    if out is None:
+        out = X.new_empty((M, N), dtype=out_dtype)
+    ldy = _matrix(out, (M, N), None, "out")
+    if pre is None and return_pre:
+        pre = X.new_empty((M, N), dtype=torch.bfloat16)
+    ldp = _opt(pre, (M, N), torch.bfloat16, "pre")
+    _check(lib().linear_fwd(_dt(X), _p(X), ldx, _p(W), ldw, NM_BF16 if bias is None else _dt(bias), _p(bias), _act(act),
+                            _p(residual), ldr, M, N, K, _dt(out), _p(out), ldy, _p(pre), ldp, _stream()), "linear_fwd")
+    return out if pre is None else (out, pre)
+
+
+@functools.lru_cache(maxsize=256)
+def _act_work_bytes(M: int, N: int) -> int:
+    need = _i64()
+    _check(lib().linear_bwd_act_work_bytes(M, N, ctypes.byref(need)), "linear_bwd_act_work_bytes")
+    return need.value
+
+
+def linear_bwd_act(dY: torch.Tensor, pre=None, act: str = "none", dZ=None, db=None, work="auto"):
+    """The gradients of an activation and of the bias in front of it: (dZ = dY act'(pre) [M, N], db [N] fp32, the sums
+    of dZ's columns before its rounding).  With act 'none' dZ is dY itself, unless a tensor dZ is given.  dZ may be dY
+    or pre."""
+    M, N = _two(dY, "dY")
+    _here(dY, pre, dZ, db)
+    lddy = _ld(dY, "dY")
+    if act != "none" and pre is None:
+        raise ValueError("pre is needed for an activation's gradient")
+    ldp = _opt(pre, (M, N), dY.dtype, "pre")
+    a = _act(act)
+    if dZ is None and a != NM_ACT_NONE:
+        dZ = dY.new_empty((M, N))
+    lddz = _opt(dZ, (M, N), dY.dtype, "dZ")
+    db = _new_vector(db, N, dY, "db")
+    work, nbytes = _workspace(work, _act_work_bytes(M, N), dY)
+    _check(lib().linear_bwd_act(_dt(dY), _p(dY), lddy, _p(pre), ldp, a, M, N, _p(dZ), lddz, _p(db), _p(work), nbytes,
+                                _stream()), "linear_bwd_act")
+    return dY if dZ is None else dZ, db
+
+
+def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
+                 out_dtype: torch.dtype = torch.bfloat16, out=None) -> torch.Tensor:
+    """dX = (dZ [M, N] @ W [N, K]) act'(pre): the gradient of linear_fwd's input, and with `act` of the
+    pre-activations [M, K] that the input came from (with 'relu' the input itself does as well).  In place: out may
+    be pre."""
+    M, N = _two(dZ, "dZ")
+    K = _two(W, "W")[1]
+    _here(dZ, W, pre, out)
+    lddz, ldw = _ld(dZ, "dZ"), _matrix(W, (N, K), dZ.dtype, "W")
+    if act != "none" and pre is None:
+        raise ValueError("pre is needed for an activation's gradient")
+    ldp = _opt(pre, (M, K), dZ.dtype, "pre")
+    if out is None:
+        out = dZ.new_empty((M, K), dtype=out_dtype)
+    lddx = _matrix(out, (M, K), None, "out")
+    _check(lib().linear_bwd_x(_dt(dZ), _p(dZ), lddz, _p(W), ldw, _p(pre), ldp, _act(act), M, N, K, _dt(out), _p(out),
+                              lddx, _stream()), "linear_bwd_x")
+    return out
+
+
+def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = torch.float32, out=None,
+                 accumulate: bool = False) -> torch.Tensor:
+    """dW [N, K] = dZ [M, N].T @ X [M, K], the gradient of linear_fwd's weight; with `accumulate` added to `out`
+    (fp32), as micro-batches do."""
+    M, N = _two(dZ, "dZ")
+    K = _two(X, "X")[1]
+    _here(dZ, X, out)
+    lddz, ldx = _ld(dZ, "dZ"), _matrix(X, (M, K), dZ.dtype, "X")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = dZ.new_empty((N, K), dtype=out_dtype)
+    lddw = _matrix(out, (N, K), None, "out")
+    _check(lib().linear_bwd_w(_dt(dZ), _p(dZ), lddz, _p(X), ldx, M, N, K, int(bool(accumulate)), _dt(out), _p(out),
+                              lddw, _stream()), "linear_bwd_w")
+    return out
+
+
+def _packed(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one range of memory, in any order of its dimensions."""
+    n = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda d: d[1]):
+        if size == 1:
+            continue
+        if stride != n:
+            return False
+        n *= size
+    return True
+
+
+def _grads_args(grads, name: str):
+    """The host arrays of a list of tensors: dtypes, addresses, counts."""
+    n = len(grads)
+    if n == 0:
+        raise ValueError(f"{name} must hold a tensor at least")
+    _here(*grads)
+    for t in grads:
+        if t is None:
+            raise TypeError(f"{name} must hold tensors, not None")
+        if not t.is_contiguous() and t.numel() and not _packed(t):
+            raise ValueError(f"{name} must be tensors whose elements lie together in memory")
+    return ((_int * n)(*[_dt(t) for t in grads]), (_vp * n)(*[t.data_ptr() for t in grads]),
+            (_i64 * n)(*[t.numel() for t in grads]))
+
+
+def _grads_work(work, n, counts, like):
+    need = _i64()
+    if isinstance(work, str):
+        _check(lib().grad_work_bytes(n, counts, ctypes.byref(need)), "grad_work_bytes")
+    return _workspace(work, need.value, like)
+
+
+def grad_norm(grads, norm=None, work="auto") -> torch.Tensor:
+    """The norm of all tensors together (bf16 and fp32, any shapes, each packed in memory): one fp32 value [1]."""
+    grads = list(grads)
+    dt, ptr, counts = _grads_args(grads, "grads")
+    _here(norm)
+    norm = _new_vector(norm, 1, grads[0], "norm")
+    work, nbytes = _grads_work(work, len(grads), counts, grads[0])
+    _check(lib().grad_norm(len(grads), dt, ptr, counts, _p(norm), _p(work), nbytes, _stream()), "grad_norm")
+    return norm
+
+
+def grad_clip(grads, max_norm: float, norm=None, out=None, work="auto") -> torch.Tensor:
+    """Scale the gradients so that their norm together is at most max_norm, in place or into the tensors `out` (bf16 or
+    fp32, of the same shapes and order in memory); returns the norm before [1] fp32.  `norm` [1]: a norm that the
+    caller already has (of gradients that lie on several GPUs, say), instead of grad_norm's.  A norm that is
+    not finite leaves the values as they are."""
+    grads = list(grads)
+    dt, ptr, counts = _grads_args(grads, "grads")
+    if out is None:
+        odt, optr = dt, ptr
+    else:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out must hold a tensor for every gradient")
+        odt, optr, _ = _grads_args(out, "out")
+        for g, o in zip(grads, out):
+            if g.shape != o.shape or (g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous())):
+                raise ValueError("out must have the gradients' shapes and orders in memory")
+    have = norm is not None
+    if have:
+        _here(norm)
+        _of(norm, (1,), torch.float32, "norm")
+        work, nbytes = None, 0
+    else:
+        norm = grads[0].new_empty(1, dtype=torch.float32)
+        work, nbytes = _grads_work(work, len(grads), counts, grads[0])
+    _check(lib().grad_clip(len(grads), dt, ptr, counts, float(max_norm), int(have), _p(norm), odt, optr, _p(work), nbytes,
+                           _stream()), "grad_clip")
+    return norm

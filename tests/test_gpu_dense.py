@@ -1,0 +1,502 @@
+"""The dense FFN block's operators against their fp64 oracle (GPU).
+
+Tolerances, from the arithmetic (U = 2^-24, half a step of fp32; half a step of bf16 is 2^-8 of the value, of e4m3
+2^-4 and of e5m2 2^-3, and of their subnormals 2^-10 and 2^-17):
+  norm      a row's squares are added in chains of at most 32, then over 6 + 15 steps: the sum is off by at most
+            (32 + 21 + 3) U of itself, 1 / sqrt by half of that and three roundings, y by three more: 40 U of |y|.
+            Its gradient's mean is off by 60 U of the mean of |g xh|; dw adds a row's terms in chains of
+            T / 512 + 1, over 4 waves and at most 512 groups (8 + 4 + 16 steps).
+  linear    a product of bf16 values is exact in fp32, and each of the K additions rounds or cuts once, at most
+            2 U of the sums so far: (2 K + 4) U of sum |x| |w|; an activation has a slope below 1.2.
+  act       the oracle's bound of the derivative; its column sums add M terms: (M + 4) U of their magnitudes.
+  clip      squares and sums in 64 bits: the norm is rounded once, the factor once more, and the product: 4 U.
+Products of small integers, and norms of exact squares, have to be exact.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_matmul_ffns_amd as nm
+from oracle import dense_oracle as O
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+U = O.U
+TD = {"bf16": torch.bfloat16, "f32": torch.float32}
+T8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+ACTS = ["none", "relu", "gelu_tanh", "silu"]
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def dev(a, dtype="bf16", pad=0, off=0):
+    """float64 array -> (device tensor, the float64 values it holds).  `pad` columns of NaN behind each row, `off`
+    elements in front of the first."""
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(TD[dtype])
+    if not pad and not off:
+        return t.cuda(), t.double().numpy()
+    if t.dim() == 1:
+        flat = torch.full((off + t.numel(),), float("nan"), dtype=t.dtype)
+        flat[off:] = t
+        return flat.cuda()[off:], t.double().numpy()
+    R, C = t.shape
+    flat = torch.full((off + R * (C + pad),), float("nan"), dtype=t.dtype)
+    flat[off:].view(R, C + pad)[:, :C] = t
+    return flat.cuda()[off:].view(R, C + pad)[:, :C], t.double().numpy()
+
+
+def buffer(R, C, dtype, pad=0, off=0, fill=-7.0):
+    """An output [R, C] inside a buffer of known values, and the check that nothing around it was written."""
+    flat = torch.full((off + R * (C + pad) + 64,), fill, dtype=torch.float32, device="cuda").to(dtype)
+    out = flat[off:off + R * (C + pad)].view(R, C + pad)[:, :C]
+    want = flat.float().clone()
+
+    def intact():
+        got = flat.float().clone()
+        got[off:off + R * (C + pad)].view(R, C + pad)[:, :C] = fill
+        return torch.equal(got, want.to(got.dtype))
+    return out, intact
+
+
+def host(t):
+    return t.detach().float().cpu().double().numpy() if t.dtype != torch.float64 else t.cpu().numpy()
+
+
+def half(x, dtype):
+    return np.abs(x) * (2.0 ** -8 if dtype == "bf16" else U) + 1e-37
+
+
+def close(got, want, tol, what=""):
+    err = np.abs(host(got) - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), (what, np.argwhere(bad)[:3].tolist(), float((err / (tol + 1e-300)).max()))
+
+
+def rows(rng, T, D):
+    return rng.normal(size=(T, D)) * np.exp(rng.normal(size=(T, 1))) * np.exp(0.5 * rng.normal(size=(1, D)))
+
+
+# ---- norm ---------------------------------------------------------------------------------------
+NORM = [(1, 1), (1, 4096), (2, 7), (5, 8), (3, 127), (9, 128), (7, 129), (4, 511), (6, 512), (5, 1000), (3, 1111),
+        (2, 2048), (11, 2050), (3, 4099), (2, 8192), (2, 8200), (1, 16384), (2, 16391), (1, 32768), (600, 264), (67, 1024)]
+
+
+@pytest.mark.parametrize("T,D", NORM)
+@pytest.mark.parametrize("dtype,wdtype,res,pad,off", [("bf16", "bf16", True, 0, 0), ("f32", "f32", False, 0, 0),
+                                                      ("bf16", "f32", True, 3, 1), ("f32", "bf16", True, 1, 3),
+                                                      ("bf16", "bf16", False, 8, 0)])
+def test_norm(T, D, dtype, wdtype, res, pad, off):
+    rng = np.random.default_rng(T * 7 + D)
+    X, x = dev(rows(rng, T, D), dtype, pad, off)
+    R, r = dev(rows(rng, T, D), dtype, pad, off) if res else (None, None)
+    W, w = dev(1 + 0.3 * rng.normal(size=D), wdtype, 0, off)
+    Y, intact = buffer(T, D, TD[dtype], pad, off)
+    H, intact_h = buffer(T, D, TD[dtype], pad + 1, off)
+    y, h, rstd = O.rms_norm(x, w, 1e-5, r)
+    gy, gh, gr = nm.rms_norm(X, W, 1e-5, R, H=H if res else None, Y=Y)
+    assert gy is Y and intact() and intact_h()
+    close(gy, y, 40 * U * np.abs(y) + half(y, dtype) * 1.01, "y")
+    close(gr, rstd, 36 * U * rstd, "rstd")
+    if res:
+        assert gh is H
+        close(gh, h, U * np.abs(h) + half(h, dtype), "h")
+    else:
+        assert gh is X
+    # the 8-bit result: the scales' rule on fp32 values, and one rounding
+    for fmt in ("e4m3", "e5m2"):
+        Q, S, _, r8 = nm.rms_norm_fp8(X, W, 1e-5, R, fmt=T8[fmt])
+        s, near = O.scales(y, fmt)
+        gs = host(S)
+        assert (gs == s)[~near].all() and ((gs == s) | (gs == 2 * s) | (2 * gs == s)).all()
+        kp = gs.shape[0] * 128
+        got = host(Q) * np.repeat(gs.T, 128, 1)
+        assert (got[:, D:] == 0).all() and got.shape == (T, kp)
+        step = np.repeat(gs.T, 128, 1)[:, :D]
+        rel, sub = (2.0 ** -4, 2.0 ** -10) if fmt == "e4m3" else (2.0 ** -3, 2.0 ** -17)
+        assert (np.abs(got[:, :D] - y) <= (rel + 60 * U) * np.abs(y) + sub * step).all()
+        assert torch.equal(r8, gr)
+    # the gradients, from what the forward stored
+    DY, dy = dev(rng.normal(size=(T, D)) * 0.02, dtype, pad, off)
+    DH, dh = dev(rng.normal(size=(T, D)) * 0.02, dtype, pad + 1, off) if res else (None, None)
+    hs, rs = host(gh), host(gr)
+    DX, intact_dx = buffer(T, D, TD[dtype], pad, off)
+    DW, intact_dw = buffer(1, D, torch.float32, 0, off)
+    gdx, gdw = nm.rms_norm_bwd(DY, gh, W, gr, dH=DH, dX=DX, dw=DW[0])
+    assert intact_dx() and intact_dw()
+    dx, dw = O.rms_norm_bwd(dy, hs, w, rs, dh)
+    xh, g = np.abs(hs * rs[:, None]), np.abs(dy * w)
+    tol = rs[:, None] * (4 * U * g + xh * 70 * U * (g * xh).mean(1, keepdims=True)) + 4 * U * np.abs(dx)
+    close(gdx, dx, tol + half(dx, dtype) * 1.01 + (0 if dh is None else 2 * U * np.abs(dh)), "dx")
+    close(gdw, dw, (T / 512 + 36) * U * (np.abs(dy) * xh).sum(0) + 1e-37, "dw")
+
+
+def test_norm_in_place_and_repeats():
+    rng = np.random.default_rng(3)
+    X, _ = dev(rows(rng, 33, 1032))
+    R, _ = dev(rows(rng, 33, 1032))
+    W, _ = dev(1 + 0.1 * rng.normal(size=1032))
+    y, h, rstd = nm.rms_norm(X, W, residual=R)
+    x2, r2 = X.clone(), R.clone()
+    y2, h2, rstd2 = nm.rms_norm(x2, W, residual=r2, H=r2, Y=x2)
+    assert y2 is x2 and h2 is r2
+    assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(rstd, rstd2)
+    q, s, h3, _ = nm.rms_norm_fp8(X, W, residual=R, H=R.clone())
+    y3 = torch.empty_like(X)
+    q4, s4, _, _ = nm.rms_norm_fp8(X, W, residual=R, Y=y3)
+    assert torch.equal(y3, y) and torch.equal(h3, h) and torch.equal(q.view(torch.uint8), q4.view(torch.uint8))
+    DY, _ = dev(rng.normal(size=(33, 1032)))
+    DH, _ = dev(rng.normal(size=(33, 1032)))
+    dx, dw = nm.rms_norm_bwd(DY, h, W, rstd, dH=DH)
+    for into in (DY.clone(), DH.clone()):
+        a, b = (into, DH) if torch.equal(into, DY) else (DY, into)
+        dx2, dw2 = nm.rms_norm_bwd(a, h, W, rstd, dH=b, dX=into)
+        assert dx2 is into and torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+def test_norm_extremes():
+    """Rows of zeros, of one huge value, with NaN and infinity: each row by itself."""
+    D = 300
+    x = np.ones((6, D))
+    x[0] = 0
+    x[1] = 1e-30
+    x[2, 5] = 3e18
+    x[3, 7] = np.nan
+    x[4, 9] = np.inf
+    X = torch.from_numpy(x).float().cuda()
+    w = torch.ones(D, device="cuda")
+    y, _, rstd = nm.rms_norm(X, w, eps=1e-5)
+    want = O.rms_norm(x[[0, 1, 2, 5]], np.ones(D), 1e-5)[0]
+    close(y[[0, 1, 2, 5]], want, 48 * U * np.abs(want))
+    assert torch.isnan(y[3]).all() and torch.isnan(y[4, 9]) and (y[4, :9] == 0).all()
+    q, s, _, _ = nm.rms_norm_fp8(X, w, eps=1e-5)
+    q = q.float()
+    assert (q[0] == 0).all() and (s[:, 0] == 1).all()
+    assert torch.isnan(q[3, :D]).all() and (s[:, 3] == 1).all()      # no finite value: scale 1
+    assert torch.isnan(q[4, 9]) and (q[4, :9] == 0).all() and (q[:, D:] == 0).all()
+    assert (s[:, 5] == s[0, 5]).all() and torch.equal(q[5, :D] * s[0, 5], torch.ones(D, device="cuda"))
+
+
+# ---- linear -------------------------------------------------------------------------------------
+SHAPES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (1, 8192, 2048), (16, 256, 512), (17, 130, 264), (33, 64, 1), (64, 64, 64),
+          (65, 127, 72), (128, 128, 128), (100, 300, 1000), (129, 257, 200), (256, 256, 64), (257, 264, 136),
+          (300, 520, 1032), (64, 1111, 777), (512, 512, 320), (2, 4096, 8192), (1000, 1024, 256)]
+
+
+def _ints(rng, *shape):
+    return rng.integers(-4, 5, size=shape).astype(np.float64)
+
+
+def _prod_tol(a, b, K):
+    """a [M, K], b [N, K]: the bound of the sums."""
+    return (2 * K + 4) * U * (np.abs(a) @ np.abs(b).T)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("variant", range(5))
+def test_linear_forward(M, N, K, variant):
+    act, out, bdt, res, pre, pad, off = [
+        ("none", "bf16", None, False, False, 0, 0), ("relu", "f32", "f32", True, True, 0, 0),
+        ("gelu_tanh", "bf16", "bf16", True, True, 8, 0), ("silu", "bf16", "bf16", False, True, 3, 1),
+        ("gelu_tanh", "f32", None, True, False, 16, 8)][variant]
+    rng = np.random.default_rng(M + 3 * N + 5 * K + variant)
+    X, x = dev(rng.normal(size=(M, K)), "bf16", pad, off)
+    W, w = dev(rng.normal(size=(N, K)) * 1.5 / np.sqrt(K), "bf16", pad, off)
+    B, b = dev(rng.normal(size=N), bdt, 0, off) if bdt else (None, None)
+    R, r = dev(rng.normal(size=(M, N)), "bf16", pad, off) if res else (None, None)
+    Y, intact = buffer(M, N, TD[out], pad, off)
+    P, intact_p = buffer(M, N, torch.bfloat16, pad, off)
+    y, z = O.linear(x, w, b, act, r)
+    got = nm.linear_fwd(X, W, bias=B, act=act, residual=R, out=Y, pre=P if pre else None)
+    assert intact() and intact_p()
+    ez = _prod_tol(x, w, K) + 2 * U * np.abs(z)
+    if pre:
+        assert got[0] is Y and got[1] is P
+        close(P, z, ez + half(z, "bf16") * 1.01, "pre")
+    ey = 1.2 * ez + O.act_error(z, act) + 2 * U * np.abs(y)
+    close(Y, y, ey + half(y, out) * 1.01, "y")
+    if M * N * K < 2 ** 20:
+        return
+    again = nm.linear_fwd(X, W, bias=B, act=act, residual=R, out_dtype=TD[out])
+    assert torch.equal(again, Y)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_exact_integers(M, N, K, out):
+    """Small integers: every sum is exact in fp32, so every order of adding gives the same bits."""
+    rng = np.random.default_rng(M + N + K)
+    X, x = dev(_ints(rng, M, K))
+    W, w = dev(_ints(rng, N, K))
+    B, b = dev(_ints(rng, N))
+    R, r = dev(_ints(rng, M, N))
+    rnd = (lambda v: torch.from_numpy(v).to(TD[out]).double().numpy())
+    assert np.array_equal(host(nm.linear_fwd(X, W, out_dtype=TD[out])), rnd(x @ w.T))
+    y, z = O.linear(x, w, b, "relu", r)
+    gy, gz = nm.linear_fwd(X, W, bias=B, act="relu", residual=R, out_dtype=TD[out], return_pre=True)
+    assert np.array_equal(host(gy), rnd(y))
+    assert np.array_equal(host(gz), torch.from_numpy(z).bfloat16().double().numpy())
+    # the gradients' products: dZ [M, N] W [N, K], gated, and dZ^T X
+    D, d = dev(_ints(rng, M, N))
+    G, g = dev(_ints(rng, M, K))
+    assert np.array_equal(host(nm.linear_bwd_x(D, W, out_dtype=TD[out])), rnd(d @ w))
+    assert np.array_equal(host(nm.linear_bwd_x(D, W, pre=G, act="relu", out_dtype=TD[out])), rnd((d @ w) * (g > 0)))
+    assert np.array_equal(host(nm.linear_bwd_w(D, X, out_dtype=TD[out])), rnd(d.T @ x))
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("act,out,pad,off", [("none", "bf16", 0, 0), ("gelu_tanh", "bf16", 8, 0), ("silu", "f32", 3, 1),
+                                             ("relu", "f32", 16, 8)])
+def test_linear_gradients(M, N, K, act, out, pad, off):
+    rng = np.random.default_rng(M + 5 * N + 3 * K + len(act))
+    D, d = dev(rng.normal(size=(M, N)), "bf16", pad, off)
+    W, w = dev(rng.normal(size=(N, K)) / np.sqrt(N), "bf16", pad, off)
+    X, x = dev(rng.normal(size=(M, K)), "bf16", pad, off)
+    P, p = dev(2 * rng.normal(size=(M, K)), "bf16", pad, off) if act != "none" else (None, None)
+    DX, intact = buffer(M, K, TD[out], pad, off)
+    assert nm.linear_bwd_x(D, W, pre=P, act=act, out=DX) is DX and intact()
+    full = d @ w
+    slope = O.dact(p, act) if p is not None else np.ones_like(full)
+    tol = np.abs(slope) * _prod_tol(d, w.T, N)
+    if p is not None:
+        tol = tol + O.dact_error(p, act) * np.abs(full)
+    dx = full * slope
+    close(DX, dx, tol + 2 * U * np.abs(dx) + half(dx, out) * 1.01, "dx")
+    DW, intact = buffer(N, K, torch.float32, pad, off)
+    assert nm.linear_bwd_w(D, X, out=DW) is DW and intact()
+    dw, tol = d.T @ x, _prod_tol(d.T, x.T, M)
+    close(DW, dw, tol + U * np.abs(dw) + 1e-37, "dw")
+    before = DW.clone()
+    nm.linear_bwd_w(D, X, out=DW, accumulate=True)
+    assert intact()
+    assert torch.equal(DW, before + before)      # the same sums, doubled exactly
+    DWb, intact = buffer(N, K, torch.bfloat16, pad, off)
+    nm.linear_bwd_w(D, X, out=DWb)
+    assert intact() and torch.equal(DWb, before.bfloat16())
+
+
+def test_linear_in_place():
+    rng = np.random.default_rng(9)
+    for M, N, K in ((5, 24, 40), (300, 264, 136)):
+        X, _ = dev(rng.normal(size=(M, K)))
+        W, _ = dev(rng.normal(size=(N, K)))
+        R, _ = dev(rng.normal(size=(M, N)))
+        y = nm.linear_fwd(X, W, act="silu", residual=R)
+        r2 = R.clone()
+        assert nm.linear_fwd(X, W, act="silu", residual=r2, out=r2) is r2 and torch.equal(r2, y)
+        P, _ = dev(rng.normal(size=(M, K)))
+        dx = nm.linear_bwd_x(R, W, pre=P, act="gelu_tanh")
+        p2 = P.clone()
+        assert nm.linear_bwd_x(R, W, pre=p2, act="gelu_tanh", out=p2) is p2 and torch.equal(p2, dx)
+        dz, db = nm.linear_bwd_act(P, X, act="gelu_tanh")
+        for i in (0, 1):
+            a, b = P.clone(), X.clone()
+            into = (a, b)[i]
+            dz2, db2 = nm.linear_bwd_act(a, b, act="gelu_tanh", dZ=into)
+            assert dz2 is into and torch.equal(dz2, dz) and torch.equal(db2, db)
+
+
+@pytest.mark.parametrize("kind", ACTS)
+def test_activation_over_its_range(kind):
+    """Every finite bf16 value as a pre-activation: forward through an identity product, and the
+    derivative; infinities and NaN by themselves."""
+    bits = np.arange(0, 0x7F80, dtype=np.uint16)
+    z = torch.from_numpy(np.concatenate([bits, bits | 0x8000]).view(np.int16)).view(torch.bfloat16)
+    n = z.numel() // 16 * 16
+    z = z[:n].view(16, -1).cuda()
+    eye = torch.eye(16, device="cuda").bfloat16()
+    z64 = z.double().cpu().numpy()
+    got = nm.linear_fwd(eye, z.t().contiguous(), act=kind, out_dtype=torch.float32)
+    want = O.act(z64, kind)
+    close(got, want, O.act_error(z64, kind) + U * np.abs(want) + 1e-36, kind)
+    one = torch.ones_like(z)
+    dz, _ = nm.linear_bwd_act(one, z, act=kind, dZ=torch.empty_like(z))
+    d = O.dact(z64, kind)
+    close(dz, d, O.dact_error(z64, kind) + half(d, "bf16") * 1.01 + 1e-36, kind)
+    odd = torch.tensor([[float("nan"), float("inf")]], device="cuda").bfloat16()
+    g = nm.linear_bwd_act(torch.ones_like(odd), odd, act=kind, dZ=torch.empty_like(odd))[0]
+    assert g[0, 1] == 1 and (torch.isnan(g[0, 0]) if kind in ("gelu_tanh", "silu") else True)
+
+
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 4096), (7, 9), (33, 255), (64, 256), (70, 257), (1000, 1111), (2500, 64)])
+@pytest.mark.parametrize("act,pad,off", [("gelu_tanh", 0, 0), ("relu", 3, 1), ("silu", 8, 0), ("none", 0, 0)])
+def test_act_gradient(M, N, act, pad, off):
+    rng = np.random.default_rng(M + N)
+    DY, dy = dev(rng.normal(size=(M, N)), "bf16", pad, off)
+    P, p = dev(2 * rng.normal(size=(M, N)), "bf16", pad, off)
+    Z, intact = buffer(M, N, torch.bfloat16, pad, off)
+    B, intact_b = buffer(1, N, torch.float32, 0, off)
+    gz, gb = nm.linear_bwd_act(DY, P, act=act, dZ=Z, db=B[0])
+    assert intact() and intact_b() and gz is Z
+    dz = dy * O.dact(p, act)
+    tol = np.abs(dy) * O.dact_error(p, act) + U * np.abs(dz)
+    close(gz, dz, tol + half(dz, "bf16") * 1.01, "dz")
+    close(gb, dz.sum(0), tol.sum(0) + (M + 4) * U * np.abs(dz).sum(0) + 1e-37, "db")
+    if act == "none":
+        same, gb2 = nm.linear_bwd_act(DY)
+        assert same is DY and torch.equal(gb2, gb)
+
+
+# ---- gradients' norm and clipping ---------------------------------------------------------------
+LISTS = [[(1,)], [(0,), (3, 5)], [(16384,), (16385,), (16383,)], [(7, 9), (1,), (0, 4), (1000, 33), (64,)],
+         [(i + 1, 3) for i in range(200)], [(70000, 41), (5,)], [(300, 1000)] * 97]
+
+
+@pytest.mark.parametrize("shapes", range(len(LISTS)))
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "mixed"])
+@pytest.mark.parametrize("off", [0, 1])
+def test_clip(shapes, dtype, off):
+    rng = np.random.default_rng(shapes)
+    gs, vs = [], []
+    for i, s in enumerate(LISTS[shapes]):
+        dt = dtype if dtype != "mixed" else ("bf16", "f32")[i % 2]
+        t = torch.from_numpy(rng.normal(size=s) * (1 + i % 5)).to(TD[dt])
+        flat = torch.full((off + t.numel() + 3,), 5.0, dtype=t.dtype, device="cuda")
+        v = flat[off:off + t.numel()].view(t.shape)
+        v.copy_(t)
+        gs.append((flat, v, dt))
+        vs.append(t.double().numpy())
+    grads = [v for _, v, _ in gs]
+    want = O.grad_norm(vs)
+    norm = nm.grad_norm(grads)
+    assert norm.shape == (1,) and abs(float(norm) - want) <= 2 * U * want
+    for ratio, odt in ((2.0, "f32"), (0.25, "f32"), (0.25, "bf16")):
+        f = O.grad_factor(want, ratio * want)
+        out = [torch.full_like(v, 9.0, dtype=TD[odt]) for v in grads]
+        keep = [v.clone() for v in grads]
+        got = nm.grad_clip(grads, ratio * want, out=out)
+        assert torch.equal(got, norm) and all(torch.equal(a, b) for a, b in zip(grads, keep))
+        for o, x in zip(out, vs):
+            close(o, f * x, 4 * U * np.abs(f * x) + half(f * x, odt) * 1.01)
+    f = O.grad_factor(want, 0.5 * want)
+    given = torch.full((1,), want, device="cuda")
+    second = [v.clone() for v in grads]
+    nm.grad_clip(second, 0.5 * want, norm=given)
+    nm.grad_clip(grads, 0.5 * want)
+    for (flat, v, dt), x, s in zip(gs, vs, second):
+        close(v, f * x, 4 * U * np.abs(f * x) + half(f * x, dt) * 1.01)
+        close(s, f * x, 4 * U * np.abs(f * x) + half(f * x, dt) * 1.01)
+        assert bool((flat[:off] == 5).all()) and bool((flat[off + v.numel():] == 5).all())
+
+
+def test_clip_range_and_not_finite():
+    """Squares beyond fp32's range on both sides; a norm that is not finite changes nothing."""
+    g = [torch.full((5,), 3e38, device="cuda"), torch.full((7,), 1e-30, device="cuda")]
+    assert torch.isinf(nm.grad_norm(g))                 # 6.7e38 is beyond fp32
+    keep = [t.clone() for t in g]
+    nm.grad_clip(g, 1.0)
+    assert all(torch.equal(a, b) for a, b in zip(g, keep))
+    big = [torch.full((4,), 1e38, device="cuda")]
+    assert abs(float(nm.grad_norm(big)) - 2e38) < 1e31
+    nm.grad_clip(big, 1.0)
+    close(big[0], np.full(4, 0.5), 8 * U)
+    small = [torch.full((4,), 2.0 ** -140, device="cuda")]
+    assert float(nm.grad_norm(small)) == 2.0 ** -139
+    for bad in (float("nan"), float("inf")):
+        t = torch.tensor([1.0, bad, 2.0], device="cuda")
+        o = torch.zeros(3, device="cuda")
+        n = nm.grad_clip([t], 0.1, out=[o])
+        assert not torch.isfinite(n).any() and torch.equal(o[[0, 2]], t[[0, 2]]) and str(o[1]) == str(t[1])
+    z = [torch.zeros(3, device="cuda")]
+    assert float(nm.grad_clip(z, 0.0)) == 0.0
+    t = torch.tensor([3.0, 4.0], device="cuda")
+    assert float(nm.grad_clip([t], 0.0)) == 5.0 and (t == 0).all()
+    t = torch.tensor([3.0, 4.0], device="cuda")
+    nm.grad_clip([t], float("inf"))
+    assert t.tolist() == [3.0, 4.0]
+    empty = [torch.empty(0, device="cuda")]
+    assert float(nm.grad_clip(empty, 1.0)) == 0.0
+    # another order in memory, the same tensor twice as an input only
+    a = torch.randn(6, 5, device="cuda").t()
+    want = float(a.double().norm()) * 2 ** 0.5
+    assert abs(float(nm.grad_norm([a, a])) - want) <= 2 * U * want
+    o = [torch.empty(6, 5, device="cuda").t(), torch.empty(6, 5, device="cuda").t()]
+    nm.grad_clip([a, a], want / 2, out=o)
+    close(o[0], host(a) / 2, 4 * U * np.abs(host(a))), close(o[1], host(a) / 2, 4 * U * np.abs(host(a)))
+
+
+# ---- streams, graphs, refusals that need a device -----------------------------------------------
+def _block(x, r, w, wu, bu, wd, bd, dy):
+    y, h, rstd = nm.rms_norm(x, w, residual=r)
+    a, z = nm.linear_fwd(y, wu, bias=bu, act="gelu_tanh", return_pre=True)
+    out = nm.linear_fwd(a, wd, bias=bd, residual=h)
+    _, db2 = nm.linear_bwd_act(dy)
+    dwd = nm.linear_bwd_w(dy, a)
+    dz = nm.linear_bwd_x(dy, wd, pre=z, act="gelu_tanh")
+    _, db1 = nm.linear_bwd_act(dz)
+    dwu = nm.linear_bwd_w(dz, y)
+    dn = nm.linear_bwd_x(dz, wu)
+    dx, dw = nm.rms_norm_bwd(dn, h, w, rstd, dH=dy)
+    grads = [dw, dwu, db1, dwd, db2]
+    norm = nm.grad_clip(grads, 0.5)
+    return [out, dx, norm, *grads]
+
+
+def _block_inputs(T, D, F, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).bfloat16()
+    return [rnd(T, D), rnd(T, D), 1 + rnd(D, std=0.1), rnd(F, D, std=D ** -0.5), rnd(F, std=0.1),
+            rnd(D, F, std=F ** -0.5), rnd(D, std=0.1), rnd(T, D, std=0.1)]
+
+
+@pytest.mark.parametrize("T,D,F", [(1, 64, 256), (130, 256, 520), (512, 512, 1024), (37, 100, 333)])
+def test_the_block_on_streams_and_in_graphs(T, D, F):
+    args = _block_inputs(T, D, F)
+    want = _block(*args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _block(*args)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs = []
+    for _ in range(2):                     # two graphs, with work memory of their own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = _block(*args)
+        graphs.append((g, res))
+    for i in range(4):
+        for t, v in zip(args, _block_inputs(T, D, F, seed=i)):
+            t.copy_(v)
+        want = _block(*args)
+        for g, res in graphs:
+            for t in res:
+                t.fill_(float("nan"))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, res in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(res, want)), i
+
+
+def test_binding_refuses():
+    x = torch.zeros(4, 16, device="cuda").bfloat16()
+    w = torch.ones(16, device="cuda")
+    with pytest.raises(ValueError):
+        nm.rms_norm(x.cpu(), w)
+    with pytest.raises(ValueError):
+        nm.rms_norm(x, w[:8])
+    with pytest.raises(ValueError):
+        nm.rms_norm(x.t(), w)
+    with pytest.raises(TypeError):
+        nm.rms_norm(x, w, residual=x.float())
+    with pytest.raises(nm.NmError):
+        nm.rms_norm(x, w, eps=0.0)
+    with pytest.raises(nm.NmError):
+        nm.rms_norm(torch.zeros(1, 32769, device="cuda"), torch.ones(32769, device="cuda"))
+    with pytest.raises(nm.NmError):
+        nm.linear_fwd(x.float(), x.float())
+    t = torch.ones(8, device="cuda")
+    with pytest.raises(nm.NmError):
+        nm.grad_clip([t, t], 1.0)                     # the same tensor twice, in place
+    with pytest.raises(nm.NmError):
+        nm.grad_clip([t[:5], t[4:]], 1.0)
+    with pytest.raises(ValueError):
+        nm.grad_clip([torch.ones(8, 8, device="cuda")[:, :4]], 1.0)
+    with pytest.raises(nm.NmError):
+        nm.grad_clip([t], float("nan"))
+    assert (t == 1).all()

@@ -642,7 +642,7 @@ nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int
     return NM_ERR_ALIGN;
   const nms::Linear g{(const uint16_t*)X, ldx, (const uint16_t*)W, ldw, 0, 0, M, N, K, Y, ldy, out == NM_BF16,
                       nms::EPI_FWD, bias, bdt == NM_BF16, act, (const uint16_t*)residual, ldr, (uint16_t*)pre, ldp,
-                      nullptr, 0, 0};
+                      nullptr, 0};
   return hip_status(nms::launch_linear(g, hs(stream)));
 }
 
@@ -680,7 +680,7 @@ nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W,
   // rows of dZ times columns of W: the product's columns are W's, its reduction runs over W's rows
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)W, ldw, 0, 1, M, K, N, dX, lddx, out == NM_BF16,
                       act == NM_ACT_NONE ? nms::EPI_PLAIN : nms::EPI_GATE, nullptr, 0, act, nullptr, 0, nullptr, 0,
-                      (const uint16_t*)pre, ldp, 0};
+                      (const uint16_t*)pre, ldp};
   return hip_status(nms::launch_linear(g, hs(stream)));
 }
 
@@ -691,7 +691,7 @@ nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X,
   if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldx < K || lddw < K) return NM_ERR_SHAPE;
   if (!aligned(dZ, 2) || !aligned(X, 2) || !aligned(dW, esize(out))) return NM_ERR_ALIGN;
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)X, ldx, 1, 1, N, K, M, dW, lddw, out == NM_BF16,
-                      nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0, accumulate != 0};
+                      accumulate ? nms::EPI_ADD : nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0};
   return hip_status(nms::launch_linear(g, hs(stream)));
 }
 

@@ -243,7 +243,8 @@ int64_t act_bwd_groups(int64_t M, int64_t N);
 hipError_t launch_linear_bwd_act(const ActBwdArgs& a, hipStream_t s);
 // C[m][n] = sum over k of A(m, k) B(n, k), bf16 operands: A(m, k) at A[m * lda + k], or with a_t at
 // A[k * lda + m]; B alike.
-enum { EPI_FWD = 0, EPI_GATE = 1, EPI_PLAIN = 2 };
+// EPI_ADD: added to C, which is fp32 then.
+enum { EPI_FWD = 0, EPI_GATE = 1, EPI_PLAIN = 2, EPI_ADD = 3 };
 struct Linear {
   const uint16_t* A;
   int64_t lda;
@@ -262,7 +263,6 @@ struct Linear {
   int64_t ldz;
   const uint16_t* P;        // EPI_GATE: the activation's derivative at P
   int64_t ldp;
-  int accumulate;           // EPI_PLAIN: added to C (fp32)
 };
 hipError_t launch_linear(const Linear& g, hipStream_t s);
 struct Grads {

@@ -4,6 +4,7 @@
 // Every kernel gives B the matrix instruction's row operand and A its column operand, so a lane holds four
 // consecutive columns n of one row m of C.
 #include "act.hpp"
+#include "dma.hpp"
 #include "launch.hpp"
 #include "pieces.hpp"
 
@@ -85,7 +86,7 @@ __device__ inline f32x4 epilogue4(const Linear& g, int64_t m, int64_t n, f32x4 v
     if (g.R) v += load4(g.R + m * g.ldr, n, g.N);
   } else if (g.epi == EPI_GATE) {
     v *= dact4(g.act, load4(g.P + m * g.ldp, n, g.N));
-  } else if (g.accumulate) {
+  } else if (g.epi == EPI_ADD) {
     v += load4((const float*)g.C + m * g.ldc, n, g.N);
   }
   return v;
@@ -167,7 +168,403 @@ hipError_t run_general(const Linear& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t linear_piece(const Linear& g, hipStream_t s) { return run_general(g, s); }
+// ---------------------------------------------------------------------------
+// Tiled kernel: BM x BN tiles of C by four waves (2 x 2) of 16 FM x 16 FN, 64-k stages of both operands in
+// two LDS buffers filled by direct-to-LDS loads.
+//
+// An operand lies in LDS as it does in memory:
+//   reduction contiguous   a row of C per 128-byte LDS row, its 16-byte chunk c at slot c ^ (row / 2 % 8): sixteen
+//                          rows' reads of one chunk cover all 64 banks once; a fragment is one 16-byte read;
+//   reduction strided      a k per LDS row of 2 BM bytes, its 32-byte segment s (16 columns: a fragment's) at
+//                          s ^ (k % 4 + 4 (k / 8 % 2)).  The transposing read gives a lane four k of one column from
+//                          four rows; a read's half wave touches eight rows (k % 4 and k / 8 % 2 all different), so
+//                          eight segments in different banks; a fragment is two reads.
+// A stage is two sub-steps of FM x FN matrix instructions (32 k each); between them the wave reads the
+// operands of the next sub-step, and issues the loads of the stages after.  The barrier sits between the two
+// sub-steps: by then every wave has read all of the stage, so the second sub-step reads the next stage's first operands,
+// and the buffer just left takes half of the loads of the stage after next; the other half follow in the next
+// stage's first sub-step.  Rows and columns beyond the operands, and k beyond K, are zeros: a lane's
+// 16 bytes lie inside the operand or outside (the contiguous sizes are multiples of eight), and outside its offset
+// is moved beyond the descriptor's size, where nothing is read.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kOutside = 0x80000000u;   // added to an offset: beyond every descriptor's size
+
+template <int FM_, int FN_>
+struct LinCfg {
+  static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN;
+  static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
+  static constexpr int LA = BM / 32, LB = BN / 32, LOADS = LA + LB;   // 1 KB loads a wave and stage
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Where a wave's loads of one operand come from, and where a lane's fragments lie in LDS.
+template <bool T, int BR, int LN>
+struct Operand {
+  static constexpr int ROW = T ? 2 * BR : 128;    // bytes of an LDS row
+  const uint16_t* base;
+  int64_t step;          // elements from a stage to the next
+  int64_t K;
+  uint32_t width;        // T: bytes of the tile's columns that exist
+  uint32_t ldb;          // bytes of a row
+  uint32_t off[LN];      // of this wave's loads, this lane
+  int c[2];              // not T: the lane's chunk in the even and the odd loads
+  __device__ void init(const uint16_t* X, int64_t ld, int64_t r0, int64_t R, int64_t K_, int wave, int lane) {
+    K = K_;
+    ldb = (uint32_t)(2 * ld);
+    if constexpr (T) {
+      base = X + r0;
+      step = 64 * ld;
+      width = (uint32_t)(2 * (R - r0 < BR ? R - r0 : BR));
+#pragma unroll
+      for (int t = 0; t < LN; ++t) {
+        const int at = (wave * LN + t) * 1024 + lane * 16, k = at / ROW, chunk = at % ROW / 16;
+        const uint32_t col = 32 * ((chunk >> 1) ^ ((k & 3) | (k >> 3 & 1) << 2)) + 16 * (chunk & 1);
+        off[t] = k * ldb + col + (col < width ? 0u : kOutside);
+      }
+    } else {
+      base = X + r0 * ld;
+      step = 64;
+      c[0] = (lane & 7) ^ (lane >> 4);
+      c[1] = c[0] ^ 4;
+#pragma unroll
+      for (int t = 0; t < LN; ++t) {
+        const int r = 8 * (wave * LN + t) + (lane >> 3);
+        off[t] = r * ldb + 16 * c[t & 1] + (r0 + r < R ? 0u : kOutside);
+      }
+    }
+  }
+  // stage kt's descriptor; nothing is read of a stage behind the last
+  __device__ u32x4 desc(int kt) const {
+    const int64_t left = K - (int64_t)kt * 64;
+    uint32_t bytes = left > 0 ? kOutside : 0u;
+    if constexpr (T) bytes = left > 0 ? (uint32_t)((left < 64 ? left : 64) - 1) * ldb + width : 0u;
+    return buffer_desc(base + kt * step, bytes);
+  }
+  // what the offsets of the even and the odd loads of stage kt carry besides
+  __device__ void tail(int kt, uint32_t (&m)[2]) const {
+    m[0] = m[1] = 0;
+    if constexpr (!T) {
+      const int64_t left = K - (int64_t)kt * 64;
+      if (left < 64) {
+        m[0] = 8 * c[0] < left ? 0u : kOutside;
+        m[1] = 8 * c[1] < left ? 0u : kOutside;
+      }
+    }
+  }
+  // a lane's address in LDS of fragment 0's operand of sub-step 0, `first` the wave's first row or column
+  __device__ static uint32_t lds0(uint32_t part, int first, int lane) {
+    const int l16 = lane & 15, lq = lane >> 4;
+    if constexpr (T) {
+      const int k = 8 * lq + (l16 >> 2);
+      return part + k * ROW + 32 * ((first >> 4) ^ ((k & 3) | (k >> 3 & 1) << 2)) + 8 * (l16 & 3);
+    }
+    return part + (first + l16) * 128 + ((lq ^ ((l16 >> 1) & 7)) << 4);
+  }
+  // fragment i of sub-step kk
+  __device__ static bf16x8 frag(uint32_t at, int kk, int i) {
+    if constexpr (T) {
+      // segment first / 16 + i: first is a multiple of 16 fragments' width, so its low bits are i's alone
+      const uint32_t a = (at ^ (uint32_t)(32 * i)) + kk * 32 * ROW;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ROW));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+    return *(lds_bf16x8*)((at ^ (uint32_t)(64 * kk)) + i * 2048);
+  }
+};
+
+// A wave's FM x FN fragments to C, by way of LDS (`region`: the wave's quarter of the stages' buffers): a lane then
+// holds four consecutive columns of rows lane / 16, and 16 lanes 64 columns, so every load and store of C and
+// of what lies like C takes whole 128-byte lines of bf16, and the code is one small loop over the rows.  Row r's 16-byte
+// chunk c lies at c ^ (r % 16): a fragment's rows are written to different banks, and read in order.
+template <int EPI, int FM, int FN>
+__device__ inline void tile_epilogue(const Linear& g, const f32x4 (&acc)[FM][FN], unsigned char* region, int64_t m0,
+                                     int64_t n0, int lane) {
+  constexpr int COLS = 16 * FN, H = COLS / 64;               // H: runs of 64 columns
+  constexpr int ROWS = (FM + FN) * 2048 / (COLS * 4);        // of a pass: the wave's quarter of 2 x 32 (FM + FN) rows of 128 bytes
+  static_assert(ROWS % 16 == 0 && 16 * FM % ROWS == 0, "a pass is whole fragments");
+  constexpr int PF = ROWS / 16, U = 4;                       // U: rows of a lane in flight together
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int64_t n = n0 + 4 * l16;
+  f32x4 bias[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    bias[h] = EPI == EPI_FWD && n + 64 * h < g.N ? bias4(g, n + 64 * h) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int p = 0; p < FM / PF; ++p) {
+#pragma unroll
+    for (int i = 0; i < PF; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        *reinterpret_cast<f32x4*>(region + (16 * i + l16) * (COLS * 4) + ((4 * j + lq) ^ l16) * 16) = acc[p * PF + i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // other lanes of this wave read it
+    const int64_t mp = m0 + p * ROWS;
+    const int rows = g.M - mp < ROWS ? (int)(g.M - mp) : ROWS;
+    for (int r0 = 0; r0 < rows; r0 += 4 * U) {
+      f32x4 x[U][H];   // what is added to C, or gates it
+      auto each = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (r0 + 4 * u + lq < rows && n + 64 * h < g.N) f(u, h, mp + r0 + 4 * u + lq, n + 64 * h);
+      };
+      if constexpr (EPI == EPI_FWD) {
+        if (g.R) each([&](int u, int h, int64_t m, int64_t c) { x[u][h] = load4(g.R + m * g.ldr, c, g.N); });
+      }
+      if constexpr (EPI == EPI_GATE) each([&](int u, int h, int64_t m, int64_t c) { x[u][h] = load4(g.P + m * g.ldp, c, g.N); });
+      if constexpr (EPI == EPI_ADD) each([&](int u, int h, int64_t m, int64_t c) { x[u][h] = load4((const float*)g.C + m * g.ldc, c, g.N); });
+      each([&](int u, int h, int64_t m, int64_t c) {
+        const int r = r0 + 4 * u + lq;
+        f32x4 v = *reinterpret_cast<const f32x4*>(region + r * (COLS * 4) + ((16 * h + l16) ^ (r & 15)) * 16);
+        if constexpr (EPI == EPI_FWD) {
+          v += bias[h];
+          if (g.Z) store4(g.Z + m * g.ldz, c, g.N, v);
+          v = act4(g.act, v);
+          if (g.R) v += x[u][h];
+        }
+        if constexpr (EPI == EPI_GATE) v *= dact4(g.act, x[u][h]);
+        if constexpr (EPI == EPI_ADD) v += x[u][h];
+        if (g.bf16_out) store4((uint16_t*)g.C + m * g.ldc, c, g.N, v);
+        else store4((float*)g.C + m * g.ldc, c, g.N, v);
+      });
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // before the next pass's values
+  }
+}
+
+template <bool AT, bool BT, int EPI, typename Cfg>
+__global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(Linear g) {
+  constexpr int FM = Cfg::FM, FN = Cfg::FN, LA = Cfg::LA, LB = Cfg::LB, LOADS = Cfg::LOADS;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave >> 1) * 16 * FM, wn = (wave & 1) * 16 * FN;
+  const int ntm = (int)((g.M + Cfg::BM - 1) / Cfg::BM), ntn = (int)((g.N + Cfg::BN - 1) / Cfg::BN);
+  int tm, tn;
+  panel_major_tile(blockIdx.x, ntm, ntn, 4, tm, tn);
+  const int64_t m0 = (int64_t)(int)uniform((uint32_t)(tm * Cfg::BM)), n0 = (int64_t)(int)uniform((uint32_t)(tn * Cfg::BN));
+  const int KT = (int)((g.K + 63) / 64);
+
+  Operand<AT, Cfg::BM, LA> A;
+  Operand<BT, Cfg::BN, LB> B;
+  A.init(g.A, g.lda, m0, g.M, g.K, wave, lane);
+  B.init(g.B, g.ldb, n0, g.N, g.K, wave, lane);
+  const uint32_t lds_base = uniform(lds_addr(smem));
+  uint32_t at_a = A.lds0(lds_base, wm, lane), at_b = B.lds0(lds_base + Cfg::A_BYTES, wn, lane);
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // load t of a wave (A's LA first) of the stage that the descriptors and tails stand for, into LDS buffer buf
+  auto dma = [&](int t, int buf, const u32x4& da, const u32x4& db, const uint32_t (&ta)[2], const uint32_t (&tb)[2]) {
+    const uint32_t to = lds_base + buf * Cfg::STAGE;
+    if (t < LA) dma16b(A.off[t < LA ? t : 0] | ta[t & 1], da, uniform(to + (wave * LA + t) * 1024));
+    else dma16b(B.off[t < LA ? 0 : t - LA] | tb[(t - LA) & 1], db, uniform(to + Cfg::A_BYTES + (wave * LB + t - LA) * 1024));
+  };
+  // one sub-step on (a, b); the next operands (kk, at pa and pb) are read into an and bn between its instructions, and
+  // loads first .. first + LOADS / 2 - 1 of stage kt are issued into buf
+  auto substep = [&](const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], int kk, uint32_t pa, uint32_t pb, bf16x8 (&an)[FM],
+                     bf16x8 (&bn)[FN], int kt, int first, int buf) {
+    constexpr int N = FM * FN, READ = N / (FM + FN), LOAD = N / 2 / (LOADS / 2);
+    const u32x4 da = A.desc(kt), db = B.desc(kt);
+    uint32_t ta[2], tb[2];
+    A.tail(kt, ta);
+    B.tail(kt, tb);
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      const int j = m / FM, i = m % FM;
+      // tied in and out of the instruction in the accumulation registers (as a builtin, the compiler moves the
+      // small accumulators between registers every stage)
+      asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(b[j]), "v"(a[i]));
+      __builtin_amdgcn_sched_barrier(0);
+      if (m % READ == 0) {
+        const int q = m / READ;
+        if (q < FM) an[q < FM ? q : 0] = A.frag(pa, kk, q);
+        else if (q < FM + FN) bn[q < FM ? 0 : q - FM] = B.frag(pb, kk, q - FM);
+      }
+      if (m % LOAD == LOAD / 2 && m / LOAD < LOADS / 2) dma(first + m / LOAD, buf, da, db, ta, tb);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  {
+    u32x4 da = A.desc(0), db = B.desc(0);
+    uint32_t ta[2], tb[2];
+    A.tail(0, ta);
+    B.tail(0, tb);
+#pragma unroll
+    for (int t = 0; t < LOADS; ++t) dma(t, 0, da, db, ta, tb);
+    da = A.desc(1);
+    db = B.desc(1);
+    A.tail(1, ta);
+    B.tail(1, tb);
+#pragma unroll
+    for (int t = 0; t < LOADS / 2; ++t) dma(t, 1, da, db, ta, tb);
+  }
+  wait_vmcnt<LOADS / 2>();   // stage 0
+  lds_barrier();
+  bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) a0[i] = A.frag(at_a, 0, i);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) b0[j] = B.frag(at_b, 0, j);
+  for (int kt = 0; kt < KT; ++kt) {
+    const int buf = kt & 1;
+    substep(a0, b0, 1, at_a, at_b, a1, b1, kt + 1, LOADS / 2, buf ^ 1);
+    wait_vmcnt<0>();   // this wave's loads of stage kt + 1
+    lds_barrier();     // every wave's; and every wave has read all it needs of stage kt
+    at_a += buf ? -Cfg::STAGE : Cfg::STAGE;
+    at_b += buf ? -Cfg::STAGE : Cfg::STAGE;
+    substep(a1, b1, 0, at_a, at_b, a0, b0, kt + 2, 0, buf);
+  }
+  wait_vmcnt<0>();   // no load may land in LDS after the workgroup ends
+  // the last instructions' results before any other instruction reads them (the compiler does not see
+  // the instructions inside the assembly statements)
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+  lds_barrier();   // every wave has read its last operands: the buffers are free
+  tile_epilogue<EPI>(g, acc, smem + wave * (Cfg::STAGE / 2), m0 + wm, n0 + wn, lane);
+}
+
+template <bool AT, bool BT, int EPI, typename Cfg>
+hipError_t run_tile(const Linear& g, hipStream_t s) {
+  auto kern = linear_tile_kernel<AT, BT, EPI, Cfg>;
+  (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * Cfg::STAGE);
+  const int64_t wgs = (g.M + Cfg::BM - 1) / Cfg::BM * ((g.N + Cfg::BN - 1) / Cfg::BN);
+  if (!grid_ok(wgs, 256)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), 2 * Cfg::STAGE, s, g);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of A (serving): B is read once and that bounds the call, so its bytes go straight from memory to
+// the registers of the matrix instruction, with no LDS and no barrier on the way.  A workgroup computes 16 FM rows of A by
+// 32 rows of B; its KS waves take every KS-th chunk of 128 k, each with the next chunk's loads in flight, and
+// add their sums through LDS in the order of the waves.  The lanes of a row that does not exist load nothing.
+// ---------------------------------------------------------------------------
+template <int FM, int KS>
+__global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
+  constexpr int FN = 2, CH = 4;   // CH: matrix instructions (32 k each) a chunk and fragment pair
+  __shared__ f32x4 part[KS][FM * FN][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int ntn = (int)((g.N + 31) / 32);
+  const int64_t m0 = (int64_t)(blockIdx.x / ntn) * (16 * FM), n0 = (int64_t)(blockIdx.x % ntn) * 32;
+  const uint16_t *arow[FM], *brow[FN];
+  bool aon[FM], bon[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + 16 * i + l16;
+    aon[i] = m < g.M;
+    arow[i] = g.A + (aon[i] ? m : m0) * g.lda + 8 * lq;
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int64_t n = n0 + 16 * j + l16;
+    bon[j] = n < g.N;
+    brow[j] = g.B + (bon[j] ? n : n0) * g.ldb + 8 * lq;
+  }
+  struct Chunk {
+    u32x4 a[CH][FM], b[CH][FN];
+  };
+  const int64_t kl = g.K - 8 * lq;   // K is a multiple of eight: a lane's eight k exist or do not
+  auto load16 = [&](const uint16_t* p, bool on, int64_t k) {
+    u32x4 v = {0, 0, 0, 0};
+    if (on && k < kl) v = *reinterpret_cast<const u32x4*>(p + k);
+    return v;
+  };
+  auto load = [&](int64_t c, Chunk& x) {
+#pragma unroll
+    for (int u = 0; u < CH; ++u) {
+      const int64_t k = (c * CH + u) * 32;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) x.b[u][j] = load16(brow[j], bon[j], k);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) x.a[u][i] = load16(arow[i], aon[i], k);
+    }
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Chunk& x) {
+#pragma unroll
+    for (int u = 0; u < CH; ++u)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.b[u][j]),
+                                                             __builtin_bit_cast(bf16x8, x.a[u][i]), acc[i][j], 0, 0, 0);
+  };
+  const int64_t chunks = (g.K + 32 * CH - 1) / (32 * CH);
+  Chunk x, y;
+  int64_t c = wave;
+  if (c < chunks) load(c, x);
+  while (c < chunks) {
+    if (c + KS < chunks) load(c + KS, y);
+    compute(x);
+    c += KS;
+    if (c >= chunks) break;
+    if (c + KS < chunks) load(c + KS, x);
+    compute(y);
+    c += KS;
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) part[wave][i * FN + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int f = wave; f < FM * FN; f += KS) {
+    f32x4 sum = part[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < KS; ++w) sum += part[w][f][lane];
+    const int64_t m = m0 + 16 * (f / FN) + l16;
+    if (m < g.M) finish4(g, m, n0 + 16 * (f % FN) + 4 * lq, sum);
+  }
+}
+
+template <int FM, int KS>
+hipError_t run_rows(const Linear& g, hipStream_t s) {
+  const int64_t wgs = (g.M + 16 * FM - 1) / (16 * FM) * ((g.N + 31) / 32);
+  if (!grid_ok(wgs, 64 * KS)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((linear_rows_kernel<FM, KS>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
+  return hipGetLastError();
+}
+
+// The tiled kernel's conditions: 16-byte loads that lie inside the operand or outside it, and 31-bit offsets
+// inside a tile.
+bool tile_ok(const Linear& g) {
+  return (uintptr_t)g.A % 16 == 0 && (uintptr_t)g.B % 16 == 0 && g.lda % 8 == 0 && g.ldb % 8 == 0 &&
+         g.lda < (1 << 22) && g.ldb < (1 << 22) && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
+}
+
+using Lin256 = LinCfg<8, 8>;
+using Lin128 = LinCfg<4, 4>;
+
+template <bool AT, bool BT, int EPI>
+hipError_t run_sized(const Linear& g, hipStream_t s) {
+  auto tiles = [&](int64_t b) { return (g.M + b - 1) / b * ((g.N + b - 1) / b); };
+  const bool large = (tiles(256) + 255) / 256 * 5 <= (tiles(128) + 511) / 512 * 3;
+  return large ? run_tile<AT, BT, EPI, Lin256>(g, s) : run_tile<AT, BT, EPI, Lin128>(g, s);
+}
+
+hipError_t linear_piece(const Linear& g, hipStream_t s) {
+  if (force_generic() || !tile_ok(g)) return run_general(g, s);
+  if (!g.a_t && !g.b_t) {
+    if (g.M <= 64 && (g.N + 127) / 128 <= 256) return g.M > 16 ? run_rows<2, 4>(g, s) : run_rows<1, 4>(g, s);
+    return run_sized<false, false, EPI_FWD>(g, s);
+  }
+  if (g.a_t) return g.epi == EPI_ADD ? run_sized<true, true, EPI_ADD>(g, s) : run_sized<true, true, EPI_PLAIN>(g, s);
+  return g.epi == EPI_GATE ? run_sized<false, true, EPI_GATE>(g, s) : run_sized<false, true, EPI_PLAIN>(g, s);
+}
 
 }  // namespace
 

@@ -48,6 +48,12 @@ __device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
 __device__ __forceinline__ void dma16b(uint32_t voff, u32x4 desc, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(desc), "s"(lds) : "memory");
 }
+// The same to LDS at base + AT: the sum is formed in M0 itself.
+template <int AT>
+__device__ __forceinline__ void dma16b_at(uint32_t voff, u32x4 desc, uint32_t base) {
+  asm volatile("s_add_u32 m0, %2, %3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(desc), "s"(base), "n"(AT)
+               : "memory", "scc");
+}
 // Descriptor of `bytes` bytes from p (p wave-uniform): untyped, no stride, no swizzle.
 __device__ __forceinline__ u32x4 buffer_desc(const void* p, uint32_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)p;

@@ -8,6 +8,8 @@
 #include "launch.hpp"
 #include "pieces.hpp"
 
+#include <utility>
+
 namespace nms {
 namespace {
 
@@ -169,31 +171,40 @@ hipError_t run_general(const Linear& g, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiled kernel: BM x BN tiles of C by four waves (2 x 2) of 16 FM x 16 FN, 64-k stages of both operands in
-// two LDS buffers filled by direct-to-LDS loads.
+// Tiled kernel: BM x BN tiles of C by four waves (2 x 2) of 16 FM x 16 FN, in steps of 32 k whose operands pass through
+// a ring of five LDS buffers, filled by direct-to-LDS loads.
 //
 // An operand lies in LDS as it does in memory:
-//   reduction contiguous   a row of C per 128-byte LDS row, its 16-byte chunk c at slot c ^ (row / 2 % 8): sixteen
+//   reduction contiguous   a row of C per 64-byte LDS row, its 16-byte chunk c at slot c ^ (row / 4 % 4): sixteen
 //                          rows' reads of one chunk cover all 64 banks once; a fragment is one 16-byte read;
 //   reduction strided      a k per LDS row of 2 BM bytes, its 32-byte segment s (16 columns: a fragment's) at
 //                          s ^ (k % 4 + 4 (k / 8 % 2)).  The transposing read gives a lane four k of one column from
 //                          four rows; a read's half wave touches eight rows (k % 4 and k / 8 % 2 all different), so
 //                          eight segments in different banks; a fragment is two reads.
-// A stage is two sub-steps of FM x FN matrix instructions (32 k each); between them the wave reads the
-// operands of the next sub-step, and issues the loads of the stages after.  The barrier sits between the two
-// sub-steps: by then every wave has read all of the stage, so the second sub-step reads the next stage's first operands,
-// and the buffer just left takes half of the loads of the stage after next; the other half follow in the next
-// stage's first sub-step.  Rows and columns beyond the operands, and k beyond K, are zeros: a lane's
+// Step s runs FM x FN matrix instructions on fragments that were read during step s - 1, and between them reads
+// step s + 1's and issues the loads of step s + 5 into the buffer that step s was read from: a load has three steps to
+// arrive.  The waves meet once a step.  Rows and columns beyond the operands, and k beyond K, are zeros: a lane's
 // 16 bytes lie inside the operand or outside (the contiguous sizes are multiples of eight), and outside its offset
 // is moved beyond the descriptor's size, where nothing is read.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kOutside = 0x80000000u;   // added to an offset: beyond every descriptor's size
 
+// f(0) .. f(N - 1) with the index as a constant
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each_of(F f) {
+  each_of(std::make_integer_sequence<int, N>(), f);
+}
+
 template <int FM_, int FN_>
 struct LinCfg {
   static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN;
-  static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
-  static constexpr int LA = BM / 32, LB = BN / 32, LOADS = LA + LB;   // 1 KB loads a wave and stage
+  static constexpr int RING = 5, A_BYTES = BM * 64, STEP = (BM + BN) * 64;
+  static constexpr int LA = BM / 64, LB = BN / 64, LOADS = LA + LB;   // 1 KB loads a wave and step
+  static constexpr int LDS = RING * STEP;
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -202,20 +213,20 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // Where a wave's loads of one operand come from, and where a lane's fragments lie in LDS.
 template <bool T, int BR, int LN>
 struct Operand {
-  static constexpr int ROW = T ? 2 * BR : 128;    // bytes of an LDS row
+  static constexpr int ROW = T ? 2 * BR : 64;     // bytes of an LDS row
   const uint16_t* base;
-  int64_t step;          // elements from a stage to the next
+  int64_t step;          // elements from a step to the next
   int64_t K;
   uint32_t width;        // T: bytes of the tile's columns that exist
   uint32_t ldb;          // bytes of a row
   uint32_t off[LN];      // of this wave's loads, this lane
-  int c[2];              // not T: the lane's chunk in the even and the odd loads
+  int c;                 // not T: the lane's chunk
   __device__ void init(const uint16_t* X, int64_t ld, int64_t r0, int64_t R, int64_t K_, int wave, int lane) {
     K = K_;
     ldb = (uint32_t)(2 * ld);
     if constexpr (T) {
       base = X + r0;
-      step = 64 * ld;
+      step = 32 * ld;
       width = (uint32_t)(2 * (R - r0 < BR ? R - r0 : BR));
 #pragma unroll
       for (int t = 0; t < LN; ++t) {
@@ -225,54 +236,47 @@ struct Operand {
       }
     } else {
       base = X + r0 * ld;
-      step = 64;
-      c[0] = (lane & 7) ^ (lane >> 4);
-      c[1] = c[0] ^ 4;
+      step = 32;
+      c = (lane & 3) ^ (lane >> 4);   // row lane / 4 of the load's 16
 #pragma unroll
       for (int t = 0; t < LN; ++t) {
-        const int r = 8 * (wave * LN + t) + (lane >> 3);
-        off[t] = r * ldb + 16 * c[t & 1] + (r0 + r < R ? 0u : kOutside);
+        const int r = 16 * (wave * LN + t) + (lane >> 2);
+        off[t] = r * ldb + 16 * c + (r0 + r < R ? 0u : kOutside);
       }
     }
   }
-  // stage kt's descriptor; nothing is read of a stage behind the last
-  __device__ u32x4 desc(int kt) const {
-    const int64_t left = K - (int64_t)kt * 64;
+  // step s's descriptor; nothing is read of a step behind the last
+  __device__ u32x4 desc(int s) const {
+    const int64_t left = K - (int64_t)s * 32;
     uint32_t bytes = left > 0 ? kOutside : 0u;
-    if constexpr (T) bytes = left > 0 ? (uint32_t)((left < 64 ? left : 64) - 1) * ldb + width : 0u;
-    return buffer_desc(base + kt * step, bytes);
+    if constexpr (T) bytes = left > 0 ? (uint32_t)((left < 32 ? left : 32) - 1) * ldb + width : 0u;
+    return buffer_desc(base + s * step, bytes);
   }
-  // what the offsets of the even and the odd loads of stage kt carry besides
-  __device__ void tail(int kt, uint32_t (&m)[2]) const {
-    m[0] = m[1] = 0;
-    if constexpr (!T) {
-      const int64_t left = K - (int64_t)kt * 64;
-      if (left < 64) {
-        m[0] = 8 * c[0] < left ? 0u : kOutside;
-        m[1] = 8 * c[1] < left ? 0u : kOutside;
-      }
-    }
+  // what the offsets of step s carry besides
+  __device__ uint32_t tail(int s) const {
+    if constexpr (T) return 0u;
+    else return 8 * c < K - (int64_t)s * 32 ? 0u : kOutside;
   }
-  // a lane's address in LDS of fragment 0's operand of sub-step 0, `first` the wave's first row or column
+  // a lane's address in LDS of its part of fragment 0, `first` the wave's first row or column
   __device__ static uint32_t lds0(uint32_t part, int first, int lane) {
     const int l16 = lane & 15, lq = lane >> 4;
     if constexpr (T) {
       const int k = 8 * lq + (l16 >> 2);
       return part + k * ROW + 32 * ((first >> 4) ^ ((k & 3) | (k >> 3 & 1) << 2)) + 8 * (l16 & 3);
     }
-    return part + (first + l16) * 128 + ((lq ^ ((l16 >> 1) & 7)) << 4);
+    return part + (first + l16) * 64 + ((lq ^ ((l16 >> 2) & 3)) << 4);
   }
-  // fragment i of sub-step kk
-  __device__ static bf16x8 frag(uint32_t at, int kk, int i) {
+  // fragment i
+  __device__ static bf16x8 frag(uint32_t at, int i) {
     if constexpr (T) {
-      // segment first / 16 + i: first is a multiple of 16 fragments' width, so its low bits are i's alone
-      const uint32_t a = (at ^ (uint32_t)(32 * i)) + kk * 32 * ROW;
+      // segment first / 16 + i: first is a multiple of the wave's fragments, so its low bits are i's alone
+      const uint32_t a = at ^ (uint32_t)(32 * i);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ROW));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
-    return *(lds_bf16x8*)((at ^ (uint32_t)(64 * kk)) + i * 2048);
+    return *(lds_bf16x8*)(at + i * 1024);
   }
 };
 
@@ -347,14 +351,14 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   int tm, tn;
   panel_major_tile(blockIdx.x, ntm, ntn, 4, tm, tn);
   const int64_t m0 = (int64_t)(int)uniform((uint32_t)(tm * Cfg::BM)), n0 = (int64_t)(int)uniform((uint32_t)(tn * Cfg::BN));
-  const int KT = (int)((g.K + 63) / 64);
+  const int steps = (int)((g.K + 31) / 32);
 
   Operand<AT, Cfg::BM, LA> A;
   Operand<BT, Cfg::BN, LB> B;
   A.init(g.A, g.lda, m0, g.M, g.K, wave, lane);
   B.init(g.B, g.ldb, n0, g.N, g.K, wave, lane);
   const uint32_t lds_base = uniform(lds_addr(smem));
-  uint32_t at_a = A.lds0(lds_base, wm, lane), at_b = B.lds0(lds_base + Cfg::A_BYTES, wn, lane);
+  const uint32_t a_first = A.lds0(lds_base, wm, lane), b_first = B.lds0(lds_base + Cfg::A_BYTES, wn, lane);
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -362,82 +366,94 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // load t of a wave (A's LA first) of the stage that the descriptors and tails stand for, into LDS buffer buf
-  auto dma = [&](int t, int buf, const u32x4& da, const u32x4& db, const uint32_t (&ta)[2], const uint32_t (&tb)[2]) {
-    const uint32_t to = lds_base + buf * Cfg::STAGE;
-    if (t < LA) dma16b(A.off[t < LA ? t : 0] | ta[t & 1], da, uniform(to + (wave * LA + t) * 1024));
-    else dma16b(B.off[t < LA ? 0 : t - LA] | tb[(t - LA) & 1], db, uniform(to + Cfg::A_BYTES + (wave * LB + t - LA) * 1024));
+  // loads of a wave (A's LA first) into LDS buffer `to`: of a step that lies whole inside K, and of any step
+  const uint32_t lds_a = uniform(lds_base + wave * (LA * 1024)), lds_b = uniform(lds_base + Cfg::A_BYTES + wave * (LB * 1024));
+  auto dma = [&](auto t_, uint32_t at, const u32x4& da, const u32x4& db, uint32_t ta, uint32_t tb) {
+    constexpr int t = decltype(t_)::value;
+    if constexpr (t < LA) dma16b_at<t * 1024>(A.off[t] | ta, da, lds_a + at);
+    else dma16b_at<(t - LA) * 1024>(B.off[t - LA] | tb, db, lds_b + at);
   };
-  // one sub-step on (a, b); the next operands (kk, at pa and pb) are read into an and bn between its instructions, and
-  // loads first .. first + LOADS / 2 - 1 of stage kt are issued into buf
-  auto substep = [&](const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], int kk, uint32_t pa, uint32_t pb, bf16x8 (&an)[FM],
-                     bf16x8 (&bn)[FN], int kt, int first, int buf) {
-    constexpr int N = FM * FN, READ = N / (FM + FN), LOAD = N / 2 / (LOADS / 2);
-    const u32x4 da = A.desc(kt), db = B.desc(kt);
-    uint32_t ta[2], tb[2];
-    A.tail(kt, ta);
-    B.tail(kt, tb);
 #pragma unroll
-    for (int m = 0; m < N; ++m) {
-      const int j = m / FM, i = m % FM;
-      // tied in and out of the instruction in the accumulation registers (as a builtin, the compiler moves the
-      // small accumulators between registers every stage)
-      asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(b[j]), "v"(a[i]));
-      __builtin_amdgcn_sched_barrier(0);
-      if (m % READ == 0) {
-        const int q = m / READ;
-        if (q < FM) an[q < FM ? q : 0] = A.frag(pa, kk, q);
-        else if (q < FM + FN) bn[q < FM ? 0 : q - FM] = B.frag(pb, kk, q - FM);
-      }
-      if (m % LOAD == LOAD / 2 && m / LOAD < LOADS / 2) dma(first + m / LOAD, buf, da, db, ta, tb);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  {
-    u32x4 da = A.desc(0), db = B.desc(0);
-    uint32_t ta[2], tb[2];
-    A.tail(0, ta);
-    B.tail(0, tb);
-#pragma unroll
-    for (int t = 0; t < LOADS; ++t) dma(t, 0, da, db, ta, tb);
-    da = A.desc(1);
-    db = B.desc(1);
-    A.tail(1, ta);
-    B.tail(1, tb);
-#pragma unroll
-    for (int t = 0; t < LOADS / 2; ++t) dma(t, 1, da, db, ta, tb);
+  for (int s = 0; s < Cfg::RING; ++s) {
+    const u32x4 da = A.desc(s), db = B.desc(s);
+    const uint32_t ta = A.tail(s), tb = B.tail(s);
+    each_of<LOADS>([&](auto t) { dma(t, s * Cfg::STEP, da, db, ta, tb); });
   }
-  wait_vmcnt<LOADS / 2>();   // stage 0
+  wait_vmcnt<(Cfg::RING - 1) * LOADS>();   // step 0
   lds_barrier();
   bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) a0[i] = A.frag(at_a, 0, i);
+  for (int i = 0; i < FM; ++i) a0[i] = A.frag(a_first, i);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) b0[j] = B.frag(at_b, 0, j);
-  for (int kt = 0; kt < KT; ++kt) {
-    const int buf = kt & 1;
-    substep(a0, b0, 1, at_a, at_b, a1, b1, kt + 1, LOADS / 2, buf ^ 1);
-    wait_vmcnt<0>();   // this wave's loads of stage kt + 1
-    lds_barrier();     // every wave's; and every wave has read all it needs of stage kt
-    at_a += buf ? -Cfg::STAGE : Cfg::STAGE;
-    at_b += buf ? -Cfg::STAGE : Cfg::STAGE;
-    substep(a1, b1, 0, at_a, at_b, a0, b0, kt + 2, 0, buf);
+  for (int j = 0; j < FN; ++j) b0[j] = B.frag(b_first, j);
+
+  uint32_t cur = 0;   // the buffer of the step that is computed, in bytes
+  u32x4 na = A.desc(Cfg::RING), nb = B.desc(Cfg::RING);   // what the next step to be loaded is read through
+  const uint64_t adv_a = 2 * A.step, adv_b = 2 * B.step;
+  auto forward = [](u32x4& d, uint64_t by) {
+    const uint64_t at = ((uint64_t)d[1] << 32 | d[0]) + by;
+    d[0] = (uint32_t)at;
+    d[1] = (uint32_t)(at >> 32);
+  };
+  // WHOLE: the step that is loaded lies inside K, so its descriptors are the last ones moved on
+  auto step = [&](auto whole, int s, const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    constexpr int N = FM * FN, READ = N / (FM + FN), LOAD = N / LOADS;
+    wait_vmcnt<(Cfg::RING - 2) * LOADS>();   // this wave's loads of step s + 1
+    lds_barrier();                           // every wave's; and every wave has read step s
+    const uint32_t next = cur == (Cfg::RING - 1) * Cfg::STEP ? 0 : cur + Cfg::STEP;
+    const uint32_t pa = a_first + next, pb = b_first + next;
+    uint32_t ta = 0, tb = 0;
+    if constexpr (!WHOLE) {
+      na = A.desc(s + Cfg::RING);
+      nb = B.desc(s + Cfg::RING);
+      ta = A.tail(s + Cfg::RING);
+      tb = B.tail(s + Cfg::RING);
+    }
+    each_of<N>([&](auto m_) {
+      constexpr int m = decltype(m_)::value, j = m / FM, i = m % FM;
+      // tied in and out of the instruction in the accumulation registers (as a builtin, the compiler moves the
+      // small accumulators between registers every step)
+      asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(b[j]), "v"(a[i]));
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (m % READ == 0) {
+        constexpr int q = m / READ;
+        if constexpr (q < FM) an[q] = A.frag(pa, q);
+        else if constexpr (q < FM + FN) bn[q - FM] = B.frag(pb, q - FM);
+      }
+      if constexpr (m % LOAD == LOAD / 2) {
+        dma(std::integral_constant<int, m / LOAD>(), cur, na, nb, ta, tb);
+        if constexpr (WHOLE && m / LOAD == LA - 1) forward(na, adv_a);
+        if constexpr (WHOLE && m / LOAD == LOADS - 1) forward(nb, adv_b);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    cur = next;
+  };
+  int s = 0;
+  for (const int whole = (int)(g.K / 32) - Cfg::RING; s + 1 < whole; s += 2) {
+    step(std::true_type(), s, a0, b0, a1, b1);
+    step(std::true_type(), s + 1, a1, b1, a0, b0);
   }
-  wait_vmcnt<0>();   // no load may land in LDS after the workgroup ends
+  for (; s < steps; s += 2) {
+    step(std::false_type(), s, a0, b0, a1, b1);
+    if (s + 1 < steps) step(std::false_type(), s + 1, a1, b1, a0, b0);
+  }
+  wait_vmcnt<0>();   // no load may land in LDS any more
   // the last instructions' results before any other instruction reads them (the compiler does not see
   // the instructions inside the assembly statements)
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   lds_barrier();   // every wave has read its last operands: the buffers are free
-  tile_epilogue<EPI>(g, acc, smem + wave * (Cfg::STAGE / 2), m0 + wm, n0 + wn, lane);
+  tile_epilogue<EPI>(g, acc, smem + wave * (Cfg::LDS / 5), m0 + wm, n0 + wn, lane);
 }
 
 template <bool AT, bool BT, int EPI, typename Cfg>
 hipError_t run_tile(const Linear& g, hipStream_t s) {
   auto kern = linear_tile_kernel<AT, BT, EPI, Cfg>;
-  (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * Cfg::STAGE);
+  (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS);
   const int64_t wgs = (g.M + Cfg::BM - 1) / Cfg::BM * ((g.N + Cfg::BN - 1) / Cfg::BN);
   if (!grid_ok(wgs, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), 2 * Cfg::STAGE, s, g);
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), Cfg::LDS, s, g);
   return hipGetLastError();
 }
 

@@ -280,67 +280,171 @@ struct Operand {
   }
 };
 
-// A wave's FM x FN fragments to C, by way of LDS (`region`: the wave's quarter of the stages' buffers): a lane then
-// holds four consecutive columns of rows lane / 16, and 16 lanes 64 columns, so every load and store of C and
-// of what lies like C takes whole 128-byte lines of bf16, and the code is one small loop over the rows.  Row r's 16-byte
-// chunk c lies at c ^ (r % 16): a fragment's rows are written to different banks, and read in order.
-template <int EPI, int FM, int FN>
-__device__ inline void tile_epilogue(const Linear& g, const f32x4 (&acc)[FM][FN], unsigned char* region, int64_t m0,
-                                     int64_t n0, int lane) {
-  constexpr int COLS = 16 * FN, H = COLS / 64;               // H: runs of 64 columns
-  constexpr int ROWS = (FM + FN) * 2048 / (COLS * 4);        // of a pass: the wave's quarter of 2 x 32 (FM + FN) rows of 128 bytes
-  static_assert(ROWS % 16 == 0 && 16 * FM % ROWS == 0, "a pass is whole fragments");
-  constexpr int PF = ROWS / 16, U = 4;                       // U: rows of a lane in flight together
-  const int l16 = lane & 15, lq = lane >> 4;
-  const int64_t n = n0 + 4 * l16;
-  f32x4 bias[H];
-#pragma unroll
-  for (int h = 0; h < H; ++h)
-    bias[h] = EPI == EPI_FWD && n + 64 * h < g.N ? bias4(g, n + 64 * h) : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int p = 0; p < FM / PF; ++p) {
+// A wave's FM x FN fragments to C, by way of LDS (`region`: the wave's part of the ring): a lane then holds four
+// consecutive columns of rows lane / 16, and 16 lanes 64 columns, so every load and store of C and of what lies
+// like C takes whole 128-byte lines of bf16.  Row r's 16-byte chunk c lies at c ^ (r % 16): a fragment's rows are written to
+// different banks, and read in order.
+template <int FM, int FN>
+struct Out {
+  static constexpr int COLS = 16 * FN, H = COLS / 64;                 // H: runs of 64 columns
+  static constexpr int ROWS = (FM + FN) * 2048 / (COLS * 4), PF = ROWS / 16, PASSES = FM / PF;   // of a pass
+  static_assert(ROWS % 16 == 0 && FM % PF == 0, "a pass is whole fragments");
+  template <int P>
+  __device__ static void put(const f32x4 (&acc)[FM][FN], unsigned char* region, int lane) {
+    const int l16 = lane & 15, lq = lane >> 4;
 #pragma unroll
     for (int i = 0; i < PF; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        *reinterpret_cast<f32x4*>(region + (16 * i + l16) * (COLS * 4) + ((4 * j + lq) ^ l16) * 16) = acc[p * PF + i][j];
+        *reinterpret_cast<f32x4*>(region + (16 * i + l16) * (COLS * 4) + ((4 * j + lq) ^ l16) * 16) = acc[P * PF + i][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // other lanes of this wave read it
-    const int64_t mp = m0 + p * ROWS;
-    const int rows = g.M - mp < ROWS ? (int)(g.M - mp) : ROWS;
-    for (int r0 = 0; r0 < rows; r0 += 4 * U) {
-      f32x4 x[U][H];   // what is added to C, or gates it
-      auto each = [&](auto f) {
+  }
+  __device__ static f32x4 get(const unsigned char* region, int r, int h, int lane) {
+    return *reinterpret_cast<const f32x4*>(region + r * (COLS * 4) + ((16 * h + (lane & 15)) ^ (r & 15)) * 16);
+  }
+};
+
+// Any tile, element by element where it ends.
+template <int EPI, int FM, int FN>
+__device__ __forceinline__ void epilogue_edge(const Linear& g, const f32x4 (&acc)[FM][FN], unsigned char* region, int64_t m0,
+                                     int64_t n0, int lane) {
+  typedef Out<FM, FN> O;
+  each_of<O::PASSES>([&](auto p) {
+    O::template put<decltype(p)::value>(acc, region, lane);
+    const int64_t mp = m0 + decltype(p)::value * O::ROWS;
+    const int rows = g.M - mp < O::ROWS ? (int)(g.M - mp) : O::ROWS;
+#pragma unroll 1
+    for (int r = lane >> 4; r < rows; r += 4) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-            if (r0 + 4 * u + lq < rows && n + 64 * h < g.N) f(u, h, mp + r0 + 4 * u + lq, n + 64 * h);
-      };
-      if constexpr (EPI == EPI_FWD) {
-        if (g.R) each([&](int u, int h, int64_t m, int64_t c) { x[u][h] = load4(g.R + m * g.ldr, c, g.N); });
-      }
-      if constexpr (EPI == EPI_GATE) each([&](int u, int h, int64_t m, int64_t c) { x[u][h] = load4(g.P + m * g.ldp, c, g.N); });
-      if constexpr (EPI == EPI_ADD) each([&](int u, int h, int64_t m, int64_t c) { x[u][h] = load4((const float*)g.C + m * g.ldc, c, g.N); });
-      each([&](int u, int h, int64_t m, int64_t c) {
-        const int r = r0 + 4 * u + lq;
-        f32x4 v = *reinterpret_cast<const f32x4*>(region + r * (COLS * 4) + ((16 * h + l16) ^ (r & 15)) * 16);
-        if constexpr (EPI == EPI_FWD) {
-          v += bias[h];
-          if (g.Z) store4(g.Z + m * g.ldz, c, g.N, v);
-          v = act4(g.act, v);
-          if (g.R) v += x[u][h];
-        }
-        if constexpr (EPI == EPI_GATE) v *= dact4(g.act, x[u][h]);
-        if constexpr (EPI == EPI_ADD) v += x[u][h];
-        if (g.bf16_out) store4((uint16_t*)g.C + m * g.ldc, c, g.N, v);
-        else store4((float*)g.C + m * g.ldc, c, g.N, v);
-      });
+      for (int h = 0; h < O::H; ++h) finish4(g, mp + r, n0 + 64 * h + 4 * (lane & 15), O::get(region, r, h, lane));
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // before the next pass's values
+  });
+}
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+// 2 GiB from p (wave-uniform), or nothing: loads give 0 and stores are dropped
+__device__ inline Rsrc rsrc(const void* p, bool on) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, on ? (int)0x7FFFFFFF : 0, 0x00020000);
+}
+
+// A tile that lies whole inside C.  Addresses are a lane's 32-bit offset, so a row costs its arithmetic, its loads and
+// stores and one addition a matrix.  Stores take no scalar offset: behind a 16-byte store that has one the compiler lets the
+// next instruction overwrite the data's registers, and on this GPU the last lanes' data then is what that wrote
+// (tests/test_dense_codegen.py).  OTHER: something is read beside the sums (the residual, the gate, C itself)
+// or the pre-activations are stored; all of a pass's reads are in flight together, since with one or two waves a SIMD
+// nothing else hides their latency.
+template <int EPI, int ACT, bool OTHER, typename T, int FM, int FN>
+__device__ __forceinline__ void epilogue_whole(const Linear& g, const f32x4 (&acc)[FM][FN], unsigned char* region, int64_t m0,
+                                      int64_t n0, int lane) {
+  typedef Out<FM, FN> O;
+  typedef std::conditional_t<EPI == EPI_ADD, u32x4, u32x2> Raw;
+  constexpr int G = O::ROWS / 4, H = O::H;
+  const int l16 = lane & 15, lq = lane >> 4;
+  f32x4 bias[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    bias[h] = EPI == EPI_FWD ? bias4(g, n0 + 4 * l16 + 64 * h) : f32x4{0.f, 0.f, 0.f, 0.f};
+  // what is read: one row stride and element size
+  const void* x = EPI == EPI_FWD ? (const void*)g.R : EPI == EPI_GATE ? (const void*)g.P : g.C;
+  const int64_t ldx = EPI == EPI_FWD ? g.ldr : EPI == EPI_GATE ? g.ldp : g.ldc;
+  constexpr int XS = EPI == EPI_ADD ? 4 : 2;
+  each_of<O::PASSES>([&](auto p) {
+    const int64_t mp = m0 + decltype(p)::value * O::ROWS;
+    const Rsrc rc = rsrc((T*)g.C + mp * g.ldc + n0, true);
+    const uint32_t vc = (uint32_t)((lq * g.ldc + 4 * l16) * sizeof(T)), sc = (uint32_t)(4 * g.ldc * sizeof(T));
+    const Rsrc rx = rsrc((const char*)x + (mp * ldx + n0) * XS, x != nullptr);
+    const uint32_t vx = (uint32_t)((lq * ldx + 4 * l16) * XS), sx = (uint32_t)(4 * ldx * XS);
+    const Rsrc rz = rsrc(g.Z + mp * g.ldz + n0, EPI == EPI_FWD && g.Z);
+    const uint32_t vz = (uint32_t)((lq * g.ldz + 4 * l16) * 2), sz = (uint32_t)(8 * g.ldz);
+    Raw r[G][H];
+    if constexpr (OTHER) {
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          if constexpr (EPI == EPI_ADD) r[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, vx + 64 * h * XS, u * sx, 0);
+          else r[u][h] = __builtin_amdgcn_raw_buffer_load_b64(rx, vx + 64 * h * XS, u * sx, 0);
+        }
+    }
+    O::template put<decltype(p)::value>(acc, region, lane);
+#pragma unroll
+    for (int u = 0; u < G; ++u)
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        f32x4 v = O::get(region, 4 * u + lq, h, lane), w = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (OTHER && EPI == EPI_ADD) w = __builtin_bit_cast(f32x4, r[u][h]);
+        if constexpr (OTHER && EPI != EPI_ADD)
+          w = f32x4{__uint_as_float(r[u][h][0] << 16), __uint_as_float(r[u][h][0] & 0xFFFF0000u),
+                    __uint_as_float(r[u][h][1] << 16), __uint_as_float(r[u][h][1] & 0xFFFF0000u)};
+        if constexpr (EPI == EPI_FWD) {
+          v += bias[h];
+          if constexpr (OTHER)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4)), rz,
+                                                  vz + u * sz + 128 * h, 0, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = act_fwd<ACT>(v[q]) + w[q];
+        }
+        if constexpr (EPI == EPI_GATE) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] *= act_bwd<ACT>(w[q]);
+        }
+        if constexpr (EPI == EPI_ADD) v += w;
+        if constexpr (sizeof(T) == 2)
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4)), rc,
+                                                vc + u * sc + 128 * h, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, vc + u * sc + 256 * h, 0, 0);
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // before the next pass's values
+  });
+}
+
+// A matrix whose rows four consecutive elements at a multiple of four columns can be read from at once, with 31-bit
+// offsets inside a pass.
+__device__ inline bool fours(const void* p, int64_t ld, int size) {
+  return !p || ((uintptr_t)p % (4 * size) == 0 && ld % 4 == 0 && ld < (1 << 22));
+}
+
+template <int EPI, int ACT, int FM, int FN>
+__device__ __forceinline__ void tile_epilogue(const Linear& g, const f32x4 (&acc)[FM][FN], unsigned char* region,
+                                              int64_t m0, int64_t n0, int lane) {
+  if (m0 >= g.M || n0 >= g.N) return;
+  const bool whole = m0 + 16 * FM <= g.M && n0 + 16 * FN <= g.N && fours(g.C, g.ldc, g.bf16_out ? 2 : 4) &&
+                     fours(g.R, g.ldr, 2) && fours(g.Z, g.ldz, 2) && fours(g.P, g.ldp, 2);
+  if (!whole) {
+    epilogue_edge<EPI>(g, acc, region, m0, n0, lane);
+  } else if constexpr (EPI == EPI_FWD) {
+    const bool other = g.R || g.Z;
+    if (g.bf16_out) {
+      if (other) epilogue_whole<EPI, ACT, true, uint16_t>(g, acc, region, m0, n0, lane);
+      else epilogue_whole<EPI, ACT, false, uint16_t>(g, acc, region, m0, n0, lane);
+    } else {
+      if (other) epilogue_whole<EPI, ACT, true, float>(g, acc, region, m0, n0, lane);
+      else epilogue_whole<EPI, ACT, false, float>(g, acc, region, m0, n0, lane);
+    }
+  } else if constexpr (EPI == EPI_ADD) {
+    epilogue_whole<EPI, ACT, true, float>(g, acc, region, m0, n0, lane);
+  } else {
+    if (g.bf16_out) epilogue_whole<EPI, ACT, EPI == EPI_GATE, uint16_t>(g, acc, region, m0, n0, lane);
+    else epilogue_whole<EPI, ACT, EPI == EPI_GATE, float>(g, acc, region, m0, n0, lane);
   }
 }
 
-template <bool AT, bool BT, int EPI, typename Cfg>
+// The tile of a workgroup.  Workgroups are dealt to the 8 XCDs in turn; an XCD takes a run of the tiles in the order of
+// groups of kGroupRows row tiles, column after column, so the 32 tiles that it computes together are about square and
+// share their operands' rows in its L2.
+constexpr int kGroupRows = 4;
+__device__ inline void xcd_tile(int id, int ntm, int ntn, int& tm, int& tn) {
+  const int tiles = ntm * ntn, x = id % 8, per = tiles / 8, rest = tiles % 8;
+  const int t = x * per + (x < rest ? x : rest) + id / 8;
+  const int group = t / (kGroupRows * ntn), first = group * kGroupRows;
+  const int rows = ntm - first < kGroupRows ? ntm - first : kGroupRows, within = t - first * ntn;
+  tm = first + within % rows;
+  tn = within / rows;
+}
+
+template <bool AT, bool BT, int EPI, int ACT, typename Cfg>
 __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(Linear g) {
   constexpr int FM = Cfg::FM, FN = Cfg::FN, LA = Cfg::LA, LB = Cfg::LB, LOADS = Cfg::LOADS;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -349,7 +453,7 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   const int wm = (wave >> 1) * 16 * FM, wn = (wave & 1) * 16 * FN;
   const int ntm = (int)((g.M + Cfg::BM - 1) / Cfg::BM), ntn = (int)((g.N + Cfg::BN - 1) / Cfg::BN);
   int tm, tn;
-  panel_major_tile(blockIdx.x, ntm, ntn, 4, tm, tn);
+  xcd_tile(blockIdx.x, ntm, ntn, tm, tn);
   const int64_t m0 = (int64_t)(int)uniform((uint32_t)(tm * Cfg::BM)), n0 = (int64_t)(int)uniform((uint32_t)(tn * Cfg::BN));
   const int steps = (int)((g.K + 31) / 32);
 
@@ -398,7 +502,9 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   // WHOLE: the step that is loaded lies inside K, so its descriptors are the last ones moved on
   auto step = [&](auto whole, int s, const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
     constexpr bool WHOLE = decltype(whole)::value;
-    constexpr int N = FM * FN, READ = N / (FM + FN), LOAD = N / LOADS;
+    // the reads end well before the step does, so that the waves' meeting finds them done; faster than one in three
+    // instructions they would queue at LDS (128 bytes a cycle for the four waves)
+    constexpr int N = FM * FN, READ = N == 64 ? 3 : 1, LOAD = N / LOADS;
     wait_vmcnt<(Cfg::RING - 2) * LOADS>();   // this wave's loads of step s + 1
     lds_barrier();                           // every wave's; and every wave has read step s
     const uint32_t next = cur == (Cfg::RING - 1) * Cfg::STEP ? 0 : cur + Cfg::STEP;
@@ -444,12 +550,12 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   // the instructions inside the assembly statements)
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   lds_barrier();   // every wave has read its last operands: the buffers are free
-  tile_epilogue<EPI>(g, acc, smem + wave * (Cfg::LDS / 5), m0 + wm, n0 + wn, lane);
+  tile_epilogue<EPI, ACT>(g, acc, smem + wave * (Cfg::LDS / 5), m0 + wm, n0 + wn, lane);
 }
 
-template <bool AT, bool BT, int EPI, typename Cfg>
+template <bool AT, bool BT, int EPI, int ACT, typename Cfg>
 hipError_t run_tile(const Linear& g, hipStream_t s) {
-  auto kern = linear_tile_kernel<AT, BT, EPI, Cfg>;
+  auto kern = linear_tile_kernel<AT, BT, EPI, ACT, Cfg>;
   (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS);
   const int64_t wgs = (g.M + Cfg::BM - 1) / Cfg::BM * ((g.N + Cfg::BN - 1) / Cfg::BN);
   if (!grid_ok(wgs, 256)) return hipErrorInvalidConfiguration;
@@ -565,21 +671,34 @@ bool tile_ok(const Linear& g) {
 using Lin256 = LinCfg<8, 8>;
 using Lin128 = LinCfg<4, 4>;
 
-template <bool AT, bool BT, int EPI>
+template <bool AT, bool BT, int EPI, int ACT>
 hipError_t run_sized(const Linear& g, hipStream_t s) {
   auto tiles = [&](int64_t b) { return (g.M + b - 1) / b * ((g.N + b - 1) / b); };
   const bool large = (tiles(256) + 255) / 256 * 5 <= (tiles(128) + 511) / 512 * 3;
-  return large ? run_tile<AT, BT, EPI, Lin256>(g, s) : run_tile<AT, BT, EPI, Lin128>(g, s);
+  return large ? run_tile<AT, BT, EPI, ACT, Lin256>(g, s) : run_tile<AT, BT, EPI, ACT, Lin128>(g, s);
+}
+template <bool BT, int EPI>
+hipError_t run_act(const Linear& g, hipStream_t s) {
+  switch (g.act) {
+    case ACT_RELU: return run_sized<false, BT, EPI, ACT_RELU>(g, s);
+    case ACT_GELU_TANH: return run_sized<false, BT, EPI, ACT_GELU_TANH>(g, s);
+    case ACT_SILU: return run_sized<false, BT, EPI, ACT_SILU>(g, s);
+  }
+  if constexpr (EPI == EPI_FWD) return run_sized<false, BT, EPI, ACT_NONE>(g, s);
+  return hipErrorInvalidValue;   // a gate has an activation
 }
 
 hipError_t linear_piece(const Linear& g, hipStream_t s) {
   if (force_generic() || !tile_ok(g)) return run_general(g, s);
   if (!g.a_t && !g.b_t) {
     if (g.M <= 64 && (g.N + 127) / 128 <= 256) return g.M > 16 ? run_rows<2, 4>(g, s) : run_rows<1, 4>(g, s);
-    return run_sized<false, false, EPI_FWD>(g, s);
+    return run_act<false, EPI_FWD>(g, s);
   }
-  if (g.a_t) return g.epi == EPI_ADD ? run_sized<true, true, EPI_ADD>(g, s) : run_sized<true, true, EPI_PLAIN>(g, s);
-  return g.epi == EPI_GATE ? run_sized<false, true, EPI_GATE>(g, s) : run_sized<false, true, EPI_PLAIN>(g, s);
+  if (g.a_t) {
+    return g.epi == EPI_ADD ? run_sized<true, true, EPI_ADD, ACT_NONE>(g, s)
+                            : run_sized<true, true, EPI_PLAIN, ACT_NONE>(g, s);
+  }
+  return g.epi == EPI_GATE ? run_act<true, EPI_GATE>(g, s) : run_sized<false, true, EPI_PLAIN, ACT_NONE>(g, s);
 }
 
 }  // namespace

@@ -199,34 +199,36 @@ __device__ __forceinline__ void each_of(F f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-template <int FM_, int FN_>
+// KU: the k of an LDS buffer; NA, NB: A's and B's buffers
+template <int FM_, int FN_, int KU_, int NA_, int NB_>
 struct LinCfg {
-  static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN;
-  static constexpr int RING = 5, A_BYTES = BM * 64, STEP = (BM + BN) * 64;
-  static constexpr int LA = BM / 64, LB = BN / 64, LOADS = LA + LB;   // 1 KB loads a wave and step
-  static constexpr int LDS = RING * STEP;
+  static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN, KU = KU_, NA = NA_, NB = NB_;
+  static constexpr int A_BYTES = BM * 2 * KU, B_BYTES = BN * 2 * KU, LDS = NA * A_BYTES + NB * B_BYTES;
+  static constexpr int LA = A_BYTES / 4096, LB = B_BYTES / 4096, LOADS = LA + LB;   // 1 KB loads a wave and buffer
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Where a wave's loads of one operand come from, and where a lane's fragments lie in LDS.
-template <bool T, int BR, int LN>
+template <bool T, int BR, int KU, int LN>
 struct Operand {
-  static constexpr int ROW = T ? 2 * BR : 64;     // bytes of an LDS row
+  static constexpr int ROW = T ? 2 * BR : 2 * KU;     // bytes of an LDS row
+  static constexpr int CH = KU / 8, SH = KU == 64 ? 1 : 2;   // not T: chunks of a row, rows (log2) that share a swizzle
+  static_assert(KU == 32 || LN % 2 == 0, "the swizzle of a wave's loads alternates");
   const uint16_t* base;
-  int64_t step;          // elements from a step to the next
+  int64_t step;          // elements from a buffer's k to the next one's
   int64_t K;
   uint32_t width;        // T: bytes of the tile's columns that exist
   uint32_t ldb;          // bytes of a row
   uint32_t off[LN];      // of this wave's loads, this lane
-  int c;                 // not T: the lane's chunk
+  int c[2];              // not T: the lane's chunk in the even and the odd loads
   __device__ void init(const uint16_t* X, int64_t ld, int64_t r0, int64_t R, int64_t K_, int wave, int lane) {
     K = K_;
     ldb = (uint32_t)(2 * ld);
     if constexpr (T) {
       base = X + r0;
-      step = 32 * ld;
+      step = KU * ld;
       width = (uint32_t)(2 * (R - r0 < BR ? R - r0 : BR));
 #pragma unroll
       for (int t = 0; t < LN; ++t) {
@@ -236,47 +238,49 @@ struct Operand {
       }
     } else {
       base = X + r0 * ld;
-      step = 32;
-      c = (lane & 3) ^ (lane >> 4);   // row lane / 4 of the load's 16
+      step = KU;
+      constexpr int RL = 64 / CH;   // rows of a load
+      c[0] = (lane % CH) ^ ((lane / CH) >> SH & (CH - 1));
+      c[1] = KU == 64 ? c[0] ^ 4 : c[0];
 #pragma unroll
       for (int t = 0; t < LN; ++t) {
-        const int r = 16 * (wave * LN + t) + (lane >> 2);
-        off[t] = r * ldb + 16 * c + (r0 + r < R ? 0u : kOutside);
+        const int r = RL * (wave * LN + t) + lane / CH;
+        off[t] = r * ldb + 16 * c[t & 1] + (r0 + r < R ? 0u : kOutside);
       }
     }
   }
-  // step s's descriptor; nothing is read of a step behind the last
-  __device__ u32x4 desc(int s) const {
-    const int64_t left = K - (int64_t)s * 32;
+  // the descriptor of buffer u's k; nothing is read behind the last
+  __device__ u32x4 desc(int u) const {
+    const int64_t left = K - (int64_t)u * KU;
     uint32_t bytes = left > 0 ? kOutside : 0u;
-    if constexpr (T) bytes = left > 0 ? (uint32_t)((left < 32 ? left : 32) - 1) * ldb + width : 0u;
-    return buffer_desc(base + s * step, bytes);
+    if constexpr (T) bytes = left > 0 ? (uint32_t)((left < KU ? left : KU) - 1) * ldb + width : 0u;
+    return buffer_desc(base + u * step, bytes);
   }
-  // what the offsets of step s carry besides
-  __device__ uint32_t tail(int s) const {
+  // what the offsets of buffer u's even and odd loads carry besides
+  __device__ uint32_t tail(int u, int odd) const {
     if constexpr (T) return 0u;
-    else return 8 * c < K - (int64_t)s * 32 ? 0u : kOutside;
+    else return 8 * c[odd] < K - (int64_t)u * KU ? 0u : kOutside;
   }
-  // a lane's address in LDS of its part of fragment 0, `first` the wave's first row or column
+  // a lane's address in LDS of its part of fragment 0 of k 0 .. 31, `first` the wave's first row or column
   __device__ static uint32_t lds0(uint32_t part, int first, int lane) {
     const int l16 = lane & 15, lq = lane >> 4;
     if constexpr (T) {
       const int k = 8 * lq + (l16 >> 2);
       return part + k * ROW + 32 * ((first >> 4) ^ ((k & 3) | (k >> 3 & 1) << 2)) + 8 * (l16 & 3);
     }
-    return part + (first + l16) * 64 + ((lq ^ ((l16 >> 2) & 3)) << 4);
+    return part + (first + l16) * ROW + ((lq ^ (l16 >> SH & (CH - 1))) << 4);
   }
-  // fragment i
-  __device__ static bf16x8 frag(uint32_t at, int i) {
+  // fragment i of k 32 kk ..
+  __device__ static bf16x8 frag(uint32_t at, int kk, int i) {
     if constexpr (T) {
       // segment first / 16 + i: first is a multiple of the wave's fragments, so its low bits are i's alone
-      const uint32_t a = at ^ (uint32_t)(32 * i);
+      const uint32_t a = (at ^ (uint32_t)(32 * i)) + kk * (32 * ROW);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ROW));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
-    return *(lds_bf16x8*)(at + i * 1024);
+    return *(lds_bf16x8*)((at ^ (uint32_t)(64 * kk)) + i * (16 * ROW));
   }
 };
 
@@ -455,14 +459,14 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   int tm, tn;
   xcd_tile(blockIdx.x, ntm, ntn, tm, tn);
   const int64_t m0 = (int64_t)(int)uniform((uint32_t)(tm * Cfg::BM)), n0 = (int64_t)(int)uniform((uint32_t)(tn * Cfg::BN));
-  const int steps = (int)((g.K + 31) / 32);
+  const int units = (int)((g.K + Cfg::KU - 1) / Cfg::KU);
 
-  Operand<AT, Cfg::BM, LA> A;
-  Operand<BT, Cfg::BN, LB> B;
+  Operand<AT, Cfg::BM, Cfg::KU, LA> A;
+  Operand<BT, Cfg::BN, Cfg::KU, LB> B;
   A.init(g.A, g.lda, m0, g.M, g.K, wave, lane);
   B.init(g.B, g.ldb, n0, g.N, g.K, wave, lane);
   const uint32_t lds_base = uniform(lds_addr(smem));
-  const uint32_t a_first = A.lds0(lds_base, wm, lane), b_first = B.lds0(lds_base + Cfg::A_BYTES, wn, lane);
+  const uint32_t a_first = A.lds0(lds_base, wm, lane), b_first = B.lds0(lds_base + Cfg::NA * Cfg::A_BYTES, wn, lane);
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -470,80 +474,155 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // loads of a wave (A's LA first) into LDS buffer `to`: of a step that lies whole inside K, and of any step
-  const uint32_t lds_a = uniform(lds_base + wave * (LA * 1024)), lds_b = uniform(lds_base + Cfg::A_BYTES + wave * (LB * 1024));
-  auto dma = [&](auto t_, uint32_t at, const u32x4& da, const u32x4& db, uint32_t ta, uint32_t tb) {
-    constexpr int t = decltype(t_)::value;
-    if constexpr (t < LA) dma16b_at<t * 1024>(A.off[t] | ta, da, lds_a + at);
-    else dma16b_at<(t - LA) * 1024>(B.off[t - LA] | tb, db, lds_b + at);
+  // load t of this wave's of an operand, into the buffer at byte `at` of the operand's
+  const uint32_t lds_a = uniform(lds_base + wave * (LA * 1024)), lds_b = uniform(lds_base + Cfg::NA * Cfg::A_BYTES + wave * (LB * 1024));
+  auto load_a = [&](auto t, uint32_t at, const u32x4& d, uint32_t t0, uint32_t t1) {
+    constexpr int T = decltype(t)::value;
+    dma16b_at<T * 1024>(A.off[T] | (T & 1 ? t1 : t0), d, lds_a + at);
   };
-#pragma unroll
-  for (int s = 0; s < Cfg::RING; ++s) {
-    const u32x4 da = A.desc(s), db = B.desc(s);
-    const uint32_t ta = A.tail(s), tb = B.tail(s);
-    each_of<LOADS>([&](auto t) { dma(t, s * Cfg::STEP, da, db, ta, tb); });
-  }
-  wait_vmcnt<(Cfg::RING - 1) * LOADS>();   // step 0
-  lds_barrier();
-  bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) a0[i] = A.frag(a_first, i);
-#pragma unroll
-  for (int j = 0; j < FN; ++j) b0[j] = B.frag(b_first, j);
-
-  uint32_t cur = 0;   // the buffer of the step that is computed, in bytes
-  u32x4 na = A.desc(Cfg::RING), nb = B.desc(Cfg::RING);   // what the next step to be loaded is read through
-  const uint64_t adv_a = 2 * A.step, adv_b = 2 * B.step;
+  auto load_b = [&](auto t, uint32_t at, const u32x4& d, uint32_t t0, uint32_t t1) {
+    constexpr int T = decltype(t)::value;
+    dma16b_at<T * 1024>(B.off[T] | (T & 1 ? t1 : t0), d, lds_b + at);
+  };
+  auto fill_a = [&](int u) {   // the loads of a whole buffer
+    const u32x4 d = A.desc(u);
+    each_of<LA>([&](auto t) { load_a(t, u % Cfg::NA * Cfg::A_BYTES, d, A.tail(u, 0), A.tail(u, 1)); });
+  };
+  auto fill_b = [&](int u) {
+    const u32x4 d = B.desc(u);
+    each_of<LB>([&](auto t) { load_b(t, u % Cfg::NB * Cfg::B_BYTES, d, B.tail(u, 0), B.tail(u, 1)); });
+  };
   auto forward = [](u32x4& d, uint64_t by) {
     const uint64_t at = ((uint64_t)d[1] << 32 | d[0]) + by;
     d[0] = (uint32_t)at;
     d[1] = (uint32_t)(at >> 32);
   };
-  // WHOLE: the step that is loaded lies inside K, so its descriptors are the last ones moved on
-  auto step = [&](auto whole, int s, const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
-    constexpr bool WHOLE = decltype(whole)::value;
-    // the reads end well before the step does, so that the waves' meeting finds them done; faster than one in three
-    // instructions they would queue at LDS (128 bytes a cycle for the four waves)
-    constexpr int N = FM * FN, READ = N == 64 ? 3 : 1, LOAD = N / LOADS;
-    wait_vmcnt<(Cfg::RING - 2) * LOADS>();   // this wave's loads of step s + 1
-    lds_barrier();                           // every wave's; and every wave has read step s
-    const uint32_t next = cur == (Cfg::RING - 1) * Cfg::STEP ? 0 : cur + Cfg::STEP;
-    const uint32_t pa = a_first + next, pb = b_first + next;
-    uint32_t ta = 0, tb = 0;
-    if constexpr (!WHOLE) {
-      na = A.desc(s + Cfg::RING);
-      nb = B.desc(s + Cfg::RING);
-      ta = A.tail(s + Cfg::RING);
-      tb = B.tail(s + Cfg::RING);
-    }
-    each_of<N>([&](auto m_) {
+  const uint64_t adv_a = 2 * A.step, adv_b = 2 * B.step;
+  // the matrix instructions of 32 k on (a, b); f(m) behind instruction m
+  auto multiply = [&](const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], auto f) {
+    each_of<FM * FN>([&](auto m_) {
       constexpr int m = decltype(m_)::value, j = m / FM, i = m % FM;
       // tied in and out of the instruction in the accumulation registers (as a builtin, the compiler moves the
       // small accumulators between registers every step)
       asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(b[j]), "v"(a[i]));
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (m % READ == 0) {
-        constexpr int q = m / READ;
-        if constexpr (q < FM) an[q] = A.frag(pa, q);
-        else if constexpr (q < FM + FN) bn[q - FM] = B.frag(pb, q - FM);
-      }
-      if constexpr (m % LOAD == LOAD / 2) {
-        dma(std::integral_constant<int, m / LOAD>(), cur, na, nb, ta, tb);
-        if constexpr (WHOLE && m / LOAD == LA - 1) forward(na, adv_a);
-        if constexpr (WHOLE && m / LOAD == LOADS - 1) forward(nb, adv_b);
-      }
+      f(m_);
       __builtin_amdgcn_sched_barrier(0);
     });
-    cur = next;
   };
-  int s = 0;
-  for (const int whole = (int)(g.K / 32) - Cfg::RING; s + 1 < whole; s += 2) {
-    step(std::true_type(), s, a0, b0, a1, b1);
-    step(std::true_type(), s + 1, a1, b1, a0, b0);
-  }
-  for (; s < steps; s += 2) {
-    step(std::false_type(), s, a0, b0, a1, b1);
-    if (s + 1 < steps) step(std::false_type(), s + 1, a1, b1, a0, b0);
+  constexpr int N = FM * FN;
+  // operand fragment q (A's first) of k 32 kk .. of the buffers at pa and pb, behind instruction READ q: the reads end well
+  // before the next meeting of the waves, which waits for them
+  constexpr int READ = N == 64 ? 3 : 1;
+  auto read = [&](auto m_, int kk, uint32_t pa, uint32_t pb, bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
+    constexpr int m = decltype(m_)::value, q = m / READ;
+    if constexpr (m % READ == 0) {
+      if constexpr (q < FM) an[q] = A.frag(pa, kk, q);
+      else if constexpr (q < FM + FN) bn[q - FM] = B.frag(pb, kk, q - FM);
+    }
+  };
+  bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
+  auto first = [&] {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a0[i] = A.frag(a_first, 0, i);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b0[j] = B.frag(b_first, 0, j);
+  };
+  // WHOLE below: the k that are loaded lie whole inside K, so the descriptor is the last one moved on
+  if constexpr (Cfg::KU == 64) {
+    static_assert(Cfg::NA == 2 && Cfg::NB == 3, "");
+    fill_a(0);
+    fill_b(0);
+    fill_b(1);
+    fill_a(1);
+    wait_vmcnt<LA + LB>();   // unit 0
+    lds_barrier();
+    first();
+    uint32_t ca = 0, cb = 0;   // unit u's buffers, in bytes
+    u32x4 na = A.desc(2), nb = B.desc(2);
+    auto unit = [&](auto whole, int u) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      constexpr int LOAD_B = N / LB, LOAD_A = N / 2 / LA;
+      uint32_t t[4] = {0, 0, 0, 0};
+      if constexpr (!WHOLE) {
+        na = A.desc(u + 2);
+        nb = B.desc(u + 2);
+        t[0] = A.tail(u + 2, 0), t[1] = A.tail(u + 2, 1), t[2] = B.tail(u + 2, 0), t[3] = B.tail(u + 2, 1);
+      }
+      const uint32_t b1st = cb + Cfg::B_BYTES == 3 * Cfg::B_BYTES ? 0 : cb + Cfg::B_BYTES;        // of unit u + 1
+      const uint32_t b2nd = b1st + Cfg::B_BYTES == 3 * Cfg::B_BYTES ? 0 : b1st + Cfg::B_BYTES;    // and u + 2 (u - 1)
+      // unit u's second half is read; B's unit u + 2 goes where unit u - 1 was
+      multiply(a0, b0, [&](auto m_) {
+        constexpr int m = decltype(m_)::value;
+        read(m_, 1, a_first + ca, b_first + cb, a1, b1);
+        if constexpr (m % LOAD_B == LOAD_B / 2) {
+          load_b(std::integral_constant<int, m / LOAD_B>(), b2nd, nb, t[2], t[3]);
+          if constexpr (WHOLE && m / LOAD_B == LB - 1) forward(nb, adv_b);
+        }
+      });
+      wait_vmcnt<LB>();   // this wave's loads of unit u + 1
+      lds_barrier();      // every wave's; and every wave has read unit u
+      multiply(a1, b1, [&](auto m_) {
+        constexpr int m = decltype(m_)::value;
+        read(m_, 0, a_first + (ca ^ Cfg::A_BYTES), b_first + b1st, a0, b0);
+        if constexpr (m % LOAD_A == LOAD_A / 2 && m / LOAD_A < LA) {
+          load_a(std::integral_constant<int, m / LOAD_A>(), ca, na, t[0], t[1]);
+          if constexpr (WHOLE && m / LOAD_A == LA - 1) forward(na, adv_a);
+        }
+      });
+      ca ^= Cfg::A_BYTES;
+      cb = b1st;
+    };
+    int u = 0;
+    for (const int whole = (int)(g.K / 64) - 2; u < whole; ++u) unit(std::true_type(), u);
+    for (; u < units; ++u) unit(std::false_type(), u);
+  } else {
+    constexpr int RING = Cfg::NA;
+    static_assert(Cfg::NA == Cfg::NB && Cfg::KU == 32, "");
+#pragma unroll
+    for (int u = 0; u < RING; ++u) {
+      fill_a(u);
+      fill_b(u);
+    }
+    wait_vmcnt<(RING - 1) * LOADS>();   // unit 0
+    lds_barrier();
+    first();
+    uint32_t ca = 0, cb = 0;   // unit u's buffers, in bytes
+    u32x4 na = A.desc(RING), nb = B.desc(RING);
+    auto unit = [&](auto whole, int u, const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      constexpr int LOAD = N / LOADS;
+      wait_vmcnt<(RING - 2) * LOADS>();   // this wave's loads of unit u + 1
+      lds_barrier();                      // every wave's; and every wave has read unit u
+      const uint32_t xa = ca == (RING - 1) * Cfg::A_BYTES ? 0 : ca + Cfg::A_BYTES, xb = cb == (RING - 1) * Cfg::B_BYTES ? 0 : cb + Cfg::B_BYTES;
+      uint32_t t[2] = {0, 0};
+      if constexpr (!WHOLE) {
+        na = A.desc(u + RING);
+        nb = B.desc(u + RING);
+        t[0] = A.tail(u + RING, 0), t[1] = B.tail(u + RING, 0);
+      }
+      multiply(a, b, [&](auto m_) {
+        constexpr int m = decltype(m_)::value, l = m / LOAD;
+        read(m_, 0, a_first + xa, b_first + xb, an, bn);
+        if constexpr (m % LOAD == LOAD / 2) {
+          if constexpr (l < LA) load_a(std::integral_constant<int, l>(), ca, na, t[0], t[0]);
+          else load_b(std::integral_constant<int, l - LA>(), cb, nb, t[1], t[1]);
+          if constexpr (WHOLE && l == LA - 1) forward(na, adv_a);
+          if constexpr (WHOLE && l == LOADS - 1) forward(nb, adv_b);
+        }
+      });
+      ca = xa;
+      cb = xb;
+    };
+    int u = 0;
+    for (const int whole = (int)(g.K / 32) - RING; u + 1 < whole; u += 2) {
+      unit(std::true_type(), u, a0, b0, a1, b1);
+      unit(std::true_type(), u + 1, a1, b1, a0, b0);
+    }
+    for (; u < units; u += 2) {
+      unit(std::false_type(), u, a0, b0, a1, b1);
+      if (u + 1 < units) unit(std::false_type(), u + 1, a1, b1, a0, b0);
+    }
   }
   wait_vmcnt<0>();   // no load may land in LDS any more
   // the last instructions' results before any other instruction reads them (the compiler does not see
@@ -668,8 +747,8 @@ bool tile_ok(const Linear& g) {
          g.lda < (1 << 22) && g.ldb < (1 << 22) && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
 }
 
-using Lin256 = LinCfg<8, 8>;
-using Lin128 = LinCfg<4, 4>;
+using Lin256 = LinCfg<8, 8, 64, 2, 3>;
+using Lin128 = LinCfg<4, 4, 32, 5, 5>;
 
 template <bool AT, bool BT, int EPI, int ACT>
 hipError_t run_sized(const Linear& g, hipStream_t s) {

@@ -810,11 +810,12 @@ nm_status rms_norm_bwd_work_bytes(int64_t T, int64_t D, int64_t* bytes);
  *   Y [M][ldy] bf16 or fp32 (out); pre [M][ldp] bf16: z, what the backward pass reads (NULL: not stored)
  * Sums, z and the activation are fp32; Y and pre are rounded once each.  bf16 only (NM_ERR_UNSUPPORTED).  Y may be
  * the residual (bf16).  The tiled kernels run when K, ldx and ldw are multiples of 8 and X and W are
- * 16-byte aligned; other calls take a slower general kernel.
+ * 16-byte aligned; other calls take a slower general kernel.  work: see linear_work_bytes.
  */
 nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
                      const void* bias, nm_act act, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K,
-                     nm_dtype out, void* Y, int64_t ldy, void* pre, int64_t ldp, nm_stream stream);
+                     nm_dtype out, void* Y, int64_t ldy, void* pre, int64_t ldp, void* work, int64_t work_bytes,
+                     nm_stream stream);
 
 /*
  * linear_bwd_act -- the gradient of an activation and of the bias in front of it:
@@ -844,7 +845,7 @@ nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes);
  */
 nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W, int64_t ldw, const void* pre,
                        int64_t ldp, nm_act act, int64_t M, int64_t N, int64_t K, nm_dtype out, void* dX, int64_t lddx,
-                       nm_stream stream);
+                       void* work, int64_t work_bytes, nm_stream stream);
 
 /*
  * linear_bwd_w -- the gradient of linear_fwd's weight:
@@ -854,7 +855,17 @@ nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W,
  * are multiples of 8 and dZ and X are 16-byte aligned.
  */
 nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
-                       int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, nm_stream stream);
+                       int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, void* work, int64_t work_bytes,
+                       nm_stream stream);
+
+/*
+ * linear_work_bytes -- host only: the work memory that linear_fwd, linear_bwd_x or linear_bwd_w uses for these sizes
+ * (*bytes; 0 for most).  Where C has too few tiles for the GPU, the reduction is cut into parts whose fp32 sums go
+ * through it, and a second launch adds them in their order.  `work` is device memory, 16-byte aligned
+ * (NM_ERR_ALIGN); with less of it, or NULL, the reduction is not cut and the call is slower.
+ */
+typedef enum { NM_LINEAR_FWD = 0, NM_LINEAR_BWD_X = 1, NM_LINEAR_BWD_W = 2 } nm_linear;
+nm_status linear_work_bytes(nm_linear call, int64_t M, int64_t N, int64_t K, int64_t* bytes);
 
 /*
  * grad_norm -- the norm of n tensors together: norm = sqrt(sum over all elements of g^2), one fp32 value.

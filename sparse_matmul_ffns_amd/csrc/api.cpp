@@ -632,18 +632,19 @@ nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H,
 
 nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
                      const void* bias, nm_act act, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K,
-                     nm_dtype out, void* Y, int64_t ldy, void* pre, int64_t ldp, nm_stream stream) {
+                     nm_dtype out, void* Y, int64_t ldy, void* pre, int64_t ldp, void* work, int64_t work_bytes,
+                     nm_stream stream) {
   if (!X || !W || !Y) return NM_ERR_NULL;
   if (dt != NM_BF16 || !dtype_ok(out) || (bias && !dtype_ok(bdt)) || !act_ok(act)) return NM_ERR_UNSUPPORTED;
   if (!rows_ok(M, N) || !rows_ok(K, 1) || ldx < K || ldw < K || (residual && ldr < N) || ldy < N || (pre && ldp < N))
     return NM_ERR_SHAPE;
   if (!aligned(X, 2) || !aligned(W, 2) || (bias && !aligned(bias, esize(bdt))) || !aligned(residual, 2) ||
-      !aligned(Y, esize(out)) || !aligned(pre, 2))
+      !aligned(Y, esize(out)) || !aligned(pre, 2) || !aligned(work, 16))
     return NM_ERR_ALIGN;
   const nms::Linear g{(const uint16_t*)X, ldx, (const uint16_t*)W, ldw, 0, 0, M, N, K, Y, ldy, out == NM_BF16,
                       nms::EPI_FWD, bias, bdt == NM_BF16, act, (const uint16_t*)residual, ldr, (uint16_t*)pre, ldp,
-                      nullptr, 0};
-  return hip_status(nms::launch_linear(g, hs(stream)));
+                      nullptr, 0, 0};
+  return hip_status(nms::launch_linear(g, (float*)work, work ? work_bytes : 0, hs(stream)));
 }
 
 nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes) {
@@ -671,28 +672,41 @@ nm_status linear_bwd_act(nm_dtype dt, const void* dY, int64_t lddy, const void* 
 
 nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W, int64_t ldw, const void* pre,
                        int64_t ldp, nm_act act, int64_t M, int64_t N, int64_t K, nm_dtype out, void* dX, int64_t lddx,
-                       nm_stream stream) {
+                       void* work, int64_t work_bytes, nm_stream stream) {
   if (!dZ || !W || !dX || (!pre && act != NM_ACT_NONE)) return NM_ERR_NULL;
   if (dt != NM_BF16 || !dtype_ok(out) || !act_ok(act)) return NM_ERR_UNSUPPORTED;
   if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldw < K || (act != NM_ACT_NONE && ldp < K) || lddx < K)
     return NM_ERR_SHAPE;
-  if (!aligned(dZ, 2) || !aligned(W, 2) || !aligned(pre, 2) || !aligned(dX, esize(out))) return NM_ERR_ALIGN;
+  if (!aligned(dZ, 2) || !aligned(W, 2) || !aligned(pre, 2) || !aligned(dX, esize(out)) || !aligned(work, 16))
+    return NM_ERR_ALIGN;
   // rows of dZ times columns of W: the product's columns are W's, its reduction runs over W's rows
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)W, ldw, 0, 1, M, K, N, dX, lddx, out == NM_BF16,
                       act == NM_ACT_NONE ? nms::EPI_PLAIN : nms::EPI_GATE, nullptr, 0, act, nullptr, 0, nullptr, 0,
-                      (const uint16_t*)pre, ldp};
-  return hip_status(nms::launch_linear(g, hs(stream)));
+                      (const uint16_t*)pre, ldp, 0};
+  return hip_status(nms::launch_linear(g, (float*)work, work ? work_bytes : 0, hs(stream)));
 }
 
 nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
-                       int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, nm_stream stream) {
+                       int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, void* work, int64_t work_bytes,
+                       nm_stream stream) {
   if (!dZ || !X || !dW) return NM_ERR_NULL;
   if (dt != NM_BF16 || !dtype_ok(out) || (accumulate && out != NM_F32)) return NM_ERR_UNSUPPORTED;
   if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldx < K || lddw < K) return NM_ERR_SHAPE;
-  if (!aligned(dZ, 2) || !aligned(X, 2) || !aligned(dW, esize(out))) return NM_ERR_ALIGN;
+  if (!aligned(dZ, 2) || !aligned(X, 2) || !aligned(dW, esize(out)) || !aligned(work, 16)) return NM_ERR_ALIGN;
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)X, ldx, 1, 1, N, K, M, dW, lddw, out == NM_BF16,
-                      accumulate ? nms::EPI_ADD : nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0};
-  return hip_status(nms::launch_linear(g, hs(stream)));
+                      accumulate ? nms::EPI_ADD : nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0, 0};
+  return hip_status(nms::launch_linear(g, (float*)work, work ? work_bytes : 0, hs(stream)));
+}
+
+nm_status linear_work_bytes(nm_linear call, int64_t M, int64_t N, int64_t K, int64_t* bytes) {
+  if (!bytes) return NM_ERR_NULL;
+  if (!rows_ok(M, N) || !rows_ok(K, 1)) return NM_ERR_SHAPE;
+  switch (call) {
+    case NM_LINEAR_FWD: *bytes = nms::linear_work_bytes(0, 0, M, N, K); return NM_OK;
+    case NM_LINEAR_BWD_X: *bytes = nms::linear_work_bytes(0, 1, M, K, N); return NM_OK;
+    case NM_LINEAR_BWD_W: *bytes = nms::linear_work_bytes(1, 1, N, K, M); return NM_OK;
+  }
+  return NM_ERR_UNSUPPORTED;
 }
 
 nm_status grad_work_bytes(int64_t n, const int64_t* counts, int64_t* bytes) {

@@ -205,6 +205,7 @@ struct LinCfg {
   static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN, KU = KU_, NA = NA_, NB = NB_;
   static constexpr int A_BYTES = BM * 2 * KU, B_BYTES = BN * 2 * KU, LDS = NA * A_BYTES + NB * B_BYTES;
   static constexpr int LA = A_BYTES / 4096, LB = B_BYTES / 4096, LOADS = LA + LB;   // 1 KB loads a wave and buffer
+  static constexpr int PER_CU = 163840 / LDS;   // workgroups that a CU holds at once
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -291,8 +292,9 @@ struct Operand {
 template <int FM, int FN>
 struct Out {
   static constexpr int COLS = 16 * FN, H = COLS / 64;                 // H: runs of 64 columns
-  static constexpr int ROWS = (FM + FN) * 2048 / (COLS * 4), PF = ROWS / 16, PASSES = FM / PF;   // of a pass
-  static_assert(ROWS % 16 == 0 && FM % PF == 0, "a pass is whole fragments");
+  static constexpr int ROWS = 64, PF = ROWS / 16, PASSES = FM / PF;   // ROWS: of a pass
+  static constexpr int REGION = ROWS * COLS * 4;                      // a wave's bytes of LDS
+  static_assert(FM % PF == 0, "a pass is whole fragments");
   template <int P>
   __device__ static void put(const f32x4 (&acc)[FM][FN], unsigned char* region, int lane) {
     const int l16 = lane & 15, lq = lane >> 4;
@@ -449,7 +451,15 @@ __device__ inline void xcd_tile(int id, int ntm, int ntn, int& tm, int& tn) {
 }
 
 template <bool AT, bool BT, int EPI, int ACT, typename Cfg>
-__global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(Linear g) {
+__global__ __launch_bounds__(256, Cfg::PER_CU) void linear_tile_kernel(Linear g) {
+  if (gridDim.y > 1) {
+    // a part of the reduction, whose sums go to a matrix of their own
+    const int64_t k0 = (int64_t)blockIdx.y * g.part_k;
+    g.A += AT ? k0 * g.lda : k0;
+    g.B += BT ? k0 * g.ldb : k0;
+    g.K = g.K - k0 < g.part_k ? g.K - k0 : g.part_k;
+    g.C = (float*)g.C + blockIdx.y * g.M * g.ldc;
+  }
   constexpr int FM = Cfg::FM, FN = Cfg::FN, LA = Cfg::LA, LB = Cfg::LB, LOADS = Cfg::LOADS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int lane = threadIdx.x & 63;
@@ -513,7 +523,7 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   constexpr int N = FM * FN;
   // operand fragment q (A's first) of k 32 kk .. of the buffers at pa and pb, behind instruction READ q: the reads end well
   // before the next meeting of the waves, which waits for them
-  constexpr int READ = N == 64 ? 3 : 1;
+  constexpr int READ = N / (FM + FN) > 3 ? 3 : N / (FM + FN);
   auto read = [&](auto m_, int kk, uint32_t pa, uint32_t pb, bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
     constexpr int m = decltype(m_)::value, q = m / READ;
     if constexpr (m % READ == 0) {
@@ -629,34 +639,46 @@ __global__ __launch_bounds__(256, Cfg::FM == 8 ? 1 : 2) void linear_tile_kernel(
   // the instructions inside the assembly statements)
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   lds_barrier();   // every wave has read its last operands: the buffers are free
-  tile_epilogue<EPI, ACT>(g, acc, smem + wave * (Cfg::LDS / 5), m0 + wm, n0 + wn, lane);
+  tile_epilogue<EPI, ACT>(g, acc, smem + wave * Out<FM, FN>::REGION, m0 + wm, n0 + wn, lane);
+}
+
+// What C becomes of the parts' sums, added in their order.
+__global__ __launch_bounds__(256) void linear_join_kernel(Linear g, const float* part, int64_t ld, int parts) {
+  const int64_t per = (g.N + 3) / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = id / per, n = id % per * 4;
+  if (m >= g.M) return;
+  const float* p = part + m * ld + n;
+  f32x4 v = *reinterpret_cast<const f32x4*>(p);
+  for (int s = 1; s < parts; ++s) v += *reinterpret_cast<const f32x4*>(p + s * g.M * ld);
+  finish4(g, m, n, v);
 }
 
 template <bool AT, bool BT, int EPI, int ACT, typename Cfg>
-hipError_t run_tile(const Linear& g, hipStream_t s) {
+hipError_t run_tile(const Linear& g, int parts, hipStream_t s) {
   auto kern = linear_tile_kernel<AT, BT, EPI, ACT, Cfg>;
   (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS);
   const int64_t wgs = (g.M + Cfg::BM - 1) / Cfg::BM * ((g.N + Cfg::BN - 1) / Cfg::BN);
   if (!grid_ok(wgs, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), Cfg::LDS, s, g);
+  hipLaunchKernelGGL(kern, dim3((unsigned)wgs, (unsigned)parts), dim3(256), Cfg::LDS, s, g);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Few rows of A (serving): B is read once and that bounds the call, so its bytes go straight from memory to
 // the registers of the matrix instruction, with no LDS and no barrier on the way.  A workgroup computes 16 FM rows of A by
-// 32 rows of B; its KS waves take every KS-th chunk of 128 k, each with the next chunk's loads in flight, and
+// 16 FN rows of B; its KS waves take every KS-th chunk of 32 CH k, each with the next chunk's loads in flight, and
 // add their sums through LDS in the order of the waves.  The lanes of a row that does not exist load nothing.
+// One token (FM 1, FN 1, KS 8, CH 4), weights that are not in a cache: 16384 x 4096 24 us (5.5 TB/s, a large copy's rate),
+// 8192 x 2048 8.7 us; with FN 2 and KS 4 31 and 10.4.
 // ---------------------------------------------------------------------------
-template <int FM, int KS>
+template <int FM, int FN, int KS, int CH>
 __global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
-  constexpr int FN = 2, CH = 4;   // CH: matrix instructions (32 k each) a chunk and fragment pair
   __shared__ f32x4 part[KS][FM * FN][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int ntn = (int)((g.N + 31) / 32);
-  const int64_t m0 = (int64_t)(blockIdx.x / ntn) * (16 * FM), n0 = (int64_t)(blockIdx.x % ntn) * 32;
+  const int ntn = (int)((g.N + 16 * FN - 1) / (16 * FN));
+  const int64_t m0 = (int64_t)(blockIdx.x / ntn) * (16 * FM), n0 = (int64_t)(blockIdx.x % ntn) * (16 * FN);
   const uint16_t *arow[FM], *brow[FN];
   bool aon[FM], bon[FN];
 #pragma unroll
@@ -732,14 +754,13 @@ __global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
   }
 }
 
-template <int FM, int KS>
+template <int FM, int FN, int KS, int CH>
 hipError_t run_rows(const Linear& g, hipStream_t s) {
-  const int64_t wgs = (g.M + 16 * FM - 1) / (16 * FM) * ((g.N + 31) / 32);
+  const int64_t wgs = (g.M + 16 * FM - 1) / (16 * FM) * ((g.N + 16 * FN - 1) / (16 * FN));
   if (!grid_ok(wgs, 64 * KS)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((linear_rows_kernel<FM, KS>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
+  hipLaunchKernelGGL((linear_rows_kernel<FM, FN, KS, CH>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
   return hipGetLastError();
 }
-
 // The tiled kernel's conditions: 16-byte loads that lie inside the operand or outside it, and 31-bit offsets
 // inside a tile.
 bool tile_ok(const Linear& g) {
@@ -748,41 +769,117 @@ bool tile_ok(const Linear& g) {
 }
 
 using Lin256 = LinCfg<8, 8, 64, 2, 3>;
+using Lin256x128 = LinCfg<8, 4, 64, 2, 3>;
 using Lin128 = LinCfg<4, 4, 32, 5, 5>;
 
 template <bool AT, bool BT, int EPI, int ACT>
-hipError_t run_sized(const Linear& g, hipStream_t s) {
-  auto tiles = [&](int64_t b) { return (g.M + b - 1) / b * ((g.N + b - 1) / b); };
-  const bool large = (tiles(256) + 255) / 256 * 5 <= (tiles(128) + 511) / 512 * 3;
-  return large ? run_tile<AT, BT, EPI, ACT, Lin256>(g, s) : run_tile<AT, BT, EPI, ACT, Lin128>(g, s);
+hipError_t run_sized(const Linear& g, const LinearPlan& p, hipStream_t s) {
+  switch (p.tile) {
+    case LinearPlan::T256: return run_tile<AT, BT, EPI, ACT, Lin256>(g, p.parts, s);
+    case LinearPlan::T256x128: return run_tile<AT, BT, EPI, ACT, Lin256x128>(g, p.parts, s);
+  }
+  return run_tile<AT, BT, EPI, ACT, Lin128>(g, p.parts, s);
 }
 template <bool BT, int EPI>
-hipError_t run_act(const Linear& g, hipStream_t s) {
+hipError_t run_act(const Linear& g, const LinearPlan& p, hipStream_t s) {
   switch (g.act) {
-    case ACT_RELU: return run_sized<false, BT, EPI, ACT_RELU>(g, s);
-    case ACT_GELU_TANH: return run_sized<false, BT, EPI, ACT_GELU_TANH>(g, s);
-    case ACT_SILU: return run_sized<false, BT, EPI, ACT_SILU>(g, s);
+    case ACT_RELU: return run_sized<false, BT, EPI, ACT_RELU>(g, p, s);
+    case ACT_GELU_TANH: return run_sized<false, BT, EPI, ACT_GELU_TANH>(g, p, s);
+    case ACT_SILU: return run_sized<false, BT, EPI, ACT_SILU>(g, p, s);
   }
-  if constexpr (EPI == EPI_FWD) return run_sized<false, BT, EPI, ACT_NONE>(g, s);
+  if constexpr (EPI == EPI_FWD) return run_sized<false, BT, EPI, ACT_NONE>(g, p, s);
   return hipErrorInvalidValue;   // a gate has an activation
 }
 
-hipError_t linear_piece(const Linear& g, hipStream_t s) {
-  if (force_generic() || !tile_ok(g)) return run_general(g, s);
+hipError_t run_tiles(const Linear& g, const LinearPlan& p, hipStream_t s) {
   if (!g.a_t && !g.b_t) {
-    if (g.M <= 64 && (g.N + 127) / 128 <= 256) return g.M > 16 ? run_rows<2, 4>(g, s) : run_rows<1, 4>(g, s);
-    return run_act<false, EPI_FWD>(g, s);
+    return g.epi == EPI_FWD ? run_act<false, EPI_FWD>(g, p, s) : run_sized<false, false, EPI_PLAIN, ACT_NONE>(g, p, s);
   }
   if (g.a_t) {
-    return g.epi == EPI_ADD ? run_sized<true, true, EPI_ADD, ACT_NONE>(g, s)
-                            : run_sized<true, true, EPI_PLAIN, ACT_NONE>(g, s);
+    return g.epi == EPI_ADD ? run_sized<true, true, EPI_ADD, ACT_NONE>(g, p, s)
+                            : run_sized<true, true, EPI_PLAIN, ACT_NONE>(g, p, s);
   }
-  return g.epi == EPI_GATE ? run_act<true, EPI_GATE>(g, s) : run_sized<false, true, EPI_PLAIN, ACT_NONE>(g, s);
+  return g.epi == EPI_GATE ? run_act<true, EPI_GATE>(g, p, s) : run_sized<false, true, EPI_PLAIN, ACT_NONE>(g, p, s);
+}
+
+hipError_t linear_piece(const Linear& g, const LinearPlan& p, float* work, hipStream_t s) {
+  if (force_generic() || !tile_ok(g)) return run_general(g, s);
+  if (p.tile == LinearPlan::ROWS) return g.M > 16 ? run_rows<2, 2, 8, 4>(g, s) : run_rows<1, 1, 8, 4>(g, s);
+  if (p.parts == 1) return run_tiles(g, p, s);
+  Linear q = g;
+  q.epi = EPI_PLAIN;
+  q.C = work;
+  q.ldc = (g.N + 3) / 4 * 4;
+  q.bf16_out = 0;
+  q.act = ACT_NONE;
+  q.bias = nullptr;
+  q.R = nullptr;
+  q.Z = nullptr;
+  q.P = nullptr;
+  q.part_k = p.part_k;
+  const hipError_t e = run_tiles(q, p, s);
+  if (e != hipSuccess) return e;
+  const int64_t wgs = (g.M * ((g.N + 3) / 4) + 255) / 256;
+  if (!grid_ok(wgs, 256)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)wgs), dim3(256), 0, s, g, (const float*)work, q.ldc, p.parts);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear(const Linear& g, hipStream_t s) {
+// The kernel for a product, by what each is expected to take: `full` rounds of as many workgroups as the GPU holds and
+// a last one, each a fixed time and one per 1024 k that grows with the part x of the GPU that is at work (its
+// power and the memory behind the L2s are shared), and where the reduction is cut the parts' bytes and a launch.  The constants are fits
+// of measured times, in us: 4096 x 4096 x 4096 takes 97 with 256 x 256 tiles, 119 with 256 x 128, 137 to 160 with 128 x
+// 128; 4096 x 2048 x 8192 151, 107, 138 to 159, and 115 in two parts of 256 x 256; 1024 x 8192 x 2048 46, 33, 39 to 45; 512 x 2048
+// x 8192 130, 80, 56, and 30 in four parts of 128 x 128; 32 x 2048 x 8192 129, 75, 51, and 16 in eight; 1000^3 37, 22, 14.
+struct TileCost {
+  int tile, bm, bn, held;          // held: workgroups that the GPU computes at once
+  double fixed, alone, shared;     // a round: fixed + (alone + shared x^2) per 1024 k
+};
+constexpr TileCost kTiles[] = {{LinearPlan::T128, 128, 128, 256, 5, 6.1, 2.1},
+                               {LinearPlan::T256x128, 256, 128, 256, 7, 9.2, 3.3},
+                               {LinearPlan::T256, 256, 256, 256, 10, 15, 6.5}};
+
+static double round_us(const TileCost& t, double k, int64_t workgroups) {
+  // two 128 x 128 tiles fit a CU, and together take as long as one after the other
+  if (t.tile == LinearPlan::T128 && workgroups > t.held) return t.fixed + 16.5 * k;
+  const double x = (double)workgroups / t.held;
+  return t.fixed + (t.alone + t.shared * x * x) * k;
+}
+
+static LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K) {
+  // Few rows: the kernel without LDS, against the best of the tiles in us: 1 x 16384 x 4096 24 and 31, 1 x 2048 x 8192 12 and 16, 16 x
+  // 8192 x 2048 11 and 15, 16 x 2048 x 8192 18 and 18; 32 x 8192 x 2048 13 and 15, but 32 x 2048 x 8192 26 and 18
+  if (!a_t && !b_t && (M <= 16 || (M <= 32 && K <= 2048))) return LinearPlan{LinearPlan::ROWS, 1, K};
+  LinearPlan best{LinearPlan::T256, 1, K};
+  double least = 1e30;
+  for (const TileCost& t : kTiles) {
+    const int64_t tiles = (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn);
+    const int64_t round = t.tile == LinearPlan::T128 ? 2 * t.held : t.held;
+    for (int p = 1; p <= 16 && (p == 1 || (K >= 256 * p && tiles * p <= 2 * round)); ++p) {
+      const int64_t part_k = p == 1 ? K : ((K + p - 1) / p + 63) / 64 * 64, parts = (K + part_k - 1) / part_k, wgs = tiles * parts;
+      const double k = part_k / 1024.0;
+      double us = (double)(wgs / round) * round_us(t, k, round);
+      if (wgs % round) us += round_us(t, k, wgs % round);
+      if (parts > 1) us += 4 + 8e-6 / 6 * (double)(parts * M) * (double)N;
+      if (us < least) {
+        least = us;
+        best = LinearPlan{t.tile, (int)parts, part_k};
+      }
+    }
+  }
+  return best;
+}
+static int64_t part_bytes(const LinearPlan& p, int64_t M, int64_t N) {
+  return p.parts > 1 ? p.parts * M * ((N + 3) / 4 * 4) * 4 : 0;
+}
+int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K) {
+  const int64_t m = M < kPieceRows ? M : kPieceRows;
+  return part_bytes(linear_plan(a_t, b_t, m, N, K), m, N);
+}
+
+hipError_t launch_linear(const Linear& g, float* work, int64_t work_bytes, hipStream_t s) {
   return in_pieces(g.M, kPieceRows, [&](int64_t m0, int64_t n) {
     Linear p = g;
     p.A += g.a_t ? m0 : m0 * g.lda;
@@ -791,7 +888,9 @@ hipError_t launch_linear(const Linear& g, hipStream_t s) {
     if (g.R) p.R += m0 * g.ldr;
     if (g.Z) p.Z += m0 * g.ldz;
     if (g.P) p.P += m0 * g.ldp;
-    return linear_piece(p, s);
+    LinearPlan plan = linear_plan(g.a_t, g.b_t, n, g.N, g.K);
+    if (work_bytes < part_bytes(plan, n, g.N)) plan.parts = 1;
+    return linear_piece(p, plan, work, s);
   });
 }
 

@@ -25,6 +25,7 @@ NM_F32, NM_BF16 = 0, 1
 NM_E4M3, NM_E5M2 = 0, 1
 NM_SOFTMAX, NM_SIGMOID = 0, 1
 NM_ACT_NONE, NM_ACT_RELU, NM_ACT_GELU_TANH, NM_ACT_SILU = range(4)
+NM_LINEAR_FWD, NM_LINEAR_BWD_X, NM_LINEAR_BWD_W = range(3)
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -83,11 +84,12 @@ _SIGNATURES = {
                      _vp],
     "rms_norm_bwd_work_bytes": [_i64, _i64, ctypes.POINTER(_i64)],
     "linear_fwd": [_int, _vp, _i64, _vp, _i64, _int, _vp, _int, _vp, _i64, _i64, _i64, _i64, _int, _vp, _i64, _vp,
-                   _i64, _vp],
+                   _i64, _vp, _i64, _vp],
     "linear_bwd_act": [_int, _vp, _i64, _vp, _i64, _int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp],
     "linear_bwd_act_work_bytes": [_i64, _i64, ctypes.POINTER(_i64)],
-    "linear_bwd_x": [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp],
-    "linear_bwd_w": [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp],
+    "linear_bwd_x": [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp],
+    "linear_bwd_w": [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp],
+    "linear_work_bytes": [_int, _i64, _i64, _i64, ctypes.POINTER(_i64)],
     "grad_norm": [_i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
     "grad_clip": [_i64, _vp, _vp, _vp, _f32, _int, _vp, _vp, _vp, _vp, _i64, _vp],
     "grad_work_bytes": [_i64, _vp, ctypes.POINTER(_i64)],
@@ -1127,8 +1129,16 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, w: torch.Tensor, rstd: torch
     return dX, dw
 
 
+@functools.lru_cache(maxsize=256)
+def _linear_work_bytes(call: int, M: int, N: int, K: int) -> int:
+    need = _i64()
+    _check(lib().linear_work_bytes(call, M, N, K, ctypes.byref(need)), "linear_work_bytes")
+    return need.value
+
+
 def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", residual=None,
-               out_dtype: torch.dtype = torch.bfloat16, out=None, pre=None, return_pre: bool = False):
+               out_dtype: torch.dtype = torch.bfloat16, out=None, pre=None, return_pre: bool = False,
+               work="auto"):
     """Y = act(X [M, K] @ W [N, K].T + bias) + residual, bf16 operands and fp32 sums; act is 'none', 'relu',
     'gelu_tanh' or 'silu'.  With `pre` (a tensor) or `return_pre` returns (Y, pre), pre [M, N] bf16 the sum before the
     activation, what linear_bwd_act and linear_bwd_x read.  In place: out may be the residual."""
@@ -1145,8 +1155,10 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
     if pre is None and return_pre:
         pre = X.new_empty((M, N), dtype=torch.bfloat16)
     ldp = _opt(pre, (M, N), torch.bfloat16, "pre")
+    work, nbytes = _workspace(work, _linear_work_bytes(NM_LINEAR_FWD, M, N, K), X)
     _check(lib().linear_fwd(_dt(X), _p(X), ldx, _p(W), ldw, NM_BF16 if bias is None else _dt(bias), _p(bias), _act(act),
-                            _p(residual), ldr, M, N, K, _dt(out), _p(out), ldy, _p(pre), ldp, _stream()), "linear_fwd")
+                            _p(residual), ldr, M, N, K, _dt(out), _p(out), ldy, _p(pre), ldp, _p(work), nbytes, _stream()),
+           "linear_fwd")
     return out if pre is None else (out, pre)
 
 
@@ -1179,7 +1191,7 @@ def linear_bwd_act(dY: torch.Tensor, pre=None, act: str = "none", dZ=None, db=No
 
 
 def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
-                 out_dtype: torch.dtype = torch.bfloat16, out=None) -> torch.Tensor:
+                 out_dtype: torch.dtype = torch.bfloat16, out=None, work="auto") -> torch.Tensor:
     """dX = (dZ [M, N] @ W [N, K]) act'(pre): the gradient of linear_fwd's input, and with `act` of the
     pre-activations [M, K] that the input came from (with 'relu' the input itself does as well).  In place: out may
     be pre."""
@@ -1193,13 +1205,14 @@ def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
     if out is None:
         out = dZ.new_empty((M, K), dtype=out_dtype)
     lddx = _matrix(out, (M, K), None, "out")
+    work, nbytes = _workspace(work, _linear_work_bytes(NM_LINEAR_BWD_X, M, N, K), dZ)
     _check(lib().linear_bwd_x(_dt(dZ), _p(dZ), lddz, _p(W), ldw, _p(pre), ldp, _act(act), M, N, K, _dt(out), _p(out),
-                              lddx, _stream()), "linear_bwd_x")
+                              lddx, _p(work), nbytes, _stream()), "linear_bwd_x")
     return out
 
 
 def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = torch.float32, out=None,
-                 accumulate: bool = False) -> torch.Tensor:
+                 accumulate: bool = False, work="auto") -> torch.Tensor:
     """dW [N, K] = dZ [M, N].T @ X [M, K], the gradient of linear_fwd's weight; with `accumulate` added to `out`
     (fp32), as micro-batches do."""
     M, N = _two(dZ, "dZ")
@@ -1211,8 +1224,9 @@ def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = tor
             raise ValueError("accumulate needs out")
         out = dZ.new_empty((N, K), dtype=out_dtype)
     lddw = _matrix(out, (N, K), None, "out")
+    work, nbytes = _workspace(work, _linear_work_bytes(NM_LINEAR_BWD_W, M, N, K), dZ)
     _check(lib().linear_bwd_w(_dt(dZ), _p(dZ), lddz, _p(X), ldx, M, N, K, int(bool(accumulate)), _dt(out), _p(out),
-                              lddw, _stream()), "linear_bwd_w")
+                              lddw, _p(work), nbytes, _stream()), "linear_bwd_w")
     return out
 
 

@@ -762,7 +762,7 @@ typedef enum { NM_ACT_NONE = 0, NM_ACT_RELU = 1, NM_ACT_GELU_TANH = 2, NM_ACT_SI
  *   H [T][ldh] dtype dt: h rounded, the next block's residual (NULL: not stored)
  * Sums and products are fp32 and taken from h before its rounding; every output is rounded once.
  * H may be X or the residual, Y may be X.  Squares are fp32: rows beyond 1e19 overflow.  0 < eps, finite, and
- * D <= 32768 (NM_ERR_UNSUPPORTED).
+ * D <= 16384 (NM_ERR_UNSUPPORTED).
  */
 nm_status rms_norm(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
                    const void* w, float eps, int64_t T, int64_t D, void* H, int64_t ldh, void* Y, int64_t ldy,
@@ -789,7 +789,7 @@ nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* resi
  *   work  device memory, 4-byte aligned, of rms_norm_bwd_work_bytes bytes (NULL when that is 0;
  *         NM_ERR_SHAPE when work_bytes is less)
  * dX is the gradient of X and of the residual.  It may be dY or dH.  Sums are fp32; dw's are added in an order that
- * depends on T and D alone.  D <= 32768 (NM_ERR_UNSUPPORTED).
+ * depends on T and D alone.  D <= 16384 (NM_ERR_UNSUPPORTED).
  */
 nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H, int64_t ldh, nm_dtype wdt,
                        const void* w, const float* rstd, const void* dH, int64_t lddh, int64_t T, int64_t D, void* dX,

@@ -65,7 +65,7 @@ bool act_ok(nm_act a) { return a >= NM_ACT_NONE && a <= NM_ACT_SILU; }
 // A number of rows and a width that an int holds.
 bool rows_ok(int64_t R, int64_t C) { return R > 0 && C > 0 && R <= INT32_MAX && C <= INT32_MAX; }
 bool same(const void* a, int64_t lda, const void* b, int64_t ldb) { return a == b && lda == ldb; }
-constexpr int64_t kNormWidth = 32768;   // a row stays in the registers of a workgroup
+constexpr int64_t kNormWidth = 16384;   // a row stays in the registers of a workgroup
 
 // the checks rms_norm and rms_norm_fp8 share
 nm_status norm_check(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
@@ -586,8 +586,8 @@ nm_status rms_norm(nm_dtype dt, const void* X, int64_t ldx, const void* residual
   if (!Y) return NM_ERR_NULL;
   const nm_status st = norm_check(dt, X, ldx, residual, ldr, wdt, w, eps, T, D, H, ldh, Y, ldy, rstd);
   if (st != NM_OK) return st;
-  const nms::NormArgs a{X, ldx, residual, ldr, w, eps, T, D, H, ldh, Y, ldy, rstd, nullptr, 0, nullptr, 0, 0};
-  return hip_status(nms::launch_rms_norm(dt, wdt, a, hs(stream)));
+  const nms::NormArgs a{X, ldx, residual, ldr, w, wdt == NM_BF16, eps, T, D, H, ldh, Y, ldy, rstd, nullptr, 0, nullptr, 0, 0};
+  return hip_status(nms::launch_rms_norm(dt, a, hs(stream)));
 }
 
 nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
@@ -599,8 +599,8 @@ nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* resi
   if (st != NM_OK) return st;
   if (ldq < up128(D) || lds < T) return NM_ERR_SHAPE;
   if (!aligned(S, 4)) return NM_ERR_ALIGN;
-  const nms::NormArgs a{X, ldx, residual, ldr, w, eps, T, D, H, ldh, Y, ldy, rstd, Q, ldq, S, lds, fmt == NM_E5M2};
-  return hip_status(nms::launch_rms_norm(dt, wdt, a, hs(stream)));
+  const nms::NormArgs a{X, ldx, residual, ldr, w, wdt == NM_BF16, eps, T, D, H, ldh, Y, ldy, rstd, Q, ldq, S, lds, fmt == NM_E5M2};
+  return hip_status(nms::launch_rms_norm(dt, a, hs(stream)));
 }
 
 nm_status rms_norm_bwd_work_bytes(int64_t T, int64_t D, int64_t* bytes) {
@@ -626,8 +626,8 @@ nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H,
   if (!aligned(dY, esize(dt)) || !aligned(H, esize(dt)) || !aligned(w, esize(wdt)) || !aligned(rstd, 4) ||
       !aligned(dH, esize(dt)) || !aligned(dX, esize(dt)) || !aligned(dw, 4) || !aligned(work, 4))
     return NM_ERR_ALIGN;
-  const nms::NormBwdArgs a{dY, lddy, H, ldh, w, rstd, dH, lddh, T, D, dX, lddx, dw, (float*)work};
-  return hip_status(nms::launch_rms_norm_bwd(dt, wdt, a, hs(stream)));
+  const nms::NormBwdArgs a{dY, lddy, H, ldh, w, wdt == NM_BF16, rstd, dH, lddh, T, D, dX, lddx, dw, (float*)work};
+  return hip_status(nms::launch_rms_norm_bwd(dt, a, hs(stream)));
 }
 
 nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
@@ -723,7 +723,7 @@ nm_status grad_norm(int64_t n, const nm_dtype* dt, const void* const* grads, con
   const nm_status st = grads_check(n, dt, grads, counts, norm, work, work_bytes, true);
   if (st != NM_OK) return st;
   const nms::Grads g{n, (const int*)dt, grads, counts, nullptr, nullptr};
-  return hip_status(nms::launch_grad_norm(g, norm, (double*)work, hs(stream)));
+  return hip_status(nms::launch_grads(g, false, norm, 0.f, (double*)work, hs(stream)));
 }
 
 nm_status grad_clip(int64_t n, const nm_dtype* dt, const void* const* grads, const int64_t* counts, float max_norm,
@@ -757,11 +757,7 @@ nm_status grad_clip(int64_t n, const nm_dtype* dt, const void* const* grads, con
   delete[] r;
   if (bad) return NM_ERR_SHAPE;
   const nms::Grads g{n, (const int*)dt, grads, counts, (const int*)odt, out};
-  if (!have_norm) {
-    const hipError_t e = nms::launch_grad_norm(g, norm, (double*)work, hs(stream));
-    if (e != hipSuccess) return hip_status(e);
-  }
-  return hip_status(nms::launch_grad_scale(g, norm, max_norm, hs(stream)));
+  return hip_status(nms::launch_grads(g, have_norm != 0, norm, max_norm, (double*)work, hs(stream)));
 }
 
 void nm_sizes(int64_t R, int64_t K, int N, int M, int V, int64_t* n_values, int64_t* meta_bytes,

@@ -195,6 +195,7 @@ struct NormArgs {
   const void* R;            // null: nothing is added
   int64_t ldr;
   const void* w;
+  int w_bf16;
   float eps;
   int64_t T, D;
   void* H;                  // null: the sum is not stored
@@ -208,13 +209,14 @@ struct NormArgs {
   int64_t lds;
   int e5m2;
 };
-hipError_t launch_rms_norm(int dt, int wdt, const NormArgs& a, hipStream_t s);
+hipError_t launch_rms_norm(int dt, const NormArgs& a, hipStream_t s);
 struct NormBwdArgs {
   const void* dY;
   int64_t lddy;
   const void* H;
   int64_t ldh;
   const void* w;
+  int w_bf16;
   const float* rstd;
   const void* dH;           // null: nothing comes through the residual
   int64_t lddh, T, D;
@@ -224,7 +226,7 @@ struct NormBwdArgs {
   float* work;
 };
 int64_t norm_bwd_groups(int64_t T, int64_t D);
-hipError_t launch_rms_norm_bwd(int dt, int wdt, const NormBwdArgs& a, hipStream_t s);
+hipError_t launch_rms_norm_bwd(int dt, const NormBwdArgs& a, hipStream_t s);
 // out[c] = sum of part[0 .. G - 1][c], in fp32 in a fixed order.
 hipError_t launch_sum_partials(const float* part, int64_t G, int64_t N, float* out, hipStream_t s);
 struct ActBwdArgs {
@@ -283,7 +285,7 @@ struct Grads {
   void* const* out;         // null for the norm alone
 };
 int64_t grad_partials(const int64_t* count, int64_t n);
-hipError_t launch_grad_norm(const Grads& g, float* norm, double* work, hipStream_t s);
-hipError_t launch_grad_scale(const Grads& g, const float* norm, float max_norm, hipStream_t s);
+// The norm, and with g.out the scaling (have_norm: *norm is given, and work is not used).
+hipError_t launch_grads(const Grads& g, bool have_norm, float* norm, float max_norm, double* work, hipStream_t s);
 
 }  // namespace nms

@@ -1242,19 +1242,33 @@ def _packed(t: torch.Tensor) -> bool:
     return True
 
 
+_DTS = {torch.bfloat16: NM_BF16, torch.float32: NM_F32}
+
+
 def _grads_args(grads, name: str):
-    """The host arrays of a list of tensors: dtypes, addresses, counts."""
+    """The host arrays of a list of tensors: dtypes, addresses, counts; and whether all are contiguous.  (map over the
+    methods: lists of hundreds of tensors are bound by what this costs a tensor.)"""
     n = len(grads)
     if n == 0:
         raise ValueError(f"{name} must hold a tensor at least")
-    _here(*grads)
-    for t in grads:
-        if t is None:
-            raise TypeError(f"{name} must hold tensors, not None")
-        if not t.is_contiguous() and t.numel() and not _packed(t):
-            raise ValueError(f"{name} must be tensors whose elements lie together in memory")
-    return ((_int * n)(*[_dt(t) for t in grads]), (_vp * n)(*[t.data_ptr() for t in grads]),
-            (_i64 * n)(*[t.numel() for t in grads]))
+    try:
+        counts = list(map(torch.Tensor.numel, grads))
+    except TypeError:
+        raise TypeError(f"{name} must hold tensors") from None
+    _here_all(grads)
+    dts = [_DTS.get(t.dtype) for t in grads]
+    if None in dts:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    plain = all(map(torch.Tensor.is_contiguous, grads))
+    if not plain and not all(t.is_contiguous() or t.numel() == 0 or _packed(t) for t in grads):
+        raise ValueError(f"{name} must be tensors whose elements lie together in memory")
+    return ((_int * n)(*dts), (_vp * n)(*map(torch.Tensor.data_ptr, grads)), (_i64 * n)(*counts), plain)
+
+
+def _here_all(ts) -> None:
+    """_here for a list of tensors."""
+    if set(map(torch.Tensor.get_device, ts)) != {torch._C._cuda_getDevice()}:
+        _here(*ts)
 
 
 def _grads_work(work, n, counts, like):
@@ -1267,7 +1281,7 @@ def _grads_work(work, n, counts, like):
 def grad_norm(grads, norm=None, work="auto") -> torch.Tensor:
     """The norm of all tensors together (bf16 and fp32, any shapes, each packed in memory): one fp32 value [1]."""
     grads = list(grads)
-    dt, ptr, counts = _grads_args(grads, "grads")
+    dt, ptr, counts, _ = _grads_args(grads, "grads")
     _here(norm)
     norm = _new_vector(norm, 1, grads[0], "norm")
     work, nbytes = _grads_work(work, len(grads), counts, grads[0])
@@ -1281,17 +1295,18 @@ def grad_clip(grads, max_norm: float, norm=None, out=None, work="auto") -> torch
     caller already has (of gradients that lie on several GPUs, say), instead of grad_norm's.  A norm that is
     not finite leaves the values as they are."""
     grads = list(grads)
-    dt, ptr, counts = _grads_args(grads, "grads")
+    dt, ptr, counts, plain = _grads_args(grads, "grads")
     if out is None:
         odt, optr = dt, ptr
     else:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must hold a tensor for every gradient")
-        odt, optr, _ = _grads_args(out, "out")
-        for g, o in zip(grads, out):
-            if g.shape != o.shape or (g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous())):
-                raise ValueError("out must have the gradients' shapes and orders in memory")
+        odt, optr, _, oplain = _grads_args(out, "out")
+        same = list(map(torch.Tensor.size, grads)) == list(map(torch.Tensor.size, out))
+        if not same or not (plain and oplain or all(g.stride() == o.stride() or (g.is_contiguous() and o.is_contiguous())
+                                                    for g, o in zip(grads, out))):
+            raise ValueError("out must have the gradients' shapes and orders in memory")
     have = norm is not None
     if have:
         _here(norm)

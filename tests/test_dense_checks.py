@@ -32,7 +32,7 @@ def test_norm(L):
     _refuses(L.rms_norm, good, ({1: None}, NULL), ({6: None}, NULL), ({12: None}, NULL), ({0: 2}, UNSUP), ({5: 2}, UNSUP),
              ({7: 0.0}, UNSUP), ({7: -1.0}, UNSUP), ({7: NAN}, UNSUP), ({7: INF}, UNSUP), ({8: 0}, SHAPE), ({8: 1 << 31}, SHAPE),
              ({9: 0}, SHAPE), ({9: 17}, SHAPE), ({2: 15}, SHAPE), ({4: 15}, SHAPE), ({11: 15}, SHAPE), ({13: 15}, SHAPE),
-             ({9: 32769, 2: 32769, 4: 32769, 11: 32769, 13: 32769}, UNSUP), ({1: FAKE + 1}, ALIGN), ({3: FAKE + 1}, ALIGN),
+             ({9: 16385, 2: 16385, 4: 16385, 11: 16385, 13: 16385}, UNSUP), ({1: FAKE + 1}, ALIGN), ({3: FAKE + 1}, ALIGN),
              ({6: FAKE + 1}, ALIGN), ({10: FAKE + 1}, ALIGN), ({12: FAKE + 1}, ALIGN), ({14: FAKE + 2}, ALIGN),
              ({0: 0, 1: FAKE + 2}, ALIGN))
     # dt, X, ldx, residual, ldr, wdt, w, eps, T, D, fmt, Q, ldq, S, lds, H, ldh, Y, ldy, rstd, stream
@@ -44,7 +44,7 @@ def test_norm(L):
     assert L.rms_norm_bwd_work_bytes(4, 2000, ctypes.byref(need)) == OK and need.value >= 4 * 2000 * 4
     assert L.rms_norm_bwd_work_bytes(1, 2000, ctypes.byref(need)) == OK and need.value == 0
     assert L.rms_norm_bwd_work_bytes(0, 16, ctypes.byref(need)) == SHAPE
-    assert L.rms_norm_bwd_work_bytes(4, 32769, ctypes.byref(need)) == UNSUP
+    assert L.rms_norm_bwd_work_bytes(4, 16385, ctypes.byref(need)) == UNSUP
     assert L.rms_norm_bwd_work_bytes(4, 16, None) == NULL
     good = [1, FAKE, 2000, FAKE, 2000, 0, FAKE, FAKE, FAKE, 2000, 4, 2000, FAKE, 2000, FAKE, FAKE, 1 << 20, None]
     _refuses(L.rms_norm_bwd, good, *[({i: None}, NULL) for i in (1, 3, 6, 7, 12, 14, 15)], ({0: 3}, UNSUP), ({5: 3}, UNSUP),
@@ -53,12 +53,13 @@ def test_norm(L):
 
 
 def test_linear(L):
-    # dt, X, ldx, W, ldw, bdt, bias, act, residual, ldr, M, N, K, out, Y, ldy, pre, ldp, stream
-    good = [1, FAKE, 32, FAKE, 32, 1, FAKE, 1, FAKE, 16, 4, 16, 32, 1, FAKE, 16, FAKE, 16, None]
+    # dt, X, ldx, W, ldw, bdt, bias, act, residual, ldr, M, N, K, out, Y, ldy, pre, ldp, work, work_bytes, stream
+    good = [1, FAKE, 32, FAKE, 32, 1, FAKE, 1, FAKE, 16, 4, 16, 32, 1, FAKE, 16, FAKE, 16, FAKE, 64, None]
     _refuses(L.linear_fwd, good, *[({i: None}, NULL) for i in (1, 3, 14)], ({0: 0}, UNSUP), ({5: 2}, UNSUP), ({7: 4}, UNSUP),
              ({7: -1}, UNSUP), ({13: 2}, UNSUP), *[({i: 0}, SHAPE) for i in (10, 11, 12)], ({10: 1 << 31}, SHAPE),
              *[({i: 31}, SHAPE) for i in (2, 4)], *[({i: 15}, SHAPE) for i in (9, 15, 17)],
-             *[({i: FAKE + 1}, ALIGN) for i in (1, 3, 6, 8, 14, 16)], ({5: 0, 6: FAKE + 2}, ALIGN), ({13: 0, 14: FAKE + 2}, ALIGN))
+             *[({i: FAKE + 1}, ALIGN) for i in (1, 3, 6, 8, 14, 16)], ({5: 0, 6: FAKE + 2}, ALIGN), ({13: 0, 14: FAKE + 2}, ALIGN),
+             ({18: FAKE + 8}, ALIGN))
     # dt, dY, lddy, pre, ldp, act, M, N, dZ, lddz, db, work, work_bytes, stream
     good = [1, FAKE, 16, FAKE, 16, 2, 4000, 16, FAKE, 16, FAKE, FAKE, 1 << 20, None]
     _refuses(L.linear_bwd_act, good, ({1: None}, NULL), ({3: None}, NULL), ({8: None, 10: None}, NULL), ({11: None}, NULL),
@@ -70,16 +71,23 @@ def test_linear(L):
     assert L.linear_bwd_act_work_bytes(1, 16, ctypes.byref(need)) == OK and need.value == 0
     assert L.linear_bwd_act_work_bytes(1, 0, ctypes.byref(need)) == SHAPE
     assert L.linear_bwd_act_work_bytes(1, 1, None) == NULL
-    # dt, dZ, lddz, W, ldw, pre, ldp, act, M, N, K, out, dX, lddx, stream
-    good = [1, FAKE, 16, FAKE, 32, FAKE, 32, 1, 4, 16, 32, 1, FAKE, 32, None]
+    # dt, dZ, lddz, W, ldw, pre, ldp, act, M, N, K, out, dX, lddx, work, work_bytes, stream
+    good = [1, FAKE, 16, FAKE, 32, FAKE, 32, 1, 4, 16, 32, 1, FAKE, 32, None, 0, None]
     _refuses(L.linear_bwd_x, good, *[({i: None}, NULL) for i in (1, 3, 5, 12)], ({0: 0}, UNSUP), ({7: 4}, UNSUP), ({11: 2}, UNSUP),
              ({2: 15}, SHAPE), ({4: 31}, SHAPE), ({6: 31}, SHAPE), ({13: 31}, SHAPE), *[({i: 0}, SHAPE) for i in (8, 9, 10)],
-             *[({i: FAKE + 1}, ALIGN) for i in (1, 3, 5, 12)])
-    # dt, dZ, lddz, X, ldx, M, N, K, accumulate, out, dW, lddw, stream
-    good = [1, FAKE, 16, FAKE, 32, 4, 16, 32, 0, 0, FAKE, 32, None]
+             *[({i: FAKE + 1}, ALIGN) for i in (1, 3, 5, 12)], ({14: FAKE + 8}, ALIGN))
+    # dt, dZ, lddz, X, ldx, M, N, K, accumulate, out, dW, lddw, work, work_bytes, stream
+    good = [1, FAKE, 16, FAKE, 32, 4, 16, 32, 0, 0, FAKE, 32, None, 0, None]
     _refuses(L.linear_bwd_w, good, *[({i: None}, NULL) for i in (1, 3, 10)], ({0: 0}, UNSUP), ({9: 2}, UNSUP), ({8: 1, 9: 1}, UNSUP),
              ({2: 15}, SHAPE), ({4: 31}, SHAPE), ({11: 31}, SHAPE), *[({i: 0}, SHAPE) for i in (5, 6, 7)],
-             ({1: FAKE + 1}, ALIGN), ({3: FAKE + 1}, ALIGN), ({10: FAKE + 2}, ALIGN))
+             ({1: FAKE + 1}, ALIGN), ({3: FAKE + 1}, ALIGN), ({10: FAKE + 2}, ALIGN), ({12: FAKE + 8}, ALIGN))
+    # which, M, N, K, bytes: parts where tiles are few and the reduction long
+    need = ctypes.c_int64()
+    for which, sizes, some in ((0, (512, 2048, 8192), True), (0, (1, 2048, 8192), False), (0, (8192, 16384, 4096), False),
+                               (1, (32, 8192, 2048), True), (2, (8192, 256, 256), True), (2, (64, 4096, 4096), False)):
+        assert L.linear_work_bytes(which, *sizes, ctypes.byref(need)) == OK and (need.value > 0) == some, (which, sizes)
+    assert L.linear_work_bytes(3, 1, 1, 1, ctypes.byref(need)) == UNSUP
+    assert L.linear_work_bytes(0, 0, 1, 1, ctypes.byref(need)) == SHAPE and L.linear_work_bytes(0, 1, 1, 1, None) == NULL
 
 
 def _lists(ptrs, counts, dts):
@@ -89,16 +97,18 @@ def _lists(ptrs, counts, dts):
 
 def test_grads(L):
     need = ctypes.c_int64()
-    assert L.grad_work_bytes(2, (ctypes.c_int64 * 2)(16384, 16385), ctypes.byref(need)) == OK and need.value == 3 * 8
+    assert L.grad_work_bytes(2, (ctypes.c_int64 * 2)(16384, 16385), ctypes.byref(need)) == OK and need.value == 0
+    assert L.grad_work_bytes(2, (ctypes.c_int64 * 2)(65536, 1), ctypes.byref(need)) == OK and need.value == 5 * 8
+    assert L.grad_work_bytes(200, (ctypes.c_int64 * 200)(*[1] * 200), ctypes.byref(need)) == OK and need.value == 200 * 8
     assert L.grad_work_bytes(2, (ctypes.c_int64 * 2)(0, 0), ctypes.byref(need)) == OK and need.value == 0
     assert L.grad_work_bytes(1, (ctypes.c_int64 * 1)(1 << 40), ctypes.byref(need)) == OK and need.value == 1024 * 8
     assert L.grad_work_bytes(1, (ctypes.c_int64 * 1)(-1), ctypes.byref(need)) == SHAPE
     assert L.grad_work_bytes(0, (ctypes.c_int64 * 1)(1), ctypes.byref(need)) == SHAPE
     assert L.grad_work_bytes(1, None, ctypes.byref(need)) == NULL
     W = 1 << 30
-    dt, ptr, cnt = _lists([FAKE, FAKE + 4096], [100, 7], [0, 1])
+    dt, ptr, cnt = _lists([FAKE, FAKE + 400000], [70000, 7], [0, 1])
     good = [2, dt, ptr, cnt, W, W + 4096, 1 << 16, None]      # n, dt, grads, counts, norm, work, work_bytes, stream
-    _refuses(L.grad_norm, good, ({0: 0}, SHAPE), ({0: 65537}, SHAPE), *[({i: None}, NULL) for i in (1, 2, 3, 4, 5)], ({6: 15}, SHAPE),
+    _refuses(L.grad_norm, good, ({0: 0}, SHAPE), ({0: 65537}, SHAPE), *[({i: None}, NULL) for i in (1, 2, 3, 4, 5)], ({6: 39}, SHAPE),
              ({4: W + 2}, ALIGN), ({5: W + 4100}, ALIGN), ({1: _lists([1, 1], [1, 1], [0, 2])[0]}, UNSUP),
              ({2: _lists([FAKE, 0], [1, 1], [0, 0])[1]}, NULL), ({2: _lists([FAKE + 2, FAKE], [1, 1], [0, 0])[1]}, ALIGN),
              ({3: _lists([1, 1], [1, -1], [0, 0])[2]}, SHAPE))
@@ -129,10 +139,12 @@ class Library:
 @pytest.fixture
 def no_device(monkeypatch):
     monkeypatch.setattr(nm, "_here", lambda *ts: None)
+    monkeypatch.setattr(nm, "_here_all", lambda ts: None)
     monkeypatch.setattr(nm, "_stream", lambda: None)
     monkeypatch.setattr(nm, "lib", Library)
     monkeypatch.setattr(nm, "_norm_work_bytes", lambda T, D: 0)
     monkeypatch.setattr(nm, "_act_work_bytes", lambda M, N: 0)
+    monkeypatch.setattr(nm, "_linear_work_bytes", lambda call, M, N, K: 0)
 
 
 def _b(*shape):

@@ -4,6 +4,7 @@ Tolerances, from the arithmetic (U = 2^-24, half a step of fp32; half a step of 
 2^-4 and of e5m2 2^-3, and of their subnormals 2^-10 and 2^-17):
   norm      a row's squares are added in chains of at most 32, then over 6 + 15 steps: the sum is off by at most
             (32 + 21 + 3) U of itself, 1 / sqrt by half of that and three roundings, y by three more: 40 U of |y|.
+            Beside an 8-bit result the squares are added in 64 bits and the products keep their remainders: 2 U and 4 U.
             Its gradient's mean is off by 60 U of the mean of |g xh|; dw adds a row's terms in chains of
             T / 512 + 1, over 4 waves and at most 512 groups (8 + 4 + 16 steps).
   linear    a product of bf16 values is exact in fp32, and each of the K additions rounds or cuts once, at most
@@ -82,7 +83,7 @@ def rows(rng, T, D):
 
 # ---- norm ---------------------------------------------------------------------------------------
 NORM = [(1, 1), (1, 4096), (2, 7), (5, 8), (3, 127), (9, 128), (7, 129), (4, 511), (6, 512), (5, 1000), (3, 1111),
-        (2, 2048), (11, 2050), (3, 4099), (2, 8192), (2, 8200), (1, 16384), (2, 16391), (1, 32768), (600, 264), (67, 1024)]
+        (2, 2048), (11, 2050), (3, 4099), (2, 8192), (2, 8200), (1, 16384), (2, 16383), (600, 264), (67, 1024)]
 
 
 @pytest.mark.parametrize("T,D", NORM)
@@ -117,8 +118,8 @@ def test_norm(T, D, dtype, wdtype, res, pad, off):
         assert (got[:, D:] == 0).all() and got.shape == (T, kp)
         step = np.repeat(gs.T, 128, 1)[:, :D]
         rel, sub = (2.0 ** -4, 2.0 ** -10) if fmt == "e4m3" else (2.0 ** -3, 2.0 ** -17)
-        assert (np.abs(got[:, :D] - y) <= (rel + 60 * U) * np.abs(y) + sub * step).all()
-        assert torch.equal(r8, gr)
+        assert (np.abs(got[:, :D] - y) <= (rel + 4 * U) * np.abs(y) + sub * step).all()
+        close(r8, rstd, 2 * U * rstd, "rstd beside 8 bits")    # squares in 64 bits, one rounding
     # the gradients, from what the forward stored
     DY, dy = dev(rng.normal(size=(T, D)) * 0.02, dtype, pad, off)
     DH, dh = dev(rng.normal(size=(T, D)) * 0.02, dtype, pad + 1, off) if res else (None, None)
@@ -136,9 +137,9 @@ def test_norm(T, D, dtype, wdtype, res, pad, off):
 
 def test_norm_in_place_and_repeats():
     rng = np.random.default_rng(3)
-    X, _ = dev(rows(rng, 33, 1032))
-    R, _ = dev(rows(rng, 33, 1032))
-    W, _ = dev(1 + 0.1 * rng.normal(size=1032))
+    X, xv = dev(rows(rng, 33, 1032))
+    R, rv = dev(rows(rng, 33, 1032))
+    W, wv = dev(1 + 0.1 * rng.normal(size=1032))
     y, h, rstd = nm.rms_norm(X, W, residual=R)
     x2, r2 = X.clone(), R.clone()
     y2, h2, rstd2 = nm.rms_norm(x2, W, residual=r2, H=r2, Y=x2)
@@ -147,7 +148,9 @@ def test_norm_in_place_and_repeats():
     q, s, h3, _ = nm.rms_norm_fp8(X, W, residual=R, H=R.clone())
     y3 = torch.empty_like(X)
     q4, s4, _, _ = nm.rms_norm_fp8(X, W, residual=R, Y=y3)
-    assert torch.equal(y3, y) and torch.equal(h3, h) and torch.equal(q.view(torch.uint8), q4.view(torch.uint8))
+    assert torch.equal(h3, h) and torch.equal(q.view(torch.uint8), q4.view(torch.uint8))
+    want = O.rms_norm(xv, wv, 1e-5, rv)[0]
+    close(y3, want, 4 * U * np.abs(want) + half(want, "bf16") * 1.01, "y beside 8 bits")
     DY, _ = dev(rng.normal(size=(33, 1032)))
     DH, _ = dev(rng.normal(size=(33, 1032)))
     dx, dw = nm.rms_norm_bwd(DY, h, W, rstd, dH=DH)
@@ -487,7 +490,7 @@ def test_binding_refuses():
     with pytest.raises(nm.NmError):
         nm.rms_norm(x, w, eps=0.0)
     with pytest.raises(nm.NmError):
-        nm.rms_norm(torch.zeros(1, 32769, device="cuda"), torch.ones(32769, device="cuda"))
+        nm.rms_norm(torch.zeros(1, 16385, device="cuda"), torch.ones(16385, device="cuda"))
     with pytest.raises(nm.NmError):
         nm.linear_fwd(x.float(), x.float())
     t = torch.ones(8, device="cuda")

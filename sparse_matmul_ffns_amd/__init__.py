@@ -62,3 +62,4 @@ from .nmsparse import (  # noqa: F401
     transpose,
 )
 from .moe import ExpertFFN  # noqa: E402,F401
+from .dense import DenseFFN  # noqa: E402,F401

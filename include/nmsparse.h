@@ -809,8 +809,9 @@ nm_status rms_norm_bwd_work_bytes(int64_t T, int64_t D, int64_t* bytes);
  *   X [M][ldx], W [N][ldw], residual [M][ldr] (NULL: none) bf16; bias [N] dtype bdt (NULL: none)
  *   Y [M][ldy] bf16 or fp32 (out); pre [M][ldp] bf16: z, what the backward pass reads (NULL: not stored)
  * Sums, z and the activation are fp32; Y and pre are rounded once each.  bf16 only (NM_ERR_UNSUPPORTED).  Y may be
- * the residual (bf16).  The tiled kernels run when K, ldx and ldw are multiples of 8 and X and W are
- * 16-byte aligned; other calls take a slower general kernel.  work: see linear_work_bytes.
+ * the residual (bf16).  The tiled kernels load X and W as they are when K, ldx and ldw
+ * are multiples of 8 and X and W 16-byte aligned; else by way of copies in `work` (linear_work_bytes), and without
+ * that a slower general kernel runs.
  */
 nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
                      const void* bias, nm_act act, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K,
@@ -840,8 +841,8 @@ nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes);
  *   dZ [M][lddz], W [N][ldw] bf16; pre [M][ldp] bf16, the pre-activations X came from (NULL with NM_ACT_NONE)
  *   dX [M][lddx] bf16 or fp32 (out); it may be pre (bf16).
  * With ReLU, X itself gives the same derivative as its pre-activations.  Sums are fp32, the result is rounded once.
- * bf16 only.  The tiled kernels run when N, K and the leading dimensions of dZ and W are multiples
- * of 8 and dZ and W are 16-byte aligned.
+ * bf16 only.  The tiled kernels load dZ and W as they are when N, K and their leading dimensions are multiples of 8
+ * and both 16-byte aligned; work as for linear_fwd.
  */
 nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W, int64_t ldw, const void* pre,
                        int64_t ldp, nm_act act, int64_t M, int64_t N, int64_t K, nm_dtype out, void* dX, int64_t lddx,
@@ -851,8 +852,8 @@ nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W,
  * linear_bwd_w -- the gradient of linear_fwd's weight:
  *   dW[n][k] = sum over m of dZ[m][n] X[m][k]      (accumulate: added to dW)
  *   dZ [M][lddz], X [M][ldx] bf16; dW [N][lddw] fp32 or bf16 (out; accumulate needs fp32, NM_ERR_UNSUPPORTED)
- * Sums are fp32.  bf16 operands only.  The tiled kernels run when N, K and the leading dimensions of dZ and X
- * are multiples of 8 and dZ and X are 16-byte aligned.
+ * Sums are fp32.  bf16 operands only.  The tiled kernels load dZ and X as they are when N, K and their leading dimensions
+ * are multiples of 8 and both 16-byte aligned; work as for linear_fwd.
  */
 nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
                        int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, void* work, int64_t work_bytes,
@@ -860,12 +861,13 @@ nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X,
 
 /*
  * linear_work_bytes -- host only: the work memory that linear_fwd, linear_bwd_x or linear_bwd_w uses for these sizes
- * (*bytes; 0 for most).  Where C has too few tiles for the GPU, the reduction is cut into parts whose fp32 sums go
- * through it, and a second launch adds them in their order.  `work` is device memory, 16-byte aligned
- * (NM_ERR_ALIGN); with less of it, or NULL, the reduction is not cut and the call is slower.
+ * (*bytes; 0 for most), `aligned` nonzero where both operands have 16-byte aligned rows.  Where the result has too few
+ * tiles for the GPU, the reduction is cut into parts whose fp32 sums go through it, and a further launch adds them in their
+ * order; operands whose rows the tiled kernels cannot load are copied to it first.  `work` is device memory, 16-byte
+ * aligned (NM_ERR_ALIGN); with less of it, or NULL, the call does without and is slower.
  */
 typedef enum { NM_LINEAR_FWD = 0, NM_LINEAR_BWD_X = 1, NM_LINEAR_BWD_W = 2 } nm_linear;
-nm_status linear_work_bytes(nm_linear call, int64_t M, int64_t N, int64_t K, int64_t* bytes);
+nm_status linear_work_bytes(nm_linear call, int64_t M, int64_t N, int64_t K, int aligned, int64_t* bytes);
 
 /*
  * grad_norm -- the norm of n tensors together: norm = sqrt(sum over all elements of g^2), one fp32 value.

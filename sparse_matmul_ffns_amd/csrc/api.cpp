@@ -643,8 +643,8 @@ nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int
     return NM_ERR_ALIGN;
   const nms::Linear g{(const uint16_t*)X, ldx, (const uint16_t*)W, ldw, 0, 0, M, N, K, Y, ldy, out == NM_BF16,
                       nms::EPI_FWD, bias, bdt == NM_BF16, act, (const uint16_t*)residual, ldr, (uint16_t*)pre, ldp,
-                      nullptr, 0, 0};
-  return hip_status(nms::launch_linear(g, (float*)work, work ? work_bytes : 0, hs(stream)));
+                      nullptr, 0, 0, 0, 0, 0, 0};
+  return hip_status(nms::launch_linear(g, work, work ? work_bytes : 0, hs(stream)));
 }
 
 nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes) {
@@ -682,8 +682,8 @@ nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W,
   // rows of dZ times columns of W: the product's columns are W's, its reduction runs over W's rows
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)W, ldw, 0, 1, M, K, N, dX, lddx, out == NM_BF16,
                       act == NM_ACT_NONE ? nms::EPI_PLAIN : nms::EPI_GATE, nullptr, 0, act, nullptr, 0, nullptr, 0,
-                      (const uint16_t*)pre, ldp, 0};
-  return hip_status(nms::launch_linear(g, (float*)work, work ? work_bytes : 0, hs(stream)));
+                      (const uint16_t*)pre, ldp, 0, 0, 0, 0, 0};
+  return hip_status(nms::launch_linear(g, work, work ? work_bytes : 0, hs(stream)));
 }
 
 nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
@@ -694,17 +694,17 @@ nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X,
   if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldx < K || lddw < K) return NM_ERR_SHAPE;
   if (!aligned(dZ, 2) || !aligned(X, 2) || !aligned(dW, esize(out)) || !aligned(work, 16)) return NM_ERR_ALIGN;
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)X, ldx, 1, 1, N, K, M, dW, lddw, out == NM_BF16,
-                      accumulate ? nms::EPI_ADD : nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0, 0};
-  return hip_status(nms::launch_linear(g, (float*)work, work ? work_bytes : 0, hs(stream)));
+                      accumulate ? nms::EPI_ADD : nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0, 0, 0, 0, 0, 0};
+  return hip_status(nms::launch_linear(g, work, work ? work_bytes : 0, hs(stream)));
 }
 
-nm_status linear_work_bytes(nm_linear call, int64_t M, int64_t N, int64_t K, int64_t* bytes) {
+nm_status linear_work_bytes(nm_linear call, int64_t M, int64_t N, int64_t K, int aligned, int64_t* bytes) {
   if (!bytes) return NM_ERR_NULL;
   if (!rows_ok(M, N) || !rows_ok(K, 1)) return NM_ERR_SHAPE;
   switch (call) {
-    case NM_LINEAR_FWD: *bytes = nms::linear_work_bytes(0, 0, M, N, K); return NM_OK;
-    case NM_LINEAR_BWD_X: *bytes = nms::linear_work_bytes(0, 1, M, K, N); return NM_OK;
-    case NM_LINEAR_BWD_W: *bytes = nms::linear_work_bytes(1, 1, N, K, M); return NM_OK;
+    case NM_LINEAR_FWD: *bytes = nms::linear_work_bytes(0, 0, M, N, K, aligned != 0); return NM_OK;
+    case NM_LINEAR_BWD_X: *bytes = nms::linear_work_bytes(0, 1, M, K, N, aligned != 0); return NM_OK;
+    case NM_LINEAR_BWD_W: *bytes = nms::linear_work_bytes(1, 1, N, K, M, aligned != 0); return NM_OK;
   }
   return NM_ERR_UNSUPPORTED;
 }

@@ -266,16 +266,20 @@ struct Linear {
   const uint16_t* P;        // EPI_GATE: the activation's derivative at P
   int64_t ldp;
   int64_t part_k;           // the reduction's length of a part, where it is cut
+  // what may be read of the operands: A's rows (or columns) and k, and B's; more than M, N and K where a copy is padded
+  int64_t ra, ka, rb, kb;
 };
 // How a product is computed: its kernel and tile, and in how many parts of part_k the reduction is cut.
 struct LinearPlan {
   enum { ROWS = 0, T128 = 1, T256x128 = 2, T256 = 3 };
   int tile, parts;
   int64_t part_k;
+  bool pack;        // copy operands whose rows are not aligned
 };
-int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K);
-// work: fp32, 16-byte aligned; with fewer than linear_work_bytes the reduction is not cut
-hipError_t launch_linear(const Linear& g, float* work, int64_t work_bytes, hipStream_t s);
+// aligned: both operands have 16-byte aligned rows.
+int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool aligned);
+// work: 16-byte aligned; with fewer than linear_work_bytes the general kernel, or an uncut reduction, does without
+hipError_t launch_linear(const Linear& g, void* work, int64_t work_bytes, hipStream_t s);
 struct Grads {
   int64_t n;
   const int* dt;

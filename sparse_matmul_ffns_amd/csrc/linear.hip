@@ -455,9 +455,12 @@ __global__ __launch_bounds__(256, Cfg::PER_CU) void linear_tile_kernel(Linear g)
   if (gridDim.y > 1) {
     // a part of the reduction, whose sums go to a matrix of their own
     const int64_t k0 = (int64_t)blockIdx.y * g.part_k;
+    auto rest = [&](int64_t k) { return k - k0 < g.part_k ? k - k0 : g.part_k; };
     g.A += AT ? k0 * g.lda : k0;
     g.B += BT ? k0 * g.ldb : k0;
-    g.K = g.K - k0 < g.part_k ? g.K - k0 : g.part_k;
+    g.K = rest(g.K);
+    g.ka = rest(g.ka);
+    g.kb = rest(g.kb);
     g.C = (float*)g.C + blockIdx.y * g.M * g.ldc;
   }
   constexpr int FM = Cfg::FM, FN = Cfg::FN, LA = Cfg::LA, LB = Cfg::LB, LOADS = Cfg::LOADS;
@@ -473,8 +476,8 @@ __global__ __launch_bounds__(256, Cfg::PER_CU) void linear_tile_kernel(Linear g)
 
   Operand<AT, Cfg::BM, Cfg::KU, LA> A;
   Operand<BT, Cfg::BN, Cfg::KU, LB> B;
-  A.init(g.A, g.lda, m0, g.M, g.K, wave, lane);
-  B.init(g.B, g.ldb, n0, g.N, g.K, wave, lane);
+  A.init(g.A, g.lda, m0, g.ra, g.ka, wave, lane);
+  B.init(g.B, g.ldb, n0, g.rb, g.kb, wave, lane);
   const uint32_t lds_base = uniform(lds_addr(smem));
   const uint32_t a_first = A.lds0(lds_base, wm, lane), b_first = B.lds0(lds_base + Cfg::NA * Cfg::A_BYTES, wn, lane);
 
@@ -671,7 +674,7 @@ hipError_t run_tile(const Linear& g, int parts, hipStream_t s) {
 // One token (FM 1, FN 1, KS 8, CH 4), weights that are not in a cache: 16384 x 4096 24 us (5.5 TB/s, a large copy's rate),
 // 8192 x 2048 8.7 us; with FN 2 and KS 4 31 and 10.4.
 // ---------------------------------------------------------------------------
-template <int FM, int FN, int KS, int CH>
+template <int FM, int FN, int KS, int CH, bool TAIL>
 __global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
   __shared__ f32x4 part[KS][FM * FN][64];
   const int lane = threadIdx.x & 63;
@@ -696,10 +699,18 @@ __global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
   struct Chunk {
     u32x4 a[CH][FM], b[CH][FN];
   };
-  const int64_t kl = g.K - 8 * lq;   // K is a multiple of eight: a lane's eight k exist or do not
+  const int64_t kl = g.K - 8 * lq;
+  // any alignment: memory takes 16-byte loads at every element; TAIL: a lane's last eight k may not all exist
   auto load16 = [&](const uint16_t* p, bool on, int64_t k) {
     u32x4 v = {0, 0, 0, 0};
-    if (on && k < kl) v = *reinterpret_cast<const u32x4*>(p + k);
+    if (!on || k >= kl) return v;
+    if (!TAIL || k + 8 <= kl) {
+      __builtin_memcpy(&v, p + k, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (k + q < kl) v[q / 2] |= (uint32_t)p[k + q] << (16 * (q & 1));
+    }
     return v;
   };
   auto load = [&](int64_t c, Chunk& x) {
@@ -758,14 +769,14 @@ template <int FM, int FN, int KS, int CH>
 hipError_t run_rows(const Linear& g, hipStream_t s) {
   const int64_t wgs = (g.M + 16 * FM - 1) / (16 * FM) * ((g.N + 16 * FN - 1) / (16 * FN));
   if (!grid_ok(wgs, 64 * KS)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((linear_rows_kernel<FM, FN, KS, CH>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
+  if (g.K % 8) hipLaunchKernelGGL((linear_rows_kernel<FM, FN, KS, CH, true>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
+  else hipLaunchKernelGGL((linear_rows_kernel<FM, FN, KS, CH, false>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
   return hipGetLastError();
 }
-// The tiled kernel's conditions: 16-byte loads that lie inside the operand or outside it, and 31-bit offsets
-// inside a tile.
-bool tile_ok(const Linear& g) {
-  return (uintptr_t)g.A % 16 == 0 && (uintptr_t)g.B % 16 == 0 && g.lda % 8 == 0 && g.ldb % 8 == 0 &&
-         g.lda < (1 << 22) && g.ldb < (1 << 22) && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
+// What the tiled kernel asks of an operand: 16-byte loads that lie inside it or outside, and 31-bit offsets
+// inside a tile.  `line` is its contiguous size.
+bool line_ok(const uint16_t* X, int64_t ld, int64_t line) {
+  return (uintptr_t)X % 16 == 0 && ld % 8 == 0 && ld < (1 << 22) && line % 8 == 0;
 }
 
 using Lin256 = LinCfg<8, 8, 64, 2, 3>;
@@ -802,11 +813,75 @@ hipError_t run_tiles(const Linear& g, const LinearPlan& p, hipStream_t s) {
   return g.epi == EPI_GATE ? run_act<true, EPI_GATE>(g, p, s) : run_sized<false, true, EPI_PLAIN, ACT_NONE>(g, p, s);
 }
 
-hipError_t linear_piece(const Linear& g, const LinearPlan& p, float* work, hipStream_t s) {
-  if (force_generic() || !tile_ok(g)) return run_general(g, s);
+int64_t part_bytes(const LinearPlan& p, int64_t M, int64_t N) {
+  return p.parts > 1 ? p.parts * M * ((N + 3) / 4 * 4) * 4 : 0;
+}
+
+// Copies of operands that the tiled kernel cannot load: X [rows][line] to P [rows][up to a multiple of eight], zeros behind
+// the line.  The first `na` workgroups copy A, the others B.
+struct Pack {
+  const uint16_t* X;
+  int64_t ld, rows, line;
+  uint16_t* P;             // null: nothing to copy
+};
+__global__ __launch_bounds__(256) void linear_pack_kernel(Pack a, Pack b, int64_t na) {
+  const bool second = blockIdx.x >= na;
+  const Pack& p = second ? b : a;
+  const int64_t per = (p.line + 7) / 8, id = ((int64_t)blockIdx.x - (second ? na : 0)) * 256 + threadIdx.x;
+  const int64_t r = id / per, c = id % per * 8;
+  if (r >= p.rows) return;
+  const uint16_t* x = p.X + r * p.ld;
+  u32x4 v = {0, 0, 0, 0};
+  if (c + 8 <= p.line) {
+    __builtin_memcpy(&v, x + c, 16);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (c + q < p.line) v[q / 2] |= (uint32_t)x[c + q] << (16 * (q & 1));
+  }
+  *reinterpret_cast<u32x4*>(p.P + (r * per + c / 8) * 8) = v;
+}
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t pack_bytes(int t, int64_t R, int64_t K) { return t ? K * up8(R) * 2 : R * up8(K) * 2; }
+
+hipError_t run_pack(const Pack& a, const Pack& b, hipStream_t s) {
+  auto wgs = [](const Pack& p) { return p.P ? (p.rows * ((p.line + 7) / 8) + 255) / 256 : 0; };
+  const int64_t na = wgs(a), nb = wgs(b);
+  if (!grid_ok(na + nb, 256)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(linear_pack_kernel, dim3((unsigned)(na + nb)), dim3(256), 0, s, a, b, na);
+  return hipGetLastError();
+}
+
+hipError_t linear_piece(const Linear& g, LinearPlan p, void* work, int64_t work_bytes, hipStream_t s) {
+  if (force_generic()) return run_general(g, s);
   if (p.tile == LinearPlan::ROWS) return g.M > 16 ? run_rows<2, 2, 8, 4>(g, s) : run_rows<1, 1, 8, 4>(g, s);
-  if (p.parts == 1) return run_tiles(g, p, s);
   Linear q = g;
+  q.ra = g.M, q.rb = g.N, q.ka = q.kb = g.K;
+  const bool ca = !line_ok(g.A, g.lda, g.a_t ? g.M : g.K), cb = !line_ok(g.B, g.ldb, g.b_t ? g.N : g.K);
+  if (ca || cb) {
+    const int64_t ba = ca ? pack_bytes(g.a_t, g.M, g.K) : 0, bb = cb ? pack_bytes(g.b_t, g.N, g.K) : 0;
+    if (!p.pack || work_bytes < ba + bb || up8(g.a_t ? g.M : g.K) >= (1 << 22) || up8(g.b_t ? g.N : g.K) >= (1 << 22))
+      return run_general(g, s);
+    Pack a{}, b{};
+    if (ca) {
+      a = Pack{g.A, g.lda, g.a_t ? g.K : g.M, g.a_t ? g.M : g.K, (uint16_t*)work};
+      q.A = a.P;
+      q.lda = up8(a.line);
+      (g.a_t ? q.ra : q.ka) = q.lda;
+    }
+    if (cb) {
+      b = Pack{g.B, g.ldb, g.b_t ? g.K : g.N, g.b_t ? g.N : g.K, (uint16_t*)((char*)work + ba)};
+      q.B = b.P;
+      q.ldb = up8(b.line);
+      (g.b_t ? q.rb : q.kb) = q.ldb;
+    }
+    const hipError_t e = run_pack(a, b, s);
+    if (e != hipSuccess) return e;
+    work = (char*)work + ba + bb;
+    work_bytes -= ba + bb;
+  }
+  if (work_bytes < part_bytes(p, g.M, g.N)) p.parts = 1;
+  if (p.parts == 1) return run_tiles(q, p, s);
   q.epi = EPI_PLAIN;
   q.C = work;
   q.ldc = (g.N + 3) / 4 * 4;
@@ -825,8 +900,6 @@ hipError_t linear_piece(const Linear& g, const LinearPlan& p, float* work, hipSt
   return hipGetLastError();
 }
 
-}  // namespace
-
 // The kernel for a product, by what each is expected to take: `full` rounds of as many workgroups as the GPU holds and
 // a last one, each a fixed time and one per 1024 k that grows with the part x of the GPU that is at work (its
 // power and the memory behind the L2s are shared), and where the reduction is cut the parts' bytes and a launch.  The constants are fits
@@ -841,18 +914,18 @@ constexpr TileCost kTiles[] = {{LinearPlan::T128, 128, 128, 256, 5, 6.1, 2.1},
                                {LinearPlan::T256x128, 256, 128, 256, 7, 9.2, 3.3},
                                {LinearPlan::T256, 256, 256, 256, 10, 15, 6.5}};
 
-static double round_us(const TileCost& t, double k, int64_t workgroups) {
+double round_us(const TileCost& t, double k, int64_t workgroups) {
   // two 128 x 128 tiles fit a CU, and together take as long as one after the other
   if (t.tile == LinearPlan::T128 && workgroups > t.held) return t.fixed + 16.5 * k;
   const double x = (double)workgroups / t.held;
   return t.fixed + (t.alone + t.shared * x * x) * k;
 }
 
-static LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K) {
+LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool aligned) {
   // Few rows: the kernel without LDS, against the best of the tiles in us: 1 x 16384 x 4096 24 and 31, 1 x 2048 x 8192 12 and 16, 16 x
   // 8192 x 2048 11 and 15, 16 x 2048 x 8192 18 and 18; 32 x 8192 x 2048 13 and 15, but 32 x 2048 x 8192 26 and 18
-  if (!a_t && !b_t && (M <= 16 || (M <= 32 && K <= 2048))) return LinearPlan{LinearPlan::ROWS, 1, K};
-  LinearPlan best{LinearPlan::T256, 1, K};
+  if (!a_t && !b_t && (M <= 16 || (M <= 32 && K <= 2048))) return LinearPlan{LinearPlan::ROWS, 1, K, false};
+  LinearPlan best{LinearPlan::T256, 1, K, false};
   double least = 1e30;
   for (const TileCost& t : kTiles) {
     const int64_t tiles = (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn);
@@ -865,21 +938,31 @@ static LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K)
       if (parts > 1) us += 4 + 8e-6 / 6 * (double)(parts * M) * (double)N;
       if (us < least) {
         least = us;
-        best = LinearPlan{t.tile, (int)parts, part_k};
+        best = LinearPlan{t.tile, (int)parts, part_k, false};
       }
     }
   }
+  // Operands that the tiles cannot load are copied first, unless the general kernel is done sooner: 1.7 us per 64 k
+  // and 1536 of its 64 x 64 tiles.  With a copy and without, us: 1000 x 1111 x 777 22 and 27, 4096 x 5001 x 3333
+  // 200 and 649, its gradients 137 and 795, 189 and 1139; 200 x 500 x 300 14 and 11.
+  if (!aligned) {
+    const double general = 4 + 1.7 / 64 * (double)K * (double)(((M + 63) / 64 * ((N + 63) / 64) + 1535) / 1536);
+    best.pack = least + 4 + 4e-6 / 5 * (double)(M * K + N * K) < general;
+  }
   return best;
 }
-static int64_t part_bytes(const LinearPlan& p, int64_t M, int64_t N) {
-  return p.parts > 1 ? p.parts * M * ((N + 3) / 4 * 4) * 4 : 0;
-}
-int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K) {
+
+}  // namespace
+
+int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool aligned) {
   const int64_t m = M < kPieceRows ? M : kPieceRows;
-  return part_bytes(linear_plan(a_t, b_t, m, N, K), m, N);
+  aligned = aligned && (a_t ? M : K) % 8 == 0 && (b_t ? N : K) % 8 == 0;
+  const LinearPlan p = linear_plan(a_t, b_t, m, N, K, aligned);
+  if (p.tile == LinearPlan::ROWS || (!aligned && !p.pack)) return 0;
+  return part_bytes(p, m, N) + (aligned ? 0 : pack_bytes(a_t, m, K) + pack_bytes(b_t, N, K));
 }
 
-hipError_t launch_linear(const Linear& g, float* work, int64_t work_bytes, hipStream_t s) {
+hipError_t launch_linear(const Linear& g, void* work, int64_t work_bytes, hipStream_t s) {
   return in_pieces(g.M, kPieceRows, [&](int64_t m0, int64_t n) {
     Linear p = g;
     p.A += g.a_t ? m0 : m0 * g.lda;
@@ -888,9 +971,8 @@ hipError_t launch_linear(const Linear& g, float* work, int64_t work_bytes, hipSt
     if (g.R) p.R += m0 * g.ldr;
     if (g.Z) p.Z += m0 * g.ldz;
     if (g.P) p.P += m0 * g.ldp;
-    LinearPlan plan = linear_plan(g.a_t, g.b_t, n, g.N, g.K);
-    if (work_bytes < part_bytes(plan, n, g.N)) plan.parts = 1;
-    return linear_piece(p, plan, work, s);
+    const bool aligned = line_ok(p.A, p.lda, p.a_t ? n : p.K) && line_ok(p.B, p.ldb, p.b_t ? p.N : p.K);
+    return linear_piece(p, linear_plan(g.a_t, g.b_t, n, g.N, g.K, aligned), work, work_bytes, s);
   });
 }
 

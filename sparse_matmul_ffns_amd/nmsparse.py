@@ -89,7 +89,7 @@ _SIGNATURES = {
     "linear_bwd_act_work_bytes": [_i64, _i64, ctypes.POINTER(_i64)],
     "linear_bwd_x": [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp],
     "linear_bwd_w": [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp],
-    "linear_work_bytes": [_int, _i64, _i64, _i64, ctypes.POINTER(_i64)],
+    "linear_work_bytes": [_int, _i64, _i64, _i64, _int, ctypes.POINTER(_i64)],
     "grad_norm": [_i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
     "grad_clip": [_i64, _vp, _vp, _vp, _f32, _int, _vp, _vp, _vp, _vp, _i64, _vp],
     "grad_work_bytes": [_i64, _vp, ctypes.POINTER(_i64)],
@@ -1130,10 +1130,15 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, w: torch.Tensor, rstd: torch
 
 
 @functools.lru_cache(maxsize=256)
-def _linear_work_bytes(call: int, M: int, N: int, K: int) -> int:
+def _linear_work_bytes(call: int, M: int, N: int, K: int, aligned: bool) -> int:
     need = _i64()
-    _check(lib().linear_work_bytes(call, M, N, K, ctypes.byref(need)), "linear_work_bytes")
+    _check(lib().linear_work_bytes(call, M, N, K, int(aligned), ctypes.byref(need)), "linear_work_bytes")
     return need.value
+
+
+def _linear_work(work, call: int, M: int, N: int, K: int, A, lda: int, B, ldb: int):
+    aligned = (A.data_ptr() | B.data_ptr()) % 16 == 0 and (lda | ldb) % 8 == 0
+    return _workspace(work, _linear_work_bytes(call, M, N, K, aligned) if isinstance(work, str) else 0, A)
 
 
 def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", residual=None,
@@ -1155,7 +1160,7 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
     if pre is None and return_pre:
         pre = X.new_empty((M, N), dtype=torch.bfloat16)
     ldp = _opt(pre, (M, N), torch.bfloat16, "pre")
-    work, nbytes = _workspace(work, _linear_work_bytes(NM_LINEAR_FWD, M, N, K), X)
+    work, nbytes = _linear_work(work, NM_LINEAR_FWD, M, N, K, X, ldx, W, ldw)
     _check(lib().linear_fwd(_dt(X), _p(X), ldx, _p(W), ldw, NM_BF16 if bias is None else _dt(bias), _p(bias), _act(act),
                             _p(residual), ldr, M, N, K, _dt(out), _p(out), ldy, _p(pre), ldp, _p(work), nbytes, _stream()),
            "linear_fwd")
@@ -1205,7 +1210,7 @@ def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
     if out is None:
         out = dZ.new_empty((M, K), dtype=out_dtype)
     lddx = _matrix(out, (M, K), None, "out")
-    work, nbytes = _workspace(work, _linear_work_bytes(NM_LINEAR_BWD_X, M, N, K), dZ)
+    work, nbytes = _linear_work(work, NM_LINEAR_BWD_X, M, N, K, dZ, lddz, W, ldw)
     _check(lib().linear_bwd_x(_dt(dZ), _p(dZ), lddz, _p(W), ldw, _p(pre), ldp, _act(act), M, N, K, _dt(out), _p(out),
                               lddx, _p(work), nbytes, _stream()), "linear_bwd_x")
     return out
@@ -1224,7 +1229,7 @@ def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = tor
             raise ValueError("accumulate needs out")
         out = dZ.new_empty((N, K), dtype=out_dtype)
     lddw = _matrix(out, (N, K), None, "out")
-    work, nbytes = _workspace(work, _linear_work_bytes(NM_LINEAR_BWD_W, M, N, K), dZ)
+    work, nbytes = _linear_work(work, NM_LINEAR_BWD_W, M, N, K, dZ, lddz, X, ldx)
     _check(lib().linear_bwd_w(_dt(dZ), _p(dZ), lddz, _p(X), ldx, M, N, K, int(bool(accumulate)), _dt(out), _p(out),
                               lddw, _p(work), nbytes, _stream()), "linear_bwd_w")
     return out

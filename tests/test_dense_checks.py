@@ -81,13 +81,17 @@ def test_linear(L):
     _refuses(L.linear_bwd_w, good, *[({i: None}, NULL) for i in (1, 3, 10)], ({0: 0}, UNSUP), ({9: 2}, UNSUP), ({8: 1, 9: 1}, UNSUP),
              ({2: 15}, SHAPE), ({4: 31}, SHAPE), ({11: 31}, SHAPE), *[({i: 0}, SHAPE) for i in (5, 6, 7)],
              ({1: FAKE + 1}, ALIGN), ({3: FAKE + 1}, ALIGN), ({10: FAKE + 2}, ALIGN), ({12: FAKE + 8}, ALIGN))
-    # which, M, N, K, bytes: parts where tiles are few and the reduction long
+    # which, M, N, K, aligned, bytes: parts where tiles are few and the reduction long, copies where rows are not aligned
     need = ctypes.c_int64()
-    for which, sizes, some in ((0, (512, 2048, 8192), True), (0, (1, 2048, 8192), False), (0, (8192, 16384, 4096), False),
-                               (1, (32, 8192, 2048), True), (2, (8192, 256, 256), True), (2, (64, 4096, 4096), False)):
-        assert L.linear_work_bytes(which, *sizes, ctypes.byref(need)) == OK and (need.value > 0) == some, (which, sizes)
-    assert L.linear_work_bytes(3, 1, 1, 1, ctypes.byref(need)) == UNSUP
-    assert L.linear_work_bytes(0, 0, 1, 1, ctypes.byref(need)) == SHAPE and L.linear_work_bytes(0, 1, 1, 1, None) == NULL
+    for which, sizes, al, some in ((0, (512, 2048, 8192), 1, True), (0, (1, 2048, 8192), 1, False), (0, (8192, 16384, 4096), 1, False),
+                                   (1, (32, 8192, 2048), 1, True), (2, (8192, 256, 256), 1, True), (2, (64, 4096, 4096), 1, False),
+                                   (0, (8192, 16384, 4096), 0, True), (0, (1, 2048, 8192), 0, False), (0, (8192, 16384, 4095), 1, True),
+                                   (1, (4096, 4096, 4095), 1, True), (2, (4095, 4096, 4096), 1, False), (0, (8, 8, 8), 0, False)):
+        assert L.linear_work_bytes(which, *sizes, al, ctypes.byref(need)) == OK and (need.value > 0) == some, (which, sizes)
+    assert L.linear_work_bytes(0, 4096, 4104, 4095, 1, ctypes.byref(need)) == OK
+    assert need.value == (4096 + 4104) * 4096 * 2
+    assert L.linear_work_bytes(3, 1, 1, 1, 1, ctypes.byref(need)) == UNSUP
+    assert L.linear_work_bytes(0, 0, 1, 1, 1, ctypes.byref(need)) == SHAPE and L.linear_work_bytes(0, 1, 1, 1, 1, None) == NULL
 
 
 def _lists(ptrs, counts, dts):
@@ -144,7 +148,7 @@ def no_device(monkeypatch):
     monkeypatch.setattr(nm, "lib", Library)
     monkeypatch.setattr(nm, "_norm_work_bytes", lambda T, D: 0)
     monkeypatch.setattr(nm, "_act_work_bytes", lambda M, N: 0)
-    monkeypatch.setattr(nm, "_linear_work_bytes", lambda call, M, N, K: 0)
+    monkeypatch.setattr(nm, "_linear_work_bytes", lambda call, M, N, K, aligned: 0)
 
 
 def _b(*shape):

@@ -23,6 +23,11 @@ def asm(tmp_path_factory):
     return {s: cg._compile(tmp_path_factory.mktemp("dense"), s) for s in SOURCES}
 
 
+# by tile: the loads of two steps, and what may be in flight at a barrier of the loop: with buffers of 64 k the next step's B
+# and that of the one behind it, or its A and B; with a ring of five of 32 k four steps' loads, or three's
+WAITS = {"LinCfgILi8ELi8E": (32, (0, 8, 16)), "LinCfgILi8ELi4E": (24, (0, 4, 12)), "LinCfgILi4ELi4E": (8, (0, 12, 16))}
+
+
 def _tiled(text):
     out = {n: b for n, b in cg._kernels(text, "_ZN3nms").items() if "linear_tile_kernel" in n}
     assert len(out) >= 18
@@ -58,7 +63,7 @@ def test_loads_are_waited_for(asm):
     loads; behind the last of them (the epilogue) for all loads."""
     for name, lines in _tiled(asm["linear.hip"]).items():
         code = _code(lines)
-        loads = 8 if "LinCfgILi8ELi8E" in name else 4
+        loads, allowed = next(v for k, v in WAITS.items() if k in name)
         bars = [i for i, c in enumerate(code) if c == "s_barrier"]
         assert len(bars) >= 4, name
         last = 0
@@ -66,10 +71,10 @@ def test_loads_are_waited_for(asm):
             assert "lgkmcnt(0)" in code[i - 1], (name, code[i - 1])
             waits = [re.search(r"vmcnt\((\d+)\)", c) for c in code[max(0, i - 60):i] if c.startswith("s_waitcnt")]
             counts = [int(w.group(1)) for w in waits if w]
-            assert counts and min(counts) in (0, 3 * loads, 4 * loads), (name, counts)
+            assert counts and min(counts) in allowed, (name, counts)
             last = i if min(counts) == 0 else last
         dma = [i for i, c in enumerate(code) if c.startswith("buffer_load_") and re.search(r"\blds\b", c)]
-        assert len(dma) >= 6 * loads, name
+        assert len(dma) >= loads, name
         ends = _in_flight_at_the_end(lines)
         assert not ends, (name, ends)
 

@@ -825,7 +825,7 @@ nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int
  *   db fp32 [N] (NULL: not wanted; not both).  dZ may be dY or pre.
  *   work  device memory, 4-byte aligned, of linear_bwd_act_work_bytes bytes (NULL when that is 0 or db is NULL;
  *         NM_ERR_SHAPE when work_bytes is less)
- * The derivative of ReLU at 0 is 0.  db adds the fp32 products before dZ's rounding, in an order that depends on M and
+ * The derivative of ReLU at 0 is 0; where it is 0 the result is 0 whatever dY holds.  db adds the fp32 products before dZ's rounding, in an order that depends on M and
  * N alone.  bf16 only (NM_ERR_UNSUPPORTED).
  */
 nm_status linear_bwd_act(nm_dtype dt, const void* dY, int64_t lddy, const void* pre, int64_t ldp, nm_act act, int64_t M,
@@ -883,7 +883,8 @@ nm_status grad_norm(int64_t n, const nm_dtype* dt, const void* const* grads, con
 
 /*
  * grad_clip -- n tensors scaled so that their norm is at most max_norm:
- *   f = max_norm / norm where max_norm < norm < infinity, else 1;  out = f * grad, rounded once
+ *   f = max_norm / norm where max_norm < norm < infinity, else 1;  out = f * grad (f and the product fp32, then to
+ *   out's type)
  *   have_norm 0: *norm is grad_norm's result, written by this call (work as for grad_norm)
  *   have_norm 1: *norm is the caller's (the norm of gradients that lie on several GPUs, say) and is read; work may be
  *                NULL

@@ -27,24 +27,29 @@ __device__ inline float act_fwd(float z) {
   return z;
 }
 
-// The derivative.  Beyond +-100 both smooth ones' are 0 or 1 in fp32 (the exponential there is 0 or
+// The derivatives of the smooth ones.  Beyond +-100 they are 0 or 1 in fp32 (the exponential there is 0 or
 // infinite); z is held there, so that no intermediate is 0 times infinity; a NaN stays one.
 template <int ACT>
 __device__ inline float act_bwd(float z) {
-  if constexpr (ACT == ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
-    const float c = fminf(fmaxf(z, -100.f), 100.f);
-    float d;
-    if constexpr (ACT == ACT_SILU) {
-      const float s = sigmoid(c);
-      d = s * __builtin_fmaf(c, 1.f - s, 1.f);
-    } else {
-      const float cc = c * c, s = sigmoid(kGelu2 * c * __builtin_fmaf(kGeluCube, cc, 1.f));
-      d = __builtin_fmaf(c * s * (1.f - s), kGelu2 * __builtin_fmaf(3.f * kGeluCube, cc, 1.f), s);
-    }
-    return z != z ? z : d;
+  static_assert(ACT == ACT_GELU_TANH || ACT == ACT_SILU, "");
+  const float c = fminf(fmaxf(z, -100.f), 100.f);
+  float d;
+  if constexpr (ACT == ACT_SILU) {
+    const float s = sigmoid(c);
+    d = s * __builtin_fmaf(c, 1.f - s, 1.f);
+  } else {
+    const float cc = c * c, s = sigmoid(kGelu2 * c * __builtin_fmaf(kGeluCube, cc, 1.f));
+    d = __builtin_fmaf(c * s * (1.f - s), kGelu2 * __builtin_fmaf(3.f * kGeluCube, cc, 1.f), s);
   }
-  return 1.f;
+  return z != z ? z : d;
+}
+
+// v times the derivative; ReLU passes v or 0, so what is not finite in a masked place goes no further.
+template <int ACT>
+__device__ inline float act_gate(float v, float z) {
+  if constexpr (ACT == ACT_NONE) return v;
+  else if constexpr (ACT == ACT_RELU) return z > 0.f ? v : 0.f;
+  else return v * act_bwd<ACT>(z);
 }
 
 // f with the activation as a constant

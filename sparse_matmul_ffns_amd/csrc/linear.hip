@@ -71,10 +71,10 @@ __device__ inline f32x4 act4(int act, f32x4 v) {
   });
   return v;
 }
-__device__ inline f32x4 dact4(int act, f32x4 v) {
+__device__ inline f32x4 gate4(int act, f32x4 v, const f32x4& z) {
   with_act(act, [&](auto a) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = act_bwd<decltype(a)::value>(v[q]);
+    for (int q = 0; q < 4; ++q) v[q] = act_gate<decltype(a)::value>(v[q], z[q]);
   });
   return v;
 }
@@ -87,7 +87,7 @@ __device__ inline f32x4 epilogue4(const Linear& g, int64_t m, int64_t n, f32x4 v
     v = act4(g.act, v);
     if (g.R) v += load4(g.R + m * g.ldr, n, g.N);
   } else if (g.epi == EPI_GATE) {
-    v *= dact4(g.act, load4(g.P + m * g.ldp, n, g.N));
+    v = gate4(g.act, v, load4(g.P + m * g.ldp, n, g.N));
   } else if (g.epi == EPI_ADD) {
     v += load4((const float*)g.C + m * g.ldc, n, g.N);
   }
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void linear_general_kernel(Linear g) {
 
 hipError_t run_general(const Linear& g, hipStream_t s) {
   const int64_t ntm = (g.M + 63) / 64, ntn = (g.N + 63) / 64;
-  if (ntn > 65535 || !grid_ok(ntm, 256)) return hipErrorInvalidConfiguration;
+  if (!grid_ok(ntm, 256)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(linear_general_kernel, dim3((unsigned)ntm, (unsigned)ntn), dim3(256), 0, s, g);
   return hipGetLastError();
 }
@@ -393,7 +393,7 @@ __device__ __forceinline__ void epilogue_whole(const Linear& g, const f32x4 (&ac
         }
         if constexpr (EPI == EPI_GATE) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] *= act_bwd<ACT>(w[q]);
+          for (int q = 0; q < 4; ++q) v[q] = act_gate<ACT>(v[q], w[q]);
         }
         if constexpr (EPI == EPI_ADD) v += w;
         if constexpr (sizeof(T) == 2)
@@ -947,15 +947,20 @@ LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool a
   // 200 and 649, its gradients 137 and 795, 189 and 1139; 200 x 500 x 300 14 and 11.
   if (!aligned) {
     const double general = 4 + 1.7 / 64 * (double)K * (double)(((M + 63) / 64 * ((N + 63) / 64) + 1535) / 1536);
-    best.pack = least + 4 + 4e-6 / 5 * (double)(M * K + N * K) < general;
+    const double elements = ((double)M + (double)N) * (double)K;   // the copies: 2 bytes each, in one launch
+    best.pack = elements < 1LL << 35 && least + 4 + 4e-6 / 5 * elements < general;
   }
   return best;
 }
 
 }  // namespace
 
+// Columns of a launch, at most: below every kernel's limit of workgroups.
+constexpr int64_t kPieceCols = int64_t(1) << 21;
+
 int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool aligned) {
   const int64_t m = M < kPieceRows ? M : kPieceRows;
+  N = N < kPieceCols ? N : kPieceCols;
   aligned = aligned && (a_t ? M : K) % 8 == 0 && (b_t ? N : K) % 8 == 0;
   const LinearPlan p = linear_plan(a_t, b_t, m, N, K, aligned);
   if (p.tile == LinearPlan::ROWS || (!aligned && !p.pack)) return 0;
@@ -963,16 +968,22 @@ int64_t linear_work_bytes(int a_t, int b_t, int64_t M, int64_t N, int64_t K, boo
 }
 
 hipError_t launch_linear(const Linear& g, void* work, int64_t work_bytes, hipStream_t s) {
-  return in_pieces(g.M, kPieceRows, [&](int64_t m0, int64_t n) {
+  auto piece = [&](int64_t m0, int64_t m, int64_t n0, int64_t n) {
     Linear p = g;
     p.A += g.a_t ? m0 : m0 * g.lda;
-    p.M = n;
-    p.C = (uint8_t*)g.C + m0 * g.ldc * (g.bf16_out ? 2 : 4);
-    if (g.R) p.R += m0 * g.ldr;
-    if (g.Z) p.Z += m0 * g.ldz;
-    if (g.P) p.P += m0 * g.ldp;
-    const bool aligned = line_ok(p.A, p.lda, p.a_t ? n : p.K) && line_ok(p.B, p.ldb, p.b_t ? p.N : p.K);
-    return linear_piece(p, linear_plan(g.a_t, g.b_t, n, g.N, g.K, aligned), work, work_bytes, s);
+    p.B += g.b_t ? n0 : n0 * g.ldb;
+    p.M = m;
+    p.N = n;
+    p.C = (uint8_t*)g.C + (m0 * g.ldc + n0) * (g.bf16_out ? 2 : 4);
+    if (g.bias) p.bias = (const uint8_t*)g.bias + n0 * (g.bias_bf16 ? 2 : 4);
+    if (g.R) p.R += m0 * g.ldr + n0;
+    if (g.Z) p.Z += m0 * g.ldz + n0;
+    if (g.P) p.P += m0 * g.ldp + n0;
+    const bool aligned = line_ok(p.A, p.lda, p.a_t ? m : p.K) && line_ok(p.B, p.ldb, p.b_t ? n : p.K);
+    return linear_piece(p, linear_plan(g.a_t, g.b_t, m, n, g.K, aligned), work, work_bytes, s);
+  };
+  return in_pieces(g.M, kPieceRows, [&](int64_t m0, int64_t m) {
+    return in_pieces(g.N, kPieceCols, [&](int64_t n0, int64_t n) { return piece(m0, m, n0, n); });
   });
 }
 

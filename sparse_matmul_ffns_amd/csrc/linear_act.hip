@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256) void linear_bwd_act_kernel(ActBwdArgs a, float
           float z[8];
           load8f((const uint16_t*)a.pre + r * a.ldp, c, a.N, z);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) d[q] *= act_bwd<ACT>(z[q]);
+          for (int q = 0; q < 8; ++q) d[q] = act_gate<ACT>(d[q], z[q]);
         }
         if (a.dZ) store8f((uint16_t*)a.dZ + r * a.lddz, c, a.N, d);
 #pragma unroll

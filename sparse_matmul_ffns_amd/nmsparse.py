@@ -1006,10 +1006,10 @@ def _act(act: str) -> int:
 
 def _here(*ts) -> None:
     """Device tensors (None is skipped) of the current device, on whose stream the call runs."""
-    _dev(*ts)
     here = torch._C._cuda_getDevice()
     for t in ts:
-        if t is not None and t.get_device() != here:
+        if t is not None and t.get_device() != here:   # -1 for one in host memory
+            _dev(t)
             raise ValueError(f"a tensor lies on cuda:{t.get_device()}, but the current device is cuda:{here}")
 
 

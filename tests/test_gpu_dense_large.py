@@ -66,6 +66,26 @@ def test_a_wide_weight():
         assert torch.equal(dW[r:r + 300], (D[:, r:r + 300].double().t() @ X.double()).float())
 
 
+@pytest.mark.parametrize("M,K", [(3, 8), (3, 5), (40, 16), (40, 11)])
+@pytest.mark.parametrize("N", [(1 << 21) + 70, (1 << 22) + 5001])
+def test_many_columns(M, N, K):
+    """More columns than a launch takes at once, in each product."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    X, W, R = (_ints(g, torch.empty(s, device="cuda", dtype=torch.bfloat16)) for s in ((M, K), (N, K), (M, N)))
+    b = _ints(g, torch.empty(N, device="cuda", dtype=torch.bfloat16))
+    z = X.double() @ W.double().t() + b.double()
+    for work in ("auto", None):
+        Y, P = nm.linear_fwd(X, W, bias=b, act="relu", residual=R, return_pre=True, work=work)
+        assert torch.equal(P, z.bfloat16()) and torch.equal(Y, (z.clamp(min=0) + R.double()).bfloat16())
+        D, V = X, W.t().contiguous()                      # dX [M, N] of D [M, K] and a weight [K, N]
+        dx = D.double() @ V.double()
+        assert torch.equal(nm.linear_bwd_x(D, V, pre=R, act="relu", work=work), torch.where(R > 0, dx, torch.zeros_like(dx)).bfloat16())
+        D = X.t().contiguous()                            # dW [M, N] of D [K, M] and X [K, N]
+        dW = torch.ones(M, N, device="cuda")
+        nm.linear_bwd_w(D, V, out=dW, accumulate=True, work=work)
+        assert torch.equal(dW, (1 + dx).float())
+
+
 def test_norm_of_many_rows():
     g = torch.Generator(device="cuda").manual_seed(2)
     T, D, n = 330000, 8192, 40

@@ -95,6 +95,25 @@ def test_values_that_are_not_finite_stay_in_their_rows():
     assert torch.equal(Y[keep], want[keep].bfloat16()) and bool(Y[9].isnan().all()) and not bool(Y[5].isfinite().any())
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 264, 512), (70, 33, 41), (5, 8, 16)])
+def test_what_relu_masks_goes_no_further(M, N, K):
+    """An infinite or undefined gradient where ReLU let nothing through: 0, in the products' epilogues too."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    D, W, P, dY = _ints(g, M, N), _ints(g, N, K), _ints(g, M, K), _ints(g, M, K)
+    bad = dY.clone()
+    bad[P <= 0] = float("inf")
+    bad[3, :][P[3] <= 0] = float("nan")
+    (dZ, db), (dz, d) = nm.linear_bwd_act(bad, P, act="relu"), nm.linear_bwd_act(dY, P, act="relu")
+    assert torch.equal(dZ, dz) and torch.equal(db, d) and bool(dz.isfinite().all())
+    want = nm.linear_bwd_x(D, W, pre=P, act="relu")
+    D[3, 0] = float("inf")                                # row 3 of the product is not finite
+    W[0] = W[0].abs() + 1
+    P[3] = -1
+    want[3] = 0
+    got = nm.linear_bwd_x(D, W, pre=P, act="relu")
+    assert torch.equal(got[3], want[3])
+
+
 @pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32])
 @pytest.mark.parametrize("K", [1, 7, 8, 31, 33, 777, 2047])
 def test_few_rows_of_any_alignment(M, K):

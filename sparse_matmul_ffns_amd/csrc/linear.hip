@@ -171,19 +171,26 @@ hipError_t run_general(const Linear& g, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiled kernel: BM x BN tiles of C by four waves (2 x 2) of 16 FM x 16 FN, in steps of 32 k whose operands pass through
-// a ring of five LDS buffers, filled by direct-to-LDS loads.
+// Tiled kernel: BM x BN tiles of C by four waves (2 x 2) of 16 FM x 16 FN, one workgroup a CU.  The operands pass through LDS
+// in buffers of 64 k, NA of A's and NA + 1 of B's, filled by direct-to-LDS loads.
 //
 // An operand lies in LDS as it does in memory:
-//   reduction contiguous   a row of C per 64-byte LDS row, its 16-byte chunk c at slot c ^ (row / 4 % 4): sixteen
-//                          rows' reads of one chunk cover all 64 banks once; a fragment is one 16-byte read;
+//   reduction contiguous   a row of C per 128-byte LDS row, its 16-byte chunk c at slot c ^ (row / 2 % 8): sixteen
+//                          rows' reads of one chunk cover all 64 banks once; a fragment is one 16-byte read.  (A row's
+//                          128 bytes are a cache line: with buffers of 32 k and 64-byte pieces the L2s give half);
 //   reduction strided      a k per LDS row of 2 BM bytes, its 32-byte segment s (16 columns: a fragment's) at
 //                          s ^ (k % 4 + 4 (k / 8 % 2)).  The transposing read gives a lane four k of one column from
 //                          four rows; a read's half wave touches eight rows (k % 4 and k / 8 % 2 all different), so
 //                          eight segments in different banks; a fragment is two reads.
-// Step s runs FM x FN matrix instructions on fragments that were read during step s - 1, and between them reads
-// step s + 1's and issues the loads of step s + 5 into the buffer that step s was read from: a load has three steps to
-// arrive.  The waves meet once a step.  Rows and columns beyond the operands, and k beyond K, are zeros: a lane's
+// Unit u (64 k) runs 2 FM x FN matrix instructions a wave, the first half on fragments that were read during unit
+// u - 1.  Between those it reads the second half's fragments and issues B's loads of unit u + NA, into the buffer of
+// unit u - 1; then the waves meet, once a unit: all have read unit u.  Between the second half's instructions it reads
+// unit u + 1's first fragments and issues A's loads of unit u + NA into the buffer that unit u was read from.  So a load has
+// NA - 1 units or more to arrive, and a unit's matrix instructions take about 1, 0.5 and 0.25 us with the three tiles: NA is what LDS holds.
+// With operands that are not in a cache that counts: 256 x 128 with NA 2 takes 139 us for 4096 x 2048 x 8192 and with 3 127
+// (bias and residual); 128 x 128 tiles with a ring of five buffers of 32 k, two workgroups a CU, 93 us for 2048 x 2048 x 8192, and
+// with NA 4 71.  8192 x 16384 x 4096 takes 812 us (1350 TFLOP/s, a large library product's rate), 4096^3 97 us.
+// Rows and columns beyond the operands, and k beyond K, are zeros: a lane's
 // 16 bytes lie inside the operand or outside (the contiguous sizes are multiples of eight), and outside its offset
 // is moved beyond the descriptor's size, where nothing is read.
 // ---------------------------------------------------------------------------
@@ -199,24 +206,26 @@ __device__ __forceinline__ void each_of(F f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-// KU: the k of an LDS buffer; NA, NB: A's and B's buffers
-template <int FM_, int FN_, int KU_, int NA_, int NB_>
+constexpr int KU = 64;   // the k of an LDS buffer
+
+// NA: A's buffers; B has one more
+template <int FM_, int FN_, int NA_>
 struct LinCfg {
-  static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN, KU = KU_, NA = NA_, NB = NB_;
+  static constexpr int FM = FM_, FN = FN_, BM = 32 * FM, BN = 32 * FN, NA = NA_, NB = NA + 1;
   static constexpr int A_BYTES = BM * 2 * KU, B_BYTES = BN * 2 * KU, LDS = NA * A_BYTES + NB * B_BYTES;
   static constexpr int LA = A_BYTES / 4096, LB = B_BYTES / 4096, LOADS = LA + LB;   // 1 KB loads a wave and buffer
-  static constexpr int PER_CU = 163840 / LDS;   // workgroups that a CU holds at once
+  static_assert(LDS <= 163840, "a CU's LDS");
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Where a wave's loads of one operand come from, and where a lane's fragments lie in LDS.
-template <bool T, int BR, int KU, int LN>
+template <bool T, int BR, int LN>
 struct Operand {
   static constexpr int ROW = T ? 2 * BR : 2 * KU;     // bytes of an LDS row
-  static constexpr int CH = KU / 8, SH = KU == 64 ? 1 : 2;   // not T: chunks of a row, rows (log2) that share a swizzle
-  static_assert(KU == 32 || LN % 2 == 0, "the swizzle of a wave's loads alternates");
+  static constexpr int CH = KU / 8;                   // not T: chunks of a row
+  static_assert(LN % 2 == 0, "the swizzle of a wave's loads alternates");
   const uint16_t* base;
   int64_t step;          // elements from a buffer's k to the next one's
   int64_t K;
@@ -241,8 +250,8 @@ struct Operand {
       base = X + r0 * ld;
       step = KU;
       constexpr int RL = 64 / CH;   // rows of a load
-      c[0] = (lane % CH) ^ ((lane / CH) >> SH & (CH - 1));
-      c[1] = KU == 64 ? c[0] ^ 4 : c[0];
+      c[0] = (lane % CH) ^ ((lane / CH) >> 1 & (CH - 1));
+      c[1] = c[0] ^ 4;
 #pragma unroll
       for (int t = 0; t < LN; ++t) {
         const int r = RL * (wave * LN + t) + lane / CH;
@@ -269,7 +278,7 @@ struct Operand {
       const int k = 8 * lq + (l16 >> 2);
       return part + k * ROW + 32 * ((first >> 4) ^ ((k & 3) | (k >> 3 & 1) << 2)) + 8 * (l16 & 3);
     }
-    return part + (first + l16) * ROW + ((lq ^ (l16 >> SH & (CH - 1))) << 4);
+    return part + (first + l16) * ROW + ((lq ^ (l16 >> 1 & (CH - 1))) << 4);
   }
   // fragment i of k 32 kk ..
   __device__ static bf16x8 frag(uint32_t at, int kk, int i) {
@@ -451,7 +460,7 @@ __device__ inline void xcd_tile(int id, int ntm, int ntn, int& tm, int& tn) {
 }
 
 template <bool AT, bool BT, int EPI, int ACT, typename Cfg>
-__global__ __launch_bounds__(256, Cfg::PER_CU) void linear_tile_kernel(Linear g) {
+__global__ __launch_bounds__(256) void linear_tile_kernel(Linear g) {
   if (gridDim.y > 1) {
     // a part of the reduction, whose sums go to a matrix of their own
     const int64_t k0 = (int64_t)blockIdx.y * g.part_k;
@@ -472,10 +481,10 @@ __global__ __launch_bounds__(256, Cfg::PER_CU) void linear_tile_kernel(Linear g)
   int tm, tn;
   xcd_tile(blockIdx.x, ntm, ntn, tm, tn);
   const int64_t m0 = (int64_t)(int)uniform((uint32_t)(tm * Cfg::BM)), n0 = (int64_t)(int)uniform((uint32_t)(tn * Cfg::BN));
-  const int units = (int)((g.K + Cfg::KU - 1) / Cfg::KU);
+  const int units = (int)((g.K + KU - 1) / KU);
 
-  Operand<AT, Cfg::BM, Cfg::KU, LA> A;
-  Operand<BT, Cfg::BN, Cfg::KU, LB> B;
+  Operand<AT, Cfg::BM, LA> A;
+  Operand<BT, Cfg::BN, LB> B;
   A.init(g.A, g.lda, m0, g.ra, g.ka, wave, lane);
   B.init(g.B, g.ldb, n0, g.rb, g.kb, wave, lane);
   const uint32_t lds_base = uniform(lds_addr(smem));
@@ -542,101 +551,56 @@ __global__ __launch_bounds__(256, Cfg::PER_CU) void linear_tile_kernel(Linear g)
     for (int j = 0; j < FN; ++j) b0[j] = B.frag(b_first, 0, j);
   };
   // WHOLE below: the k that are loaded lie whole inside K, so the descriptor is the last one moved on
-  if constexpr (Cfg::KU == 64) {
-    static_assert(Cfg::NA == 2 && Cfg::NB == 3, "");
-    fill_a(0);
-    fill_b(0);
-    fill_b(1);
-    fill_a(1);
-    wait_vmcnt<LA + LB>();   // unit 0
-    lds_barrier();
-    first();
-    uint32_t ca = 0, cb = 0;   // unit u's buffers, in bytes
-    u32x4 na = A.desc(2), nb = B.desc(2);
-    auto unit = [&](auto whole, int u) {
-      constexpr bool WHOLE = decltype(whole)::value;
-      constexpr int LOAD_B = N / LB, LOAD_A = N / 2 / LA;
-      uint32_t t[4] = {0, 0, 0, 0};
-      if constexpr (!WHOLE) {
-        na = A.desc(u + 2);
-        nb = B.desc(u + 2);
-        t[0] = A.tail(u + 2, 0), t[1] = A.tail(u + 2, 1), t[2] = B.tail(u + 2, 0), t[3] = B.tail(u + 2, 1);
-      }
-      const uint32_t b1st = cb + Cfg::B_BYTES == 3 * Cfg::B_BYTES ? 0 : cb + Cfg::B_BYTES;        // of unit u + 1
-      const uint32_t b2nd = b1st + Cfg::B_BYTES == 3 * Cfg::B_BYTES ? 0 : b1st + Cfg::B_BYTES;    // and u + 2 (u - 1)
-      // unit u's second half is read; B's unit u + 2 goes where unit u - 1 was
-      multiply(a0, b0, [&](auto m_) {
-        constexpr int m = decltype(m_)::value;
-        read(m_, 1, a_first + ca, b_first + cb, a1, b1);
-        if constexpr (m % LOAD_B == LOAD_B / 2) {
-          load_b(std::integral_constant<int, m / LOAD_B>(), b2nd, nb, t[2], t[3]);
-          if constexpr (WHOLE && m / LOAD_B == LB - 1) forward(nb, adv_b);
-        }
-      });
-      wait_vmcnt<LB>();   // this wave's loads of unit u + 1
-      lds_barrier();      // every wave's; and every wave has read unit u
-      multiply(a1, b1, [&](auto m_) {
-        constexpr int m = decltype(m_)::value;
-        read(m_, 0, a_first + (ca ^ Cfg::A_BYTES), b_first + b1st, a0, b0);
-        if constexpr (m % LOAD_A == LOAD_A / 2 && m / LOAD_A < LA) {
-          load_a(std::integral_constant<int, m / LOAD_A>(), ca, na, t[0], t[1]);
-          if constexpr (WHOLE && m / LOAD_A == LA - 1) forward(na, adv_a);
-        }
-      });
-      ca ^= Cfg::A_BYTES;
-      cb = b1st;
-    };
-    int u = 0;
-    for (const int whole = (int)(g.K / 64) - 2; u < whole; ++u) unit(std::true_type(), u);
-    for (; u < units; ++u) unit(std::false_type(), u);
-  } else {
-    constexpr int RING = Cfg::NA;
-    static_assert(Cfg::NA == Cfg::NB && Cfg::KU == 32, "");
+  constexpr int NA = Cfg::NA;
+  fill_a(0);
+  fill_b(0);
 #pragma unroll
-    for (int u = 0; u < RING; ++u) {
-      fill_a(u);
-      fill_b(u);
-    }
-    wait_vmcnt<(RING - 1) * LOADS>();   // unit 0
-    lds_barrier();
-    first();
-    uint32_t ca = 0, cb = 0;   // unit u's buffers, in bytes
-    u32x4 na = A.desc(RING), nb = B.desc(RING);
-    auto unit = [&](auto whole, int u, const bf16x8 (&a)[FM], const bf16x8 (&b)[FN], bf16x8 (&an)[FM], bf16x8 (&bn)[FN]) {
-      constexpr bool WHOLE = decltype(whole)::value;
-      constexpr int LOAD = N / LOADS;
-      wait_vmcnt<(RING - 2) * LOADS>();   // this wave's loads of unit u + 1
-      lds_barrier();                      // every wave's; and every wave has read unit u
-      const uint32_t xa = ca == (RING - 1) * Cfg::A_BYTES ? 0 : ca + Cfg::A_BYTES, xb = cb == (RING - 1) * Cfg::B_BYTES ? 0 : cb + Cfg::B_BYTES;
-      uint32_t t[2] = {0, 0};
-      if constexpr (!WHOLE) {
-        na = A.desc(u + RING);
-        nb = B.desc(u + RING);
-        t[0] = A.tail(u + RING, 0), t[1] = B.tail(u + RING, 0);
-      }
-      multiply(a, b, [&](auto m_) {
-        constexpr int m = decltype(m_)::value, l = m / LOAD;
-        read(m_, 0, a_first + xa, b_first + xb, an, bn);
-        if constexpr (m % LOAD == LOAD / 2) {
-          if constexpr (l < LA) load_a(std::integral_constant<int, l>(), ca, na, t[0], t[0]);
-          else load_b(std::integral_constant<int, l - LA>(), cb, nb, t[1], t[1]);
-          if constexpr (WHOLE && l == LA - 1) forward(na, adv_a);
-          if constexpr (WHOLE && l == LOADS - 1) forward(nb, adv_b);
-        }
-      });
-      ca = xa;
-      cb = xb;
-    };
-    int u = 0;
-    for (const int whole = (int)(g.K / 32) - RING; u + 1 < whole; u += 2) {
-      unit(std::true_type(), u, a0, b0, a1, b1);
-      unit(std::true_type(), u + 1, a1, b1, a0, b0);
-    }
-    for (; u < units; u += 2) {
-      unit(std::false_type(), u, a0, b0, a1, b1);
-      if (u + 1 < units) unit(std::false_type(), u + 1, a1, b1, a0, b0);
-    }
+  for (int u = 1; u < NA; ++u) {
+    fill_b(u);
+    fill_a(u);
   }
+  wait_vmcnt<(NA - 1) * LOADS>();   // unit 0
+  lds_barrier();
+  first();
+  uint32_t ca = 0, cb = 0;   // unit u's buffers, in bytes
+  u32x4 na = A.desc(NA), nb = B.desc(NA);
+  auto next = [](uint32_t at, uint32_t bytes, int n) { return at == (n - 1) * bytes ? 0 : at + bytes; };
+  auto unit = [&](auto whole, int u) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    constexpr int LOAD_B = N / LB, LOAD_A = N / 2 / LA;
+    uint32_t t[4] = {0, 0, 0, 0};
+    if constexpr (!WHOLE) {
+      na = A.desc(u + NA);
+      nb = B.desc(u + NA);
+      t[0] = A.tail(u + NA, 0), t[1] = A.tail(u + NA, 1), t[2] = B.tail(u + NA, 0), t[3] = B.tail(u + NA, 1);
+    }
+    const uint32_t xa = next(ca, Cfg::A_BYTES, NA), xb = next(cb, Cfg::B_BYTES, NA + 1);   // of unit u + 1
+    const uint32_t free = cb == 0 ? NA * Cfg::B_BYTES : cb - Cfg::B_BYTES;                 // B's of unit u - 1
+    // unit u's second half is read; B's unit u + NA goes where unit u - 1 was
+    multiply(a0, b0, [&](auto m_) {
+      constexpr int m = decltype(m_)::value;
+      read(m_, 1, a_first + ca, b_first + cb, a1, b1);
+      if constexpr (m % LOAD_B == LOAD_B / 2) {
+        load_b(std::integral_constant<int, m / LOAD_B>(), free, nb, t[2], t[3]);
+        if constexpr (WHOLE && m / LOAD_B == LB - 1) forward(nb, adv_b);
+      }
+    });
+    wait_vmcnt<(NA - 2) * LOADS + LB>();   // this wave's loads of unit u + 1
+    lds_barrier();                         // every wave's; and every wave has read unit u
+    multiply(a1, b1, [&](auto m_) {
+      constexpr int m = decltype(m_)::value;
+      read(m_, 0, a_first + xa, b_first + xb, a0, b0);
+      if constexpr (m % LOAD_A == LOAD_A / 2 && m / LOAD_A < LA) {
+        load_a(std::integral_constant<int, m / LOAD_A>(), ca, na, t[0], t[1]);
+        if constexpr (WHOLE && m / LOAD_A == LA - 1) forward(na, adv_a);
+      }
+    });
+    ca = xa;
+    cb = xb;
+  };
+  int u = 0;
+  for (const int whole = (int)(g.K / 64) - NA; u < whole; ++u) unit(std::true_type(), u);
+  for (; u < units; ++u) unit(std::false_type(), u);
   wait_vmcnt<0>();   // no load may land in LDS any more
   // the last instructions' results before any other instruction reads them (the compiler does not see
   // the instructions inside the assembly statements)
@@ -779,9 +743,9 @@ bool line_ok(const uint16_t* X, int64_t ld, int64_t line) {
   return (uintptr_t)X % 16 == 0 && ld % 8 == 0 && ld < (1 << 22) && line % 8 == 0;
 }
 
-using Lin256 = LinCfg<8, 8, 64, 2, 3>;
-using Lin256x128 = LinCfg<8, 4, 64, 2, 3>;
-using Lin128 = LinCfg<4, 4, 32, 5, 5>;
+using Lin256 = LinCfg<8, 8, 2>;
+using Lin256x128 = LinCfg<8, 4, 3>;
+using Lin128 = LinCfg<4, 4, 4>;
 
 template <bool AT, bool BT, int EPI, int ACT>
 hipError_t run_sized(const Linear& g, const LinearPlan& p, hipStream_t s) {
@@ -900,24 +864,24 @@ hipError_t linear_piece(const Linear& g, LinearPlan p, void* work, int64_t work_
   return hipGetLastError();
 }
 
-// The kernel for a product, by what each is expected to take: `full` rounds of as many workgroups as the GPU holds and
-// a last one, each a fixed time and one per 1024 k that grows with the part x of the GPU that is at work (its
-// power and the memory behind the L2s are shared), and where the reduction is cut the parts' bytes and a launch.  The constants are fits
-// of measured times, in us: 4096 x 4096 x 4096 takes 97 with 256 x 256 tiles, 119 with 256 x 128, 137 to 160 with 128 x
-// 128; 4096 x 2048 x 8192 151, 107, 138 to 159, and 115 in two parts of 256 x 256; 1024 x 8192 x 2048 46, 33, 39 to 45; 512 x 2048
-// x 8192 130, 80, 56, and 30 in four parts of 128 x 128; 32 x 2048 x 8192 129, 75, 51, and 16 in eight; 1000^3 37, 22, 14.
+// The kernel for a product, by what each is expected to take: rounds of one workgroup a CU, each a fixed time and one
+// per 1024 k that grows with the part x of the GPU that is at work (its power and the memory behind the L2s are shared),
+// and where the reduction is cut a launch, the parts' bytes and a step per part.  The constants are fits of measured
+// times of operands that are not in a cache, in us, of 65 products in three operand orders; the choice by them is
+// at most 11 % behind the best one there, 0.5 % on average.  With 256 x 256, 256 x 128 and 128 x 128 tiles, each with its best number of
+// parts: 4096 x 4096 x 4096 97, 118, 151; 4096 x 2048 x 8192 123, 113, 134; 1024 x 8192 x 2048 48, 35, 45; 2048 x 2048 x 8192 72, 71, 71 (4, 2 and 1
+// parts); 1000^3 26, 22, 16; 512 x 2048 x 8192 37, 33, 33 (12, 8 and 4).
 struct TileCost {
-  int tile, bm, bn, held;          // held: workgroups that the GPU computes at once
+  int tile, bm, bn;
   double fixed, alone, shared;     // a round: fixed + (alone + shared x^2) per 1024 k
 };
-constexpr TileCost kTiles[] = {{LinearPlan::T128, 128, 128, 256, 5, 6.1, 2.1},
-                               {LinearPlan::T256x128, 256, 128, 256, 7, 9.2, 3.3},
-                               {LinearPlan::T256, 256, 256, 256, 10, 15, 6.5}};
+constexpr TileCost kTiles[] = {{LinearPlan::T128, 128, 128, 5.2, 8.6, 0.4},
+                               {LinearPlan::T256x128, 256, 128, 7.4, 11.8, 1.8},
+                               {LinearPlan::T256, 256, 256, 10.6, 16.6, 5.6}};
+constexpr int kRound = 256;        // workgroups that the GPU computes at once
 
 double round_us(const TileCost& t, double k, int64_t workgroups) {
-  // two 128 x 128 tiles fit a CU, and together take as long as one after the other
-  if (t.tile == LinearPlan::T128 && workgroups > t.held) return t.fixed + 16.5 * k;
-  const double x = (double)workgroups / t.held;
+  const double x = (double)workgroups / kRound;
   return t.fixed + (t.alone + t.shared * x * x) * k;
 }
 
@@ -929,13 +893,12 @@ LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool a
   double least = 1e30;
   for (const TileCost& t : kTiles) {
     const int64_t tiles = (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn);
-    const int64_t round = t.tile == LinearPlan::T128 ? 2 * t.held : t.held;
-    for (int p = 1; p <= 16 && (p == 1 || (K >= 256 * p && tiles * p <= 2 * round)); ++p) {
+    for (int p = 1; p <= 16 && (p == 1 || (K >= 256 * p && tiles * p <= 4 * kRound)); ++p) {
       const int64_t part_k = p == 1 ? K : ((K + p - 1) / p + 63) / 64 * 64, parts = (K + part_k - 1) / part_k, wgs = tiles * parts;
       const double k = part_k / 1024.0;
-      double us = (double)(wgs / round) * round_us(t, k, round);
-      if (wgs % round) us += round_us(t, k, wgs % round);
-      if (parts > 1) us += 4 + 8e-6 / 6 * (double)(parts * M) * (double)N;
+      double us = (double)(wgs / kRound) * round_us(t, k, kRound);
+      if (wgs % kRound) us += round_us(t, k, wgs % kRound);
+      if (parts > 1) us += 3.6 + 0.3 * (double)parts + 1e-6 * (double)(parts * M) * (double)N;
       if (us < least) {
         least = us;
         best = LinearPlan{t.tile, (int)parts, part_k, false};

@@ -54,7 +54,14 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void rms_norm_kernel(NormArgs 
   typedef std::conditional_t<F8, double, float> Sum;
   __shared__ Sum part[16];
   const int t = threadIdx.x % NT;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT;
+  int64_t group = blockIdx.x;
+  if constexpr (F8) {
+    // Workgroups are dealt to the 8 XCDs in turn; an XCD takes a run of rows, so that their scales, which
+    // lie together, meet in its L2
+    const int64_t x = group % 8, per = gridDim.x / 8, rest = gridDim.x % 8;
+    group = x * per + (x < rest ? x : rest) + group / 8;
+  }
+  const int64_t row = group * ROWS + threadIdx.x / NT;
   if (row >= a.T) return;   // NT 64: no barrier follows; else ROWS is 1 and every row exists
   const T* X = (const T*)a.X + row * a.ldx;
   const T* R = a.R ? (const T*)a.R + row * a.ldr : nullptr;
@@ -313,7 +320,7 @@ hipError_t run_bwd(const NormBwdArgs& a, hipStream_t s) {
 // The threads of a row and their vectors, by its width (at most 16384).  Measured on bf16 rows that are not in
 // a cache, us: 8192 x 4096 with a residual (268 MB) 44.5 with 256 threads, 43.4 with 128, 49 with 64, 51 with 1024 (its gradients, 268 MB,
 // 48.7, 55.6, - and 75); 64 x 4096 3.6, 4.3, 5.5, 3.3; 4096 x 2048 13.0, 11.3, 11.6, 16.9; 4096 x 8192 45.5 with 256 and 44.0 with 512.  To 8
-// bits 8192 x 4096 takes 44.2 and 4096 x 2048 14.4.
+// bits 4096 x 2048 takes 14.8 (15.5 with 64; 15.9 before an XCD's workgroups took neighbouring rows).
 template <typename T>
 hipError_t fwd_by_width(const NormArgs& a, hipStream_t s) {
   const int64_t n = (a.D + 7) / 8;

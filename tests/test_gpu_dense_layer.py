@@ -6,6 +6,8 @@ output carries three of them in its FFN part, a gradient at most six (0.0055); t
 norm.  The gradients are also held to differences of a 64-bit block.
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -132,6 +134,64 @@ def test_passes_and_clipping():
     layer.W_up.mul_(2)
     with pytest.raises(RuntimeError):
         layer.backward(x)
+
+
+def test_threads_on_streams_of_their_own():
+    """One layer, four threads with a stream each, passes of different sizes at once: each gives what it gives alone."""
+    ps = [_parts(60 + 70 * i, 256, 520, "silu", True, i) for i in range(4)]
+    for p in ps[1:]:
+        p.update({k: ps[0][k] for k in ("wn", "wu", "wd", "bu", "bd")})
+    layer = _layer(ps[0], "silu")
+    args = [[p[k].cuda() for k in ("x", "r", "dy")] for p in ps]
+
+    def step(x, r, dy):
+        y, saved = layer.forward(x, r, return_saved=True)
+        dx, grads = layer.backward(dy, saved)
+        return [y, dx, nm.grad_clip(grads, 0.1), *grads]
+    want = [step(*a) for a in args]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(10):
+                    got[i] = step(*args[i])
+            stream.synchronize()
+        except Exception as e:
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for a, b in zip(got, want):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_the_layer_in_a_graph():
+    """A training step captured once and replayed with new inputs and weights, an eager step between the replays."""
+    p = _parts(130, 128, 264, "gelu_tanh", True, 9)
+    layer = _layer(p, "gelu_tanh")
+    x, r, dy = (p[k].cuda() for k in ("x", "r", "dy"))
+
+    def step():
+        y, saved = layer.forward(x, r, return_saved=True)
+        dx, grads = layer.backward(dy, saved)
+        return [y, dx, nm.grad_clip(grads, 0.1), *grads]
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(3):
+        x.mul_(-0.5)
+        layer.W_up.mul_(1.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, step())), i
 
 
 def test_the_norm_feeds_the_8_bit_product():

@@ -674,9 +674,9 @@ def _ld(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor whose rows are contiguous; strides of dimensions of one element are
     whatever torch left there and do not count."""
     stride = t.stride()
-    if len(stride) != 2 or (stride[1] != 1 and t.shape[1] != 1):
+    if len(stride) != 2 or (stride[1] != 1 and t.size(1) != 1):
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    return stride[0] if t.shape[0] > 1 else max(stride[0], t.shape[1])
+    return stride[0] if t.size(0) > 1 else max(stride[0], t.size(1))
 
 
 def _fp8(t: torch.Tensor, name: str) -> int:
@@ -1060,16 +1060,17 @@ def _workspace(work, need: int, like):
     return work, work.numel() * work.element_size()
 
 
-def _norm_args(X, w, residual, H, rstd):
+def _norm_args(X, w, residual, H, rstd, *others):
     T, D = _two(X, "X")
-    _here(X, w, residual, H, rstd)
+    _here(X, w, residual, H, rstd, *others)
     if w.shape != (D,) or not w.is_contiguous():
         raise ValueError(f"w must be a contiguous [{D}] tensor")
     ldx = _ld(X, "X")
     ldr = _opt(residual, (T, D), X.dtype, "residual")
     if H is None and residual is not None:
-        H = X.new_empty((T, D))
-    ldh = _opt(H, (T, D), X.dtype, "H")
+        H, ldh = X.new_empty((T, D)), D
+    else:
+        ldh = _opt(H, (T, D), X.dtype, "H")
     return T, D, ldx, ldr, H, ldh, _new_vector(rstd, T, X, "rstd")
 
 
@@ -1077,8 +1078,7 @@ def rms_norm(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=None,
     """h = X [T, D] + residual, Y = h / sqrt(mean(h^2) + eps) * w: returns (Y, H, rstd), H the rounded sum
     (without a residual X itself, unless H is given) and rstd [T] fp32, what rms_norm_bwd reads.  In place: H may be
     X or the residual, Y may be X."""
-    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd)
-    _here(Y)
+    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Y)
     Y, ldy = _new_or(Y, (T, D), X.dtype, X, "Y")
     _check(lib().rms_norm(_dt(X), _p(X), ldx, _p(residual), ldr, _dt(w), _p(w), eps, T, D, _p(H), ldh, _p(Y), ldy,
                           _p(rstd), _stream()), "rms_norm")
@@ -1090,8 +1090,7 @@ def rms_norm_fp8(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=N
     """rms_norm with its result in 8 bits and a power-of-two scale per row and 128 columns, as fp8_gemm_nt takes it:
     returns (Q [T, Dp], S [Dp / 128, T], H, rstd), Dp = D rounded up to 128, the columns beyond D 0.  With a tensor Y
     [T, D] the result is stored there in X's dtype too."""
-    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd)
-    _here(Q, S, Y)
+    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Q, S, Y)
     Dp = _up(D, 128)
     if Q is None:
         Q = X.new_empty((T, Dp), dtype=fmt)
@@ -1154,9 +1153,7 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
     if bias is not None and (bias.shape != (N,) or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous [{N}] tensor")
     ldr = _opt(residual, (M, N), X.dtype, "residual")
-    if out is None:
-        out = X.new_empty((M, N), dtype=out_dtype)
-    ldy = _matrix(out, (M, N), None, "out")
+    out, ldy = _new_or(out, (M, N), out_dtype if out is None else None, X, "out")
     if pre is None and return_pre:
         pre = X.new_empty((M, N), dtype=torch.bfloat16)
     ldp = _opt(pre, (M, N), torch.bfloat16, "pre")
@@ -1207,9 +1204,7 @@ def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
     if act != "none" and pre is None:
         raise ValueError("pre is needed for an activation's gradient")
     ldp = _opt(pre, (M, K), dZ.dtype, "pre")
-    if out is None:
-        out = dZ.new_empty((M, K), dtype=out_dtype)
-    lddx = _matrix(out, (M, K), None, "out")
+    out, lddx = _new_or(out, (M, K), out_dtype if out is None else None, dZ, "out")
     work, nbytes = _linear_work(work, NM_LINEAR_BWD_X, M, N, K, dZ, lddz, W, ldw)
     _check(lib().linear_bwd_x(_dt(dZ), _p(dZ), lddz, _p(W), ldw, _p(pre), ldp, _act(act), M, N, K, _dt(out), _p(out),
                               lddx, _p(work), nbytes, _stream()), "linear_bwd_x")
@@ -1224,11 +1219,9 @@ def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = tor
     K = _two(X, "X")[1]
     _here(dZ, X, out)
     lddz, ldx = _ld(dZ, "dZ"), _matrix(X, (M, K), dZ.dtype, "X")
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = dZ.new_empty((N, K), dtype=out_dtype)
-    lddw = _matrix(out, (N, K), None, "out")
+    if out is None and accumulate:
+        raise ValueError("accumulate needs out")
+    out, lddw = _new_or(out, (N, K), out_dtype if out is None else None, dZ, "out")
     work, nbytes = _linear_work(work, NM_LINEAR_BWD_W, M, N, K, dZ, lddz, X, ldx)
     _check(lib().linear_bwd_w(_dt(dZ), _p(dZ), lddz, _p(X), ldx, M, N, K, int(bool(accumulate)), _dt(out), _p(out),
                               lddw, _p(work), nbytes, _stream()), "linear_bwd_w")

@@ -867,7 +867,7 @@ hipError_t linear_piece(const Linear& g, LinearPlan p, void* work, int64_t work_
 // The kernel for a product, by what each is expected to take: rounds of one workgroup a CU, each a fixed time and one
 // per 1024 k that grows with the part x of the GPU that is at work (its power and the memory behind the L2s are shared),
 // and where the reduction is cut a launch, the parts' bytes and a step per part.  The constants are fits of measured
-// times of operands that are not in a cache, in us, of 65 products in three operand orders; the choice by them is
+// times of operands that are not in a cache, in us, of 54 products in three operand orders; the choice by them is
 // at most 11 % behind the best one there, 0.5 % on average.  With 256 x 256, 256 x 128 and 128 x 128 tiles, each with its best number of
 // parts: 4096 x 4096 x 4096 97, 118, 151; 4096 x 2048 x 8192 123, 113, 134; 1024 x 8192 x 2048 48, 35, 45; 2048 x 2048 x 8192 72, 71, 71 (4, 2 and 1
 // parts); 1000^3 26, 22, 16; 512 x 2048 x 8192 37, 33, 33 (12, 8 and 4).

@@ -747,7 +747,8 @@ nm_status moe_combine_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void*
  *
  * An output of these calls may be one of the call's own inputs, at the same
  * address with the same row stride and type, where that is stated; no other
- * overlap is allowed.
+ * overlap is allowed.  Work memory holds nothing between calls, but calls that
+ * may run at the same time need their own.
  * ---------------------------------------------------------------------------
  */
 

@@ -6,7 +6,10 @@
 // squares are 64-bit: the square of an fp32 value neither overflows nor vanishes there, and the result is
 // the norm of the values rounded once.  Partial sums are added in a fixed order.
 //
-// Bound by bytes: every value is read for the norm, read again and written.
+// Bound by bytes: every value is read for the norm, read again and written.  537 MB that are not in a cache: the norm 95 us
+// (5.6 TB/s; with 2048 workgroups 99, with four of a thread's loads in flight 97), clipped in place in bf16 243 (four in flight, 2048
+// workgroups: 319), fp32 to other tensors 311; 537 MB of bf16 in 192 tensors to fp32
+// 437.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -199,7 +202,7 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(Table t, const double* 
 }
 
 // Few elements: the norm and, where max_norm is not negative, the scaling in one workgroup, whose waves take a
-// chunk each.  2 matrices of 128 x 128 and a few vectors: one launch in place of two or three.
+// chunk each.  2 matrices of 128 x 128 and a few vectors: 8 us on the GPU in one launch; in three 25 us a call, now 14.
 __global__ __launch_bounds__(1024) void grad_one_kernel(Table t, float* norm, float max_norm) {
   __shared__ double sh[16];
   const uint32_t wave = threadIdx.x >> 6;

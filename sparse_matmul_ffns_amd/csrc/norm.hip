@@ -278,7 +278,8 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void rms_norm_bwd_kernel(NormB
 template <typename T, int NT, int V>
 hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
   constexpr int ROWS = NT == 64 ? 4 : 1, TH = NT * ROWS;
-  return in_pieces(a.T, kPieceRows256, [&](int64_t r0, int64_t n) {
+  constexpr int64_t PIECE = (int64_t(1) << 30) / NT;   // rows of a launch: 2^30 work-items
+  return in_pieces(a.T, PIECE, [&](int64_t r0, int64_t n) {
     NormArgs p = a;
     p.X = (const T*)a.X + r0 * a.ldx;
     if (a.R) p.R = (const T*)a.R + r0 * a.ldr;

@@ -6,7 +6,8 @@ namespace nms {
 namespace {
 
 // out[c] = sum over g of part[g][c], in fp32: 64 columns a workgroup, its 16 waves every 16th row each,
-// then the waves' sums in their order.  The order does not depend on anything but G.
+// then the waves' sums in their order.  The order does not depend on anything but G.  512 x 4096 and 64 x 8192 take 5 us,
+// which is a launch behind another one (with every load in flight at once the same).
 __global__ __launch_bounds__(1024) void sum_partials_kernel(const float* part, int64_t G, int64_t N, float* out) {
   __shared__ float sh[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

@@ -112,6 +112,22 @@ def test_norm_of_many_rows():
     assert bool(((dw.double() - dw1.double()).abs() <= (2 * n + 8) * 2 ** -24 * mag).all())
 
 
+def test_norm_of_wide_rows_past_one_launch():
+    """4194307 rows of 8200 (69 GB, in place): at 1024 work-items a row, more than 2^32 of them."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    T, D, n = (1 << 22) + 3, 8200, 4096
+    base = torch.randn(n, D, generator=g, device="cuda").bfloat16()
+    w = torch.randn(D, generator=g, device="cuda").bfloat16()
+    X, rstd = torch.empty(T, D, device="cuda", dtype=torch.bfloat16), torch.zeros(T, device="cuda")
+    for r in range(0, T, n):
+        X[r:r + n] = base[:T - r]
+    want, _, r0 = nm.rms_norm(base, w)
+    nm.rms_norm(X, w, Y=X, rstd=rstd)
+    for r in range(0, T, n):
+        m = min(n, T - r)
+        assert torch.equal(X[r:r + m], want[:m]) and torch.equal(rstd[r:r + m], r0[:m]), r
+
+
 def test_act_gradient_of_many_rows():
     g = torch.Generator(device="cuda").manual_seed(3)
     M, N, n = 290000, 8192, 24

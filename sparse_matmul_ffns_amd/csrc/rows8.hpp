@@ -74,11 +74,4 @@ __device__ inline void store8f(T* p, int64_t c, int64_t D, const float (&v)[8]) 
   r.template store<TAIL>(p, c, D);
 }
 
-// Sum over the 64 lanes, the same in each of them and in the same order in every wave.
-__device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) v += __shfl_xor(v, d);
-  return v;
-}
-
 }  // namespace nms

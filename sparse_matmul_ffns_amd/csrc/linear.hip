@@ -7,6 +7,7 @@
 #include "dma.hpp"
 #include "launch.hpp"
 #include "pieces.hpp"
+#include "rows8.hpp"
 
 #include <utility>
 
@@ -635,8 +636,7 @@ hipError_t run_tile(const Linear& g, int parts, hipStream_t s) {
 // the registers of the matrix instruction, with no LDS and no barrier on the way.  A workgroup computes 16 FM rows of A by
 // 16 FN rows of B; its KS waves take every KS-th chunk of 32 CH k, each with the next chunk's loads in flight, and
 // add their sums through LDS in the order of the waves.  The lanes of a row that does not exist load nothing.
-// One token (FM 1, FN 1, KS 8, CH 4), weights that are not in a cache: 16384 x 4096 24 us (5.5 TB/s, a large copy's rate),
-// 8192 x 2048 8.7 us; with FN 2 and KS 4 31 and 10.4.
+// 16 x 8192 x 2048 12.7 us, 16 x 2048 x 8192 19.2 (one workgroup a 16 columns leaves half of the CUs without work there; with 16 waves 19.8).
 // ---------------------------------------------------------------------------
 template <int FM, int FN, int KS, int CH, bool TAIL>
 __global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
@@ -737,6 +737,75 @@ hipError_t run_rows(const Linear& g, hipStream_t s) {
   else hipLaunchKernelGGL((linear_rows_kernel<FM, FN, KS, CH, false>), dim3((unsigned)wgs), dim3(64 * KS), 0, s, g);
   return hipGetLastError();
 }
+// ---------------------------------------------------------------------------
+// One row of A (a token): products on the vector unit, so that a wave's load of B is a kilobyte of one row (the matrix
+// instruction's operand is 64 bytes of each of 16 rows, which costs where rows lie far apart).  A workgroup takes four rows
+// of B, its waves every blockDim / 64-th chunk of 512 k, two chunks in flight; sums over the lanes, then over the waves in their order.
+// Weights that are not in a cache, replayed from a graph, us (in brackets the kernel for few rows): 2048 x 8192 10.0 (12.4),
+// 4096 x 16384 29.2 (35.3; 4.6 TB/s), 16384 x 4096 28.7 (29.7), 8192 x 2048 9.5 (9.5), 8192 x 2049 11.1 (17.4), 1000 x 1000 3.8 (3.1).
+// Two rows in this manner take 12.0 and 10.4 for the first and the fourth (13.4 and 10.0), four 14.3 and 13.0 (14.6 and 10.6).
+// ---------------------------------------------------------------------------
+template <bool TAIL>
+__global__ __launch_bounds__(512) void linear_token_kernel(Linear g) {
+  constexpr int NR = 4, U = 2;
+  __shared__ float part[8][NR];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int64_t n0 = (int64_t)blockIdx.x * NR;
+  const uint16_t* brow[NR];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) brow[j] = g.B + (n0 + j < g.N ? n0 + j : n0) * g.ldb;
+  float acc[NR] = {};
+  const int64_t step = (int64_t)waves * 512;
+  for (int64_t k0 = wave * 512 + lane * 8; k0 < g.K; k0 += U * step) {
+    Row8<uint16_t> a[U], b[U][NR];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = k0 + u * step;
+      if (k >= g.K) break;
+#pragma unroll
+      for (int j = 0; j < NR; ++j) b[u][j].template load<TAIL>(brow[j], k, g.K);
+      a[u].template load<TAIL>(g.A, k, g.K);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u * step >= g.K) break;
+      float x[8];
+      a[u].get(x);
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        float w[8];
+        b[u][j].get(w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[j] = __builtin_fmaf(x[q], w[q], acc[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+#pragma unroll
+    for (int d = 32; d >= 1; d /= 2) acc[j] += __shfl_xor(acc[j], d);
+    if (lane == 0) part[wave][j] = acc[j];
+  }
+  __syncthreads();
+  if (threadIdx.x > 0) return;
+  f32x4 v;
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    v[j] = part[0][j];
+    for (int w = 1; w < waves; ++w) v[j] += part[w][j];
+  }
+  finish4(g, 0, n0, v);
+}
+
+hipError_t run_token(const Linear& g, hipStream_t s) {
+  const int threads = g.K > 7168 ? 512 : (int)((g.K + 1023) / 1024) * 64;   // two chunks a wave, up to eight waves
+  const int64_t wgs = (g.N + 3) / 4;
+  if (!grid_ok(wgs, threads)) return hipErrorInvalidConfiguration;
+  if (g.K % 8) hipLaunchKernelGGL(linear_token_kernel<true>, dim3((unsigned)wgs), dim3(threads), 0, s, g);
+  else hipLaunchKernelGGL(linear_token_kernel<false>, dim3((unsigned)wgs), dim3(threads), 0, s, g);
+  return hipGetLastError();
+}
+
 // What the tiled kernel asks of an operand: 16-byte loads that lie inside it or outside, and 31-bit offsets
 // inside a tile.  `line` is its contiguous size.
 bool line_ok(const uint16_t* X, int64_t ld, int64_t line) {
@@ -818,6 +887,7 @@ hipError_t run_pack(const Pack& a, const Pack& b, hipStream_t s) {
 
 hipError_t linear_piece(const Linear& g, LinearPlan p, void* work, int64_t work_bytes, hipStream_t s) {
   if (force_generic()) return run_general(g, s);
+  if (p.tile == LinearPlan::ROWS && g.M == 1) return run_token(g, s);
   if (p.tile == LinearPlan::ROWS) return g.M > 16 ? run_rows<2, 2, 8, 4>(g, s) : run_rows<1, 1, 8, 4>(g, s);
   Linear q = g;
   q.ra = g.M, q.rb = g.N, q.ka = q.kb = g.K;

@@ -956,8 +956,8 @@ double round_us(const TileCost& t, double k, int64_t workgroups) {
 }
 
 LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool aligned) {
-  // Few rows: the kernel without LDS, against the best of the tiles in us: 1 x 16384 x 4096 24 and 31, 1 x 2048 x 8192 12 and 16, 16 x
-  // 8192 x 2048 11 and 15, 16 x 2048 x 8192 18 and 18; 32 x 8192 x 2048 13 and 15, but 32 x 2048 x 8192 26 and 18
+  // Few rows: the kernel without LDS, against the best of the tiles in us: 1 x 2048 x 8192 12 and 16 (10 by the kernel for one
+  // row), 16 x 8192 x 2048 11 and 15, 16 x 2048 x 8192 18 and 18; 32 x 8192 x 2048 13 and 15, but 32 x 2048 x 8192 26 and 18
   if (!a_t && !b_t && (M <= 16 || (M <= 32 && K <= 2048))) return LinearPlan{LinearPlan::ROWS, 1, K, false};
   LinearPlan best{LinearPlan::T256, 1, K, false};
   double least = 1e30;

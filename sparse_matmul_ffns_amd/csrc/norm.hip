@@ -36,6 +36,15 @@ __device__ inline uint32_t max16(uint32_t m) {
   return dpp_umax<0x121>(dpp_umax<0x122>(dpp_umax<0x124>(dpp_umax<0x128>(m))));
 }
 
+// The bits of an fp32 value that lies where y lies: y's first 20 bits behind the point and, where more follow, the last of them set
+// (rounding to odd).  Rounding that to 8 bits, or comparing it with a border of 8 bits, comes out as for y
+// itself, ties included; rounding y's nearest fp32 value would round twice.  (Below fp32's normal numbers it is rounded again.)
+__device__ inline uint32_t odd_bits(double y) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, y);
+  const uint32_t rest = (uint32_t)b, hi = (uint32_t)(b >> 32) | (rest < 1u ? rest : 1u);
+  return __float_as_uint((float)__builtin_bit_cast(double, (uint64_t)hi << 32));
+}
+
 template <bool TAIL>
 __device__ inline void load_w(const void* w, int bf16, int64_t c, int64_t D, float (&v)[8]) {
   if (bf16) load8f<uint16_t, TAIL>((const uint16_t*)w, c, D, v);
@@ -46,8 +55,8 @@ __device__ inline void load_w(const void* w, int bf16, int64_t c, int64_t D, flo
 // i-th, so that neighbours read neighbouring bytes and a block of 128 columns lies in 16 neighbouring
 // lanes.  The row stays in registers between its two uses.
 //   h = x + residual, rstd = 1 / sqrt(mean h^2 + eps), y = h rstd w.
-// F8: y decides between 8-bit values and scales, so it is the exact product rounded once: squares are summed in 64 bits, rstd
-// has a second word, and the products keep their remainders.
+// F8: y decides between 8-bit values and scales, so everything behind the loads is 64-bit (which the vector unit does at fp32's
+// rate) and y is rounded once, to 8 bits.
 template <typename T, int NT, int V, bool F8, bool TAIL>
 __global__ __launch_bounds__(NT == 64 ? 256 : NT) void rms_norm_kernel(NormArgs a) {
   constexpr int ROWS = NT == 64 ? 4 : 1;
@@ -75,62 +84,69 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void rms_norm_kernel(NormArgs 
       if (R) r[i].template load<TAIL>(R, c, D);
     }
   }
-  float h[V][8];
-  Sum sum = 0;
+  Sum h[V][8], sum = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int64_t c = 8 * (int64_t)(t + NT * i);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) h[i][q] = 0.f;
+    for (int q = 0; q < 8; ++q) h[i][q] = 0;
     if (c >= D) continue;
-    x[i].get(h[i]);
+    float f[8];
+    x[i].get(f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) h[i][q] = (Sum)f[q];
     if (R) {
-      float f[8];
-      r[i].get(f);
+      float e[8];
+      r[i].get(e);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) h[i][q] += f[q];
+      for (int q = 0; q < 8; ++q) {
+        f[q] += e[q];
+        if constexpr (F8) h[i][q] += (double)e[q];
+        else h[i][q] = f[q];
+      }
     }
-    if (a.H) store8f<T, TAIL>((T*)a.H + row * a.ldh, c, D, h[i]);
+    if (a.H) store8f<T, TAIL>((T*)a.H + row * a.ldh, c, D, f);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum = F8 ? __builtin_fma((double)h[i][q], (double)h[i][q], sum) : (Sum)__builtin_fmaf(h[i][q], h[i][q], (float)sum);
+    for (int q = 0; q < 8; ++q) {
+      if constexpr (F8) sum = __builtin_fma(h[i][q], h[i][q], sum);
+      else sum = __builtin_fmaf(h[i][q], h[i][q], sum);
+    }
   }
   sum = row_sum<NT>(sum, part);
-  float rstd, rest = 0.f;   // 1 / sqrt = rstd + rest
+  Sum rho;
   if constexpr (F8) {
-    // one Newton step in 64 bits from the 32-bit result
+    // two Newton steps in 64 bits from the 32-bit result (the second for its last eight bits)
     const double m = sum / (double)D + (double)a.eps;
-    const double r0 = (double)(1.f / sqrtf((float)m)), e = r0 * __builtin_fma(-0.5 * m * r0, r0, 1.5);
-    const double r1 = r0 - r0 == 0.0 && e - e == 0.0 ? e : r0;   // infinite or vanishing sums stay what they are
-    rstd = (float)r1;
-    rest = (float)(r1 - (double)rstd);
+    rho = (double)(1.f / sqrtf((float)m));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const double e = rho * __builtin_fma(-0.5 * m * rho, rho, 1.5);
+      rho = __builtin_isfinite(e) ? e : rho;   // infinite or vanishing sums stay what they are
+    }
   } else {
-    rstd = 1.f / sqrtf(sum / (float)D + a.eps);
+    rho = 1.f / sqrtf(sum / (float)D + a.eps);
   }
+  const float rstd = (float)rho;
   if (a.rstd && t == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int64_t c = 8 * (int64_t)(t + NT * i);
     if (c >= Dq) continue;   // whole blocks: all of their 16 lanes go on
     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    Raw8<uint32_t> v;
+    if constexpr (F8) v.zero();
     if (c < D) {
       float w[8];
       load_w<TAIL>(a.w, a.w_bf16, c, D, w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float p = h[i][q] * rstd;
-        y[q] = p * w[q];
-        if constexpr (F8) {
-          const float pe = __builtin_fmaf(h[i][q], rest, __builtin_fmaf(h[i][q], rstd, -p));
-          const float ye = __builtin_fmaf(pe, w[q], __builtin_fmaf(p, w[q], -y[q]));
-          if (ye - ye == 0.f) y[q] += ye;   // not beside an infinity or NaN
-        }
+        const Sum p = h[i][q] * rho * (Sum)w[q];
+        y[q] = (float)p;
+        if constexpr (F8) v.w[q] = !TAIL || c + q < D ? odd_bits(p) : 0u;
       }
       if (a.Y) store8f<T, TAIL>((T*)a.Y + row * a.ldy, c, D, y);
     }
     if constexpr (F8) {
-      Raw8<uint32_t> v;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v.w[q] = c + q < D ? __float_as_uint(y[q]) : 0u;
       uint32_t m = max16(v.row_max());
       if (m >= 0x7F800000u) {   // the same in a block's 16 lanes
         v.clean();

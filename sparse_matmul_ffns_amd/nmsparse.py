@@ -1060,14 +1060,15 @@ def _workspace(work, need: int, like):
     return work, work.numel() * work.element_size()
 
 
-def _norm_args(X, w, residual, H, rstd, *others):
+def _norm_args(X, w, residual, H, rstd, Y, *others):
     T, D = _two(X, "X")
-    _here(X, w, residual, H, rstd, *others)
+    _here(X, w, residual, H, rstd, Y, *others)
     if w.shape != (D,) or not w.is_contiguous():
         raise ValueError(f"w must be a contiguous [{D}] tensor")
     ldx = _ld(X, "X")
     ldr = _opt(residual, (T, D), X.dtype, "residual")
-    if H is None and residual is not None:
+    # without a residual h is X itself, unless Y takes its place
+    if H is None and (residual is not None or (Y is not None and Y.data_ptr() == X.data_ptr())):
         H, ldh = X.new_empty((T, D)), D
     else:
         ldh = _opt(H, (T, D), X.dtype, "H")
@@ -1076,8 +1077,8 @@ def _norm_args(X, w, residual, H, rstd, *others):
 
 def rms_norm(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=None, H=None, Y=None, rstd=None):
     """h = X [T, D] + residual, Y = h / sqrt(mean(h^2) + eps) * w: returns (Y, H, rstd), H the rounded sum
-    (without a residual X itself, unless H is given) and rstd [T] fp32, what rms_norm_bwd reads.  In place: H may be
-    X or the residual, Y may be X."""
+    (without a residual X itself, unless H is given or Y is X) and rstd [T] fp32, what rms_norm_bwd reads.  In place:
+    H may be X or the residual, Y may be X."""
     T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Y)
     Y, ldy = _new_or(Y, (T, D), X.dtype, X, "Y")
     _check(lib().rms_norm(_dt(X), _p(X), ldx, _p(residual), ldr, _dt(w), _p(w), eps, T, D, _p(H), ldh, _p(Y), ldy,
@@ -1090,7 +1091,7 @@ def rms_norm_fp8(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=N
     """rms_norm with its result in 8 bits and a power-of-two scale per row and 128 columns, as fp8_gemm_nt takes it:
     returns (Q [T, Dp], S [Dp / 128, T], H, rstd), Dp = D rounded up to 128, the columns beyond D 0.  With a tensor Y
     [T, D] the result is stored there in X's dtype too."""
-    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Q, S, Y)
+    T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Y, Q, S)
     Dp = _up(D, 128)
     if Q is None:
         Q = X.new_empty((T, Dp), dtype=fmt)

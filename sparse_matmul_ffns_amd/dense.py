@@ -75,7 +75,7 @@ class DenseFFN:
         those of parameters(), in their order and fp32.
 
         Refused (RuntimeError): a second backward() of a pass that took the place of one without a backward pass; x or the
-        parameters changed in place since the pass (as torch sees it)."""
+        parameters changed in place since the pass, by torch's calls or by this library's (a tensor's version counts both)."""
         if saved is None:
             saved = self.saved
             if saved is None:

@@ -90,7 +90,7 @@ class ExpertFFN:
         [T, E], dW_up [E, F, D] and dW_down [E, D, F] in fp32).
 
         Refused (RuntimeError): a second backward() of a pass that took the place of one without
-        a backward pass, as two forwards and then two backwards make it; x, logits (as torch sees it) or
+        a backward pass, as two forwards and then two backwards make it; x, logits (by torch's calls or this library's) or
         the weights changed since the pass."""
         if saved is None:
             saved = self.saved

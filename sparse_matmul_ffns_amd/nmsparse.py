@@ -189,6 +189,14 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _wrote(given) -> None:
+    """Count an in-place change of the outputs that the caller gave (None: not given), as torch's own calls do.  The kernels write
+    by address, which torch does not see; the layers' checks and torch's own of tensors kept for a backward pass go by that count."""
+    given = [t for t in given if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def sizes(R: int, K: int, N: int = 2, M: int = 4, V: int = 0):
     """(n_values, meta_bytes, colsel_bytes) of the compressed form (host-only)."""
     a, b, c = _i64(), _i64(), _i64()
@@ -197,17 +205,20 @@ def sizes(R: int, K: int, N: int = 2, M: int = 4, V: int = 0):
 
 
 def nm_prune(A: torch.Tensor, N: int = 2, M: int = 4, mask: torch.Tensor | None = None) -> torch.Tensor:
+    given = (mask,)
     _dev(A, mask)
     R, K = A.shape
     lda = _rows(A, "A")
     if mask is None:
         mask = torch.empty((R, K), dtype=torch.uint8, device=A.device)
     _check(lib().nm_prune(_dt(A), _p(A), lda, R, K, N, M, _p(mask), _rows(mask, "mask"), _stream()), "nm_prune")
+    _wrote(given)
     return mask
 
 
 def nm_compress(A: torch.Tensor, mask: torch.Tensor, N: int = 2, M: int = 4,
                 bad_groups: torch.Tensor | None = None, values=None, meta=None):
+    given = (bad_groups, values, meta)
     _dev(A, mask, bad_groups, values, meta)
     R, K = A.shape
     nv, mb, _ = sizes(R, K, N, M)
@@ -218,11 +229,13 @@ def nm_compress(A: torch.Tensor, mask: torch.Tensor, N: int = 2, M: int = 4,
     _flat(values, "values"), _flat(meta, "meta")
     _check(lib().nm_compress(_dt(A), _p(A), _rows(A, "A"), _p(mask), _rows(mask, "mask"), R, K, N, M,
                              _p(values), _p(meta), _p(bad_groups), _stream()), "nm_compress")
+    _wrote(given)
     return values, meta
 
 
 def nm_prune_compress(A: torch.Tensor, N: int = 2, M: int = 4, mask=None, values=None, meta=None):
     """nm_prune and nm_compress in one call: returns (mask, values, meta)."""
+    given = (mask, values, meta)
     _dev(A, mask, values, meta)
     R, K = A.shape
     nv, mb, _ = sizes(R, K, N, M)
@@ -235,12 +248,14 @@ def nm_prune_compress(A: torch.Tensor, N: int = 2, M: int = 4, mask=None, values
     _flat(values, "values"), _flat(meta, "meta")
     _check(lib().nm_prune_compress(_dt(A), _p(A), _rows(A, "A"), R, K, N, M, _p(mask), _rows(mask, "mask"),
                                    _p(values), _p(meta), _stream()), "nm_prune_compress")
+    _wrote(given)
     return mask, values, meta
 
 
 def nm_prune_compress_transpose(A: torch.Tensor, B: torch.Tensor, N: int = 2, M: int = 4, mask=None, values=None,
                                 meta=None, Bt=None):
     """nm_prune_compress(A) and transpose(B) in one launch (bf16): returns (mask, values, meta, Bt)."""
+    given = (mask, values, meta, Bt)
     _dev(A, B, mask, values, meta, Bt)
     R, K = A.shape
     KB, Nc = B.shape
@@ -261,10 +276,12 @@ def nm_prune_compress_transpose(A: torch.Tensor, B: torch.Tensor, N: int = 2, M:
     _check(lib().nm_prune_compress_transpose(_dt(A), _p(A), _rows(A, "A"), R, K, N, M, _p(mask), _rows(mask, "mask"),
                                              _p(values), _p(meta), _p(B), _rows(B, "B"), KB, Nc, _p(Bt),
                                              _rows(Bt, "Bt"), _stream()), "nm_prune_compress_transpose")
+    _wrote(given)
     return mask, values, meta, Bt
 
 
 def nm_decompress(values: torch.Tensor, meta: torch.Tensor, K: int, N: int = 2, M: int = 4, out=None):
+    given = (out,)
     _dev(values, meta, out)
     _flat(values, "values"), _flat(meta, "meta")
     R = values.shape[0]
@@ -272,10 +289,12 @@ def nm_decompress(values: torch.Tensor, meta: torch.Tensor, K: int, N: int = 2, 
         out = torch.empty((R, K), dtype=values.dtype, device=values.device)
     _check(lib().nm_decompress(_dt(values), _p(values), _p(meta), R, K, N, M, _p(out), _rows(out, "out"),
                                _stream()), "nm_decompress")
+    _wrote(given)
     return out
 
 
 def spmm_nm(values: torch.Tensor, meta: torch.Tensor, K: int, B: torch.Tensor, out=None) -> torch.Tensor:
+    given = (out,)
     _dev(values, meta, B, out)
     _flat(values, "values"), _flat(meta, "meta")
     if B.dtype != values.dtype:
@@ -288,6 +307,7 @@ def spmm_nm(values: torch.Tensor, meta: torch.Tensor, K: int, B: torch.Tensor, o
         out = torch.empty((R, Nc), dtype=torch.float32, device=B.device)
     _check(lib().spmm_nm(_dt(B), _p(values), _p(meta), R, K, _p(B), _rows(B, "B"), Nc, _p(out),
                          _rows(out, "out"), _stream()), "spmm_nm")
+    _wrote(given)
     return out
 
 
@@ -296,6 +316,7 @@ def spmm_nm_t(values: torch.Tensor, meta: torch.Tensor, K: int, Bt: torch.Tensor
     """C = decompress(values, meta) @ Bt.T with Bt [Nc, K] (rows contiguous).  C is fp32, or bf16
     (each sum rounded to nearest even: spmm_nm_t_out_bf16) when `out` is bf16 or
     out_dtype=torch.bfloat16."""
+    given = (out,)
     _dev(values, meta, Bt, out)
     _flat(values, "values"), _flat(meta, "meta")
     if Bt.dtype != values.dtype:
@@ -309,11 +330,13 @@ def spmm_nm_t(values: torch.Tensor, meta: torch.Tensor, K: int, Bt: torch.Tensor
     if out.dtype == torch.bfloat16:
         _check(lib().spmm_nm_t_out_bf16(_dt(Bt), _p(values), _p(meta), R, K, _p(Bt), _rows(Bt, "Bt"), Nc, _p(out),
                                         _rows(out, "out"), _stream()), "spmm_nm_t_out_bf16")
+        _wrote(given)
         return out
     if out.dtype != torch.float32:
         raise TypeError("out must be fp32 or bf16")
     _check(lib().spmm_nm_t(_dt(Bt), _p(values), _p(meta), R, K, _p(Bt), _rows(Bt, "Bt"), Nc, _p(out),
                            _rows(out, "out"), _stream()), "spmm_nm_t")
+    _wrote(given)
     return out
 
 
@@ -321,6 +344,7 @@ def spmm_nm_t_lowrank(values: torch.Tensor, meta: torch.Tensor, K: int, Bt: torc
                       Vt: torch.Tensor, out=None, Tt=None):
     """A 2:4 weight plus a low-rank adapter, applied lazily: Tt = Bt @ Vt.T ([Nc, rank], fp32) and
     C = decompress(values, meta) @ Bt.T + U @ Tt.T ([R, Nc], fp32).  Returns (C, Tt)."""
+    given = (out, Tt)
     _dev(values, meta, Bt, U, Vt, out, Tt)
     _flat(values, "values"), _flat(meta, "meta")
     if not (Bt.dtype == values.dtype == U.dtype == Vt.dtype):
@@ -343,6 +367,7 @@ def spmm_nm_t_lowrank(values: torch.Tensor, meta: torch.Tensor, K: int, Bt: torc
     _check(lib().spmm_nm_t_lowrank(_dt(Bt), _p(values), _p(meta), R, K, _p(Bt), _rows(Bt, "Bt"), Nc, _p(U),
                                    _rows(U, "U"), _p(Vt), _rows(Vt, "Vt"), rank, _p(Tt), _p(out), _rows(out, "out"),
                                    _stream()), "spmm_nm_t_lowrank")
+    _wrote(given)
     return out, Tt
 
 
@@ -351,6 +376,7 @@ def spmm_nm_t_relu_venom(values: torch.Tensor, meta: torch.Tensor, K: int, Bt: t
     """The up-projection C = decompress(values, meta) @ Bt.T ([R, Nc]) with its activations
     h = ReLU(bf16(C)).T ([Nc, R]) pruned to V:N:M on the way out: returns (h_values, h_meta,
     h_colsel), as prune_act_venom(h, V, M, apply_relu=True) would."""
+    given = (h_values, h_meta, h_colsel)
     _dev(values, meta, Bt, h_values, h_meta, h_colsel)
     _flat(values, "values"), _flat(meta, "meta")
     if Bt.dtype != values.dtype:
@@ -372,6 +398,7 @@ def spmm_nm_t_relu_venom(values: torch.Tensor, meta: torch.Tensor, K: int, Bt: t
             raise ValueError(f"{name} is too small")
     _check(lib().spmm_nm_t_relu_venom(_dt(Bt), _p(values), _p(meta), R, K, _p(Bt), _rows(Bt, "Bt"), Nc, V, M,
                                       _p(h_values), _p(h_meta), _p(h_colsel), _stream()), "spmm_nm_t_relu_venom")
+    _wrote(given)
     return h_values, h_meta, h_colsel
 
 
@@ -385,6 +412,7 @@ def spmm_nm_general(values: torch.Tensor, meta: torch.Tensor, K: int, N: int, M:
     """C = decompress(values, meta) @ Bt.T for any N:M compressed matrix (fp32 C).  `work`: a uint8
     device tensor of at least general_work_bytes(...) bytes, None for none, or "auto" to allocate
     one with torch when the pattern uses it."""
+    given = (out,)
     _dev(values, meta, Bt, out)
     _flat(values, "values"), _flat(meta, "meta")
     if Bt.dtype != values.dtype:
@@ -407,6 +435,7 @@ def spmm_nm_general(values: torch.Tensor, meta: torch.Tensor, K: int, N: int, M:
                                  _rows(out, "out"), _p(work) if work is not None else None,
                                  work.numel() * work.element_size() if work is not None else 0, _stream()),
            "spmm_nm_general")
+    _wrote(given)
     return out
 
 
@@ -414,6 +443,7 @@ def spmm_nm_general_noalloc(values: torch.Tensor, meta: torch.Tensor, K: int, N:
                             out: torch.Tensor) -> torch.Tensor:
     """spmm_nm_general with the library's fixed scratch buffer instead of work memory: the call
     allocates nothing (the caller passes `out`).  Calls that overlap on one GPU race."""
+    given = (out,)
     _dev(values, meta, Bt, out)
     _flat(values, "values"), _flat(meta, "meta")
     if Bt.dtype != values.dtype:
@@ -424,6 +454,7 @@ def spmm_nm_general_noalloc(values: torch.Tensor, meta: torch.Tensor, K: int, N:
         raise ValueError("Bt must have K columns and out must be an fp32 [R, Nc] tensor")
     _check(lib().spmm_nm_general_noalloc(_dt(Bt), _p(values), _p(meta), R, K, N, M, _p(Bt), _rows(Bt, "Bt"), Nc,
                                          _p(out), _rows(out, "out"), _stream()), "spmm_nm_general_noalloc")
+    _wrote(given)
     return out
 
 
@@ -432,6 +463,7 @@ def sddmm_venom(dY: torch.Tensor, W_down: torch.Tensor, h_values: torch.Tensor, 
     """dZ [T, (F/M)*2] fp32: dY @ W_down^T at the entries the V:N:M activations h_s keep (times
     ReLU's derivative when apply_relu).  With `dYt` (a [Nc, T] bf16 tensor) the call also writes
     dY^T there and returns (out, dYt)."""
+    given = (out, dYt)
     _dev(dY, W_down, h_values, h_meta, h_colsel, out, dYt)
     _flat(h_values, "h_values"), _flat(h_meta, "h_meta"), _flat(h_colsel, "h_colsel")
     if dY.dtype != W_down.dtype or h_values.dtype != dY.dtype:
@@ -448,6 +480,7 @@ def sddmm_venom(dY: torch.Tensor, W_down: torch.Tensor, h_values: torch.Tensor, 
     _check(lib().sddmm_venom(_dt(dY), _p(dY), _rows(dY, "dY"), _p(W_down), _rows(W_down, "W_down"), T, F, Nc, V, M,
                              _p(h_values), _p(h_meta), _p(h_colsel), int(bool(apply_relu)), _p(out), _p(dYt),
                              _rows(dYt, "dYt") if dYt is not None else 0, _stream()), "sddmm_venom")
+    _wrote(given)
     return (out, dYt) if dYt is not None else out
 
 
@@ -460,6 +493,7 @@ def spmm_venom_tn(h_values: torch.Tensor, h_meta: torch.Tensor, h_colsel: torch.
                   dYt: torch.Tensor, out=None, work="auto") -> torch.Tensor:
     """dW [F, Nc] fp32 = h_s^T @ dY for V:N:M activations h_s [T, F], given dYt = dY^T [Nc, T].
     `work`: a uint8 device tensor, None, or "auto" (allocated with torch when the call uses it)."""
+    given = (out,)
     _dev(h_values, h_meta, h_colsel, dYt, out)
     _flat(h_values, "h_values"), _flat(h_meta, "h_meta"), _flat(h_colsel, "h_colsel")
     if h_values.dtype != dYt.dtype:
@@ -483,6 +517,7 @@ def spmm_venom_tn(h_values: torch.Tensor, h_meta: torch.Tensor, h_colsel: torch.
                                _p(work) if work is not None else None,
                                work.numel() * work.element_size() if work is not None else 0, _stream()),
            "spmm_venom_tn")
+    _wrote(given)
     return out
 
 
@@ -493,6 +528,7 @@ def general_scratch_bytes() -> int:
 
 def transpose(X: torch.Tensor, out=None) -> torch.Tensor:
     """out[c, r] = X[r, c] (bf16), e.g. B [K, Nc] -> Bt [Nc, K] for spmm_nm_t."""
+    given = (out,)
     _dev(X, out)
     R, C = X.shape
     if out is None:
@@ -501,11 +537,13 @@ def transpose(X: torch.Tensor, out=None) -> torch.Tensor:
         raise ValueError("out must be [C, R] with X's dtype")
     _check(lib().nm_transpose(_dt(X), _p(X), _rows(X, "X"), R, C, _p(out), _rows(out, "out"), _stream()),
            "nm_transpose")
+    _wrote(given)
     return out
 
 
 def prune_act_venom(Z: torch.Tensor, V: int, M: int = 8, apply_relu: bool = False, want_mask: bool = False,
                     values=None, meta=None, colsel=None, mask=None):
+    given = (values, meta, colsel, mask)
     _dev(Z, values, meta, colsel, mask)
     R, K = Z.shape
     nv, mb, cb = sizes(R, K, 2, M, V)
@@ -521,11 +559,13 @@ def prune_act_venom(Z: torch.Tensor, V: int, M: int = 8, apply_relu: bool = Fals
     ldm = _rows(mask, "mask") if mask is not None else 0
     _check(lib().prune_act_venom(_dt(Z), _p(Z), _rows(Z, "Z"), R, K, V, M, int(bool(apply_relu)), _p(values),
                                  _p(meta), _p(colsel), _p(mask), ldm, _stream()), "prune_act_venom")
+    _wrote(given)
     return (values, meta, colsel, mask) if mask is not None else (values, meta, colsel)
 
 
 def spmm_venom(values: torch.Tensor, meta: torch.Tensor, colsel: torch.Tensor, K: int, V: int, M: int,
                B: torch.Tensor, out=None) -> torch.Tensor:
+    given = (out,)
     _dev(values, meta, colsel, B, out)
     _flat(values, "values"), _flat(meta, "meta"), _flat(colsel, "colsel")
     if B.dtype != values.dtype:
@@ -538,10 +578,12 @@ def spmm_venom(values: torch.Tensor, meta: torch.Tensor, colsel: torch.Tensor, K
         out = torch.empty((R, Nc), dtype=torch.float32, device=B.device)
     _check(lib().spmm_venom(_dt(B), _p(values), _p(meta), _p(colsel), R, K, V, M, _p(B), _rows(B, "B"), Nc,
                             _p(out), _rows(out, "out"), _stream()), "spmm_venom")
+    _wrote(given)
     return out
 
 
 def nm_reprune_t(values: torch.Tensor, meta: torch.Tensor, R: int, K: int, values_t=None, meta_t=None):
+    given = (values_t, meta_t)
     _dev(values, meta, values_t, meta_t)
     _flat(values, "values"), _flat(meta, "meta")
     if values_t is None:
@@ -550,6 +592,7 @@ def nm_reprune_t(values: torch.Tensor, meta: torch.Tensor, R: int, K: int, value
         meta_t = torch.empty((K, (R + 7) // 8), dtype=torch.uint8, device=values.device)
     _check(lib().nm_reprune_t(_dt(values), _p(values), _p(meta), R, K, _p(values_t), _p(meta_t), _stream()),
            "nm_reprune_t")
+    _wrote(given)
     return values_t, meta_t
 
 
@@ -557,6 +600,7 @@ def nm_reprune_t_transpose(values: torch.Tensor, meta: torch.Tensor, R: int, K: 
                            values_t=None, meta_t=None, Xt=None):
     """nm_reprune_t of (values, meta) and transpose of X (bf16) in one launch; returns
     (values_t, meta_t, Xt)."""
+    given = (values_t, meta_t, Xt)
     _dev(values, meta, values_t, meta_t, X, Xt)
     _flat(values, "values"), _flat(meta, "meta")
     if values_t is None:
@@ -571,6 +615,7 @@ def nm_reprune_t_transpose(values: torch.Tensor, meta: torch.Tensor, R: int, K: 
     _check(lib().nm_reprune_t_transpose(_dt(values), _p(values), _p(meta), R, K, _p(values_t), _p(meta_t), _p(X),
                                         _rows(X, "X"), RX, CX, _p(Xt), _rows(Xt, "Xt"), _stream()),
            "nm_reprune_t_transpose")
+    _wrote(given)
     return values_t, meta_t, Xt
 
 
@@ -578,18 +623,21 @@ def mfma_rate_probe(kind: int, iters: int, sink: torch.Tensor) -> int:
     """Launch the matrix-rate probe (kind 0 dense bf16 MFMA, 1 2:4 SMFMAC) on the current stream;
     returns the dense-equivalent flops of the launch.  `sink` is an fp32 CUDA tensor of at least
     512 * 256 elements."""
+    given = (sink,)
     _dev(sink)
     if sink.dtype != torch.float32 or sink.numel() < 512 * 256:
         raise ValueError("sink must be an fp32 tensor of at least 131072 elements")
     flops = _i64(0)
     _check(lib().nm_mfma_rate_probe(int(kind), int(iters), _p(sink), ctypes.byref(flops), _stream()),
            "nm_mfma_rate_probe")
+    _wrote(given)
     return flops.value
 
 
 def nm_to_panels(values: torch.Tensor, meta: torch.Tensor, R: int, K: int, values_p=None, meta_p=None):
     """The panel layout (for spmm_nm_t_panels) of a bf16 2:4 form given row-major; returns
     (values_p, meta_p), flat buffers of the row-major sizes."""
+    given = (values_p, meta_p)
     _dev(values, meta, values_p, meta_p)
     _flat(values, "values"), _flat(meta, "meta")
     if values_p is None:
@@ -598,6 +646,7 @@ def nm_to_panels(values: torch.Tensor, meta: torch.Tensor, R: int, K: int, value
         meta_p = torch.empty((R * K // 8,), dtype=torch.uint8, device=values.device)
     _check(lib().nm_to_panels(_dt(values), _p(values), _p(meta), R, K, _p(values_p), _p(meta_p), _stream()),
            "nm_to_panels")
+    _wrote(given)
     return values_p, meta_p
 
 
@@ -605,6 +654,7 @@ def nm_reprune_t_transpose_panels(values: torch.Tensor, meta: torch.Tensor, R: i
                                   values_t=None, meta_t=None, Xt=None):
     """nm_reprune_t_transpose with the re-pruned transpose (K x R, compressed along R) in the panel
     layout; returns (values_t, meta_t, Xt), values_t and meta_t flat."""
+    given = (values_t, meta_t, Xt)
     _dev(values, meta, values_t, meta_t, X, Xt)
     _flat(values, "values"), _flat(meta, "meta")
     if values_t is None:
@@ -619,11 +669,13 @@ def nm_reprune_t_transpose_panels(values: torch.Tensor, meta: torch.Tensor, R: i
     _check(lib().nm_reprune_t_transpose_panels(_dt(values), _p(values), _p(meta), R, K, _p(values_t), _p(meta_t),
                                                _p(X), _rows(X, "X"), RX, CX, _p(Xt), _rows(Xt, "Xt"), _stream()),
            "nm_reprune_t_transpose_panels")
+    _wrote(given)
     return values_t, meta_t, Xt
 
 
 def spmm_nm_t_panels(values: torch.Tensor, meta: torch.Tensor, R: int, K: int, Bt: torch.Tensor, out=None):
     """spmm_nm_t of an R x K bf16 2:4 weight in the panel layout: C [R, Nc] fp32."""
+    given = (out,)
     _dev(values, meta, Bt, out)
     _flat(values, "values"), _flat(meta, "meta")
     Nc = Bt.shape[0]
@@ -631,12 +683,14 @@ def spmm_nm_t_panels(values: torch.Tensor, meta: torch.Tensor, R: int, K: int, B
         out = torch.empty((R, Nc), dtype=torch.float32, device=Bt.device)
     _check(lib().spmm_nm_t_panels(_dt(Bt), _p(values), _p(meta), R, K, _p(Bt), _rows(Bt, "Bt"), Nc, _p(out),
                                   _rows(out, "out"), _stream()), "spmm_nm_t_panels")
+    _wrote(given)
     return out
 
 
 def sddmm_nm(D: torch.Tensor, X: torch.Tensor, meta: torch.Tensor, out=None, Dt=None):
     """dW values of a 2:4 layer; with `Dt` (a [T, R] tensor, bf16) the call is sddmm_nm_dt, which also
     writes Dt = D^T, and returns (out, Dt)."""
+    given = (out, Dt)
     _dev(D, X, meta, out, Dt)
     _flat(meta, "meta")
     if D.dtype != X.dtype:
@@ -653,9 +707,11 @@ def sddmm_nm(D: torch.Tensor, X: torch.Tensor, meta: torch.Tensor, out=None, Dt=
             raise ValueError("Dt must be [T, R] with D's dtype")
         _check(lib().sddmm_nm_dt(_dt(D), _p(D), _rows(D, "D"), _p(X), _rows(X, "X"), R, Kc, T, _p(meta), _p(out),
                                  _p(Dt), _rows(Dt, "Dt"), _stream()), "sddmm_nm_dt")
+        _wrote(given)
         return out, Dt
     _check(lib().sddmm_nm(_dt(D), _p(D), _rows(D, "D"), _p(X), _rows(X, "X"), R, Kc, T, _p(meta), _p(out),
                           _stream()), "sddmm_nm")
+    _wrote(given)
     return out
 
 
@@ -706,6 +762,7 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, g
     int32, weights [T, k] fp32).  Experts are taken by softmax or sigmoid score plus `bias` [E] (which
     has no part in the weights), from the topk_groups best of `groups` runs of experts; -1 and weight 0
     where fewer than k experts have a logit above -infinity."""
+    given = (ids, weights)
     _dev(logits, bias, ids, weights)
     ldl = _ld(logits, "logits")
     T, E = logits.shape
@@ -721,12 +778,14 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, g
         _of(weights, (T, k), torch.float32, "weights")
     _check(lib().moe_route(_dt(logits), _p(logits), ldl, T, E, _score(score), _p(bias), groups, topk_groups, group_top,
                            k, int(bool(renorm)), scale, _p(ids), _p(weights), _stream()), "moe_route")
+    _wrote(given)
     return ids, weights
 
 
 def moe_route_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, dweights: torch.Tensor,
                   score: str = "softmax", renorm: bool = True, scale: float = 1.0, dlogits=None) -> torch.Tensor:
     """The gradient [T, E] of moe_route's weights with respect to the logits, in the logits' dtype."""
+    given = (dlogits,)
     _dev(logits, ids, weights, dweights, dlogits)
     ldl = _ld(logits, "logits")
     T, E = logits.shape
@@ -742,6 +801,7 @@ def moe_route_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     _check(lib().moe_route_bwd(_dt(logits), _p(logits), ldl, T, E, _score(score), k, int(bool(renorm)), scale, _p(ids),
                                _p(weights), _p(dweights), _p(dlogits), _ld(dlogits, "dlogits"), _stream()),
            "moe_route_bwd")
+    _wrote(given)
     return dlogits
 
 
@@ -761,6 +821,7 @@ def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=Non
     """The order of the T * k slots by expert: returns (offsets [E + 1], counts [E], src [rows], pos
     [T, k]), int32, parts of one allocation when none is given.  `work`: an int32 device tensor, or "auto"
     (allocated with torch when the call uses it)."""
+    given = (offsets, counts, src, pos)
     _dev(ids, offsets, counts, src, pos)
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
@@ -788,6 +849,7 @@ def moe_plan(ids: torch.Tensor, E: int, align: int = 1, offsets=None, counts=Non
         _flat(work, "work")
     _check(lib().moe_plan(_p(ids), T, k, E, align, _p(offsets), _p(counts), _p(src), src.numel(), _p(pos), _p(work),
                           work.numel() * work.element_size() if work is not None else 0, _stream()), "moe_plan")
+    _wrote(given)
     return offsets, counts, src, pos
 
 
@@ -809,6 +871,7 @@ def fp8_quantize(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=No
     """X [rows, K] (or its rows src // div, 0 where src is negative; 0 where gate is not > 0) in 8 bits
     with a power-of-two scale per row and 128 columns: returns (Q [rows, Kp], S [Kp / 128, rows]), Kp = K
     rounded up to 128, the columns beyond K 0."""
+    given = (Q, S)
     ldx, RX, R, K, ldg = _quantize_args(X, src, gate)
     _dev(Q, S)
     Kp = _up(K, 128)
@@ -820,6 +883,7 @@ def fp8_quantize(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=No
         raise ValueError("Q must be [rows, Kp] and S an fp32 [Kp / 128, rows] tensor")
     _check(lib().fp8_quantize(_dt(X), _p(X), ldx, RX, _p(src), div, _p(gate), ldg, R, K, _fp8(Q, "Q"), _p(Q),
                               _ld(Q, "Q"), _p(S), _ld(S, "S"), _stream()), "fp8_quantize")
+    _wrote(given)
     return Q, S
 
 
@@ -827,6 +891,7 @@ def fp8_quantize_t(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=
                    S=None):
     """fp8_quantize's input transposed, with a scale per column of X and 128 rows: returns (Q [K, Rp],
     S [Rp / 128, K]), Rp = the rows rounded up to 128, the columns beyond them 0."""
+    given = (Q, S)
     ldx, RX, R, K, ldg = _quantize_args(X, src, gate)
     _dev(Q, S)
     Rp = _up(R, 128)
@@ -838,6 +903,7 @@ def fp8_quantize_t(X: torch.Tensor, fmt: torch.dtype = torch.float8_e4m3fn, src=
         raise ValueError("Q must be [K, Rp] and S an fp32 [Rp / 128, K] tensor")
     _check(lib().fp8_quantize_t(_dt(X), _p(X), ldx, RX, _p(src), div, _p(gate), ldg, R, K, _fp8(Q, "Q"), _p(Q),
                                 _ld(Q, "Q"), _p(S), _ld(S, "S"), _stream()), "fp8_quantize_t")
+    _wrote(given)
     return Q, S
 
 
@@ -885,6 +951,7 @@ def fp8_gemm_nt(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Te
     """C = (A with its scales) @ (B with its scales).T for 8-bit A [M, K] and B [N, K]: sa [K / 128, M] per
     row and 128-block of A; sb [N / 128, K / 128] per 128 x 128 block of B (b_block 128) or [K / 128, N] per
     row (b_block 1).  C is bf16 or fp32."""
+    given = (out,)
     _dev(A, sa, B, sb, out)
     M, K = A.shape
     if B.dim() != 2 or B.shape[1] != K:
@@ -899,6 +966,7 @@ def fp8_gemm_nt(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Te
     _check(lib().fp8_gemm_nt(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), ldsa, _fp8(B, "B"), _p(B), _ld(B, "B"),
                              _p(sb), ldsb, b_block, M, N, K, _dt(out), _p(out), _ld(out, "out"), _stream()),
            "fp8_gemm_nt")
+    _wrote(given)
     return out
 
 
@@ -906,6 +974,7 @@ def fp8_gemm_nt_grouped(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: 
                         out_dtype: torch.dtype = torch.bfloat16, out=None) -> torch.Tensor:
     """Rows offsets[e] .. offsets[e + 1] - 1 of A [rows, K] times expert e's B [E, N, K] transposed, with
     sa [K / 128, rows] and sb [E, N / 128, K / 128]: C [rows, N], 0 in the rows of no expert."""
+    given = (out,)
     _dev(A, sa, B, sb, offsets, out)
     rows, K = A.shape
     if B.dim() != 3 or B.shape[2] != K:
@@ -920,6 +989,7 @@ def fp8_gemm_nt_grouped(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: 
     _check(lib().fp8_gemm_nt_grouped(_fp8(A, "A"), _p(A), _ld(A, "A"), _p(sa), _scales(sa, (Kb, rows), "sa"),
                                      _fp8(B, "B"), _p(B), ldb, _p(sb), Kb, _p(offsets), E, rows, N, K, _dt(out), _p(out),
                                      _ld(out, "out"), _stream()), "fp8_gemm_nt_grouped")
+    _wrote(given)
     return out
 
 
@@ -928,6 +998,7 @@ def fp8_gemm_nt_grouped_k(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb
     """For every expert, columns offsets[e] .. offsets[e + 1] - 1 of A [M, rows] times those of B [N, rows]
     transposed, with sa [rows / 128, M] and sb [rows / 128, N]: C [E, M, N].  The offsets are multiples of
     128 (moe_plan with align 128)."""
+    given = (out,)
     _dev(A, sa, B, sb, offsets, out)
     M, rows = A.shape
     if B.dim() != 2 or B.shape[1] != rows:
@@ -944,11 +1015,13 @@ def fp8_gemm_nt_grouped_k(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb
                                        _fp8(B, "B"), _p(B), _ld(B, "B"), _p(sb), _scales(sb, (Rb, N), "sb"),
                                        _p(offsets), E, M, N, rows, _dt(out), _p(out), N, _stream()),
            "fp8_gemm_nt_grouped_k")
+    _wrote(given)
     return out
 
 
 def moe_combine(O: torch.Tensor, pos: torch.Tensor, weights=None, out=None) -> torch.Tensor:
     """Y [T, D]: the sum over j of weights[t, j] times row pos[t, j] of O [rows, D] (weights None: 1)."""
+    given = (out,)
     _dev(O, pos, weights, out)
     rows, D = O.shape
     if pos.dim() != 2:
@@ -963,12 +1036,14 @@ def moe_combine(O: torch.Tensor, pos: torch.Tensor, weights=None, out=None) -> t
         raise ValueError("out must be [T, D] with O's dtype")
     _check(lib().moe_combine(_dt(O), _p(O), _ld(O, "O"), rows, _p(pos), _p(weights), T, k, D, _p(out),
                              _ld(out, "out"), _stream()), "moe_combine")
+    _wrote(given)
     return out
 
 
 def moe_combine_bwd(dY: torch.Tensor, O: torch.Tensor, src: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
                     dO=None, dweights=None):
     """The gradients of moe_combine: (dO [rows, D] in O's dtype, 0 in the rows of no slot; dweights [T, k])."""
+    given = (dO, dweights)
     _dev(dY, O, src, pos, weights, dO, dweights)
     rows, D = O.shape
     if pos.dim() != 2:
@@ -989,6 +1064,7 @@ def moe_combine_bwd(dY: torch.Tensor, O: torch.Tensor, src: torch.Tensor, pos: t
     _check(lib().moe_combine_bwd(_dt(O), _p(dY), _ld(dY, "dY"), _p(O), _ld(O, "O"), rows, _p(src), _p(pos),
                                  _p(weights), T, k, D, _p(dO), _ld(dO, "dO"), _p(dweights), _stream()),
            "moe_combine_bwd")
+    _wrote(given)
     return dO, dweights
 
 
@@ -1079,10 +1155,12 @@ def rms_norm(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=None,
     """h = X [T, D] + residual, Y = h / sqrt(mean(h^2) + eps) * w: returns (Y, H, rstd), H the rounded sum
     (without a residual X itself, unless H is given or Y is X) and rstd [T] fp32, what rms_norm_bwd reads.  In place:
     H may be X or the residual, Y may be X."""
+    given = (H, Y, rstd)
     T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Y)
     Y, ldy = _new_or(Y, (T, D), X.dtype, X, "Y")
     _check(lib().rms_norm(_dt(X), _p(X), ldx, _p(residual), ldr, _dt(w), _p(w), eps, T, D, _p(H), ldh, _p(Y), ldy,
                           _p(rstd), _stream()), "rms_norm")
+    _wrote(given)
     return Y, X if H is None else H, rstd
 
 
@@ -1091,6 +1169,7 @@ def rms_norm_fp8(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=N
     """rms_norm with its result in 8 bits and a power-of-two scale per row and 128 columns, as fp8_gemm_nt takes it:
     returns (Q [T, Dp], S [Dp / 128, T], H, rstd), Dp = D rounded up to 128, the columns beyond D 0.  With a tensor Y
     [T, D] the result is stored there in X's dtype too."""
+    given = (H, Q, S, Y, rstd)
     T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Y, Q, S)
     Dp = _up(D, 128)
     if Q is None:
@@ -1100,6 +1179,7 @@ def rms_norm_fp8(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=N
     ldy = _opt(Y, (T, D), X.dtype, "Y")
     _check(lib().rms_norm_fp8(_dt(X), _p(X), ldx, _p(residual), ldr, _dt(w), _p(w), eps, T, D, _fp8(Q, "Q"), _p(Q),
                               ldq, _p(S), lds, _p(H), ldh, _p(Y), ldy, _p(rstd), _stream()), "rms_norm_fp8")
+    _wrote(given)
     return Q, S, X if H is None else H, rstd
 
 
@@ -1114,6 +1194,7 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, w: torch.Tensor, rstd: torch
                  work="auto"):
     """The gradients of rms_norm at its stored H and rstd: (dX [T, D], the gradient of X and of the residual; dw [D]
     fp32).  `dH` is the gradient that reaches H by other ways (through the residual); dX may be dY or dH."""
+    given = (dX, dw)
     T, D = _two(H, "H")
     _here(dY, H, w, rstd, dH, dX, dw)
     if w.shape != (D,) or not w.is_contiguous():
@@ -1126,6 +1207,7 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, w: torch.Tensor, rstd: torch
     work, nbytes = _workspace(work, _norm_work_bytes(T, D), H)
     _check(lib().rms_norm_bwd(_dt(H), _p(dY), lddy, _p(H), ldh, _dt(w), _p(w), _p(rstd), _p(dH), lddh, T, D, _p(dX),
                               lddx, _p(dw), _p(work), nbytes, _stream()), "rms_norm_bwd")
+    _wrote(given)
     return dX, dw
 
 
@@ -1147,6 +1229,7 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
     """Y = act(X [M, K] @ W [N, K].T + bias) + residual, bf16 operands and fp32 sums; act is 'none', 'relu',
     'gelu_tanh' or 'silu'.  With `pre` (a tensor) or `return_pre` returns (Y, pre), pre [M, N] bf16 the sum before the
     activation, what linear_bwd_act and linear_bwd_x read.  In place: out may be the residual."""
+    given = (out, pre)
     M, K = _two(X, "X")
     N = _two(W, "W")[0]
     _here(X, W, bias, residual, out, pre)
@@ -1162,6 +1245,7 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
     _check(lib().linear_fwd(_dt(X), _p(X), ldx, _p(W), ldw, NM_BF16 if bias is None else _dt(bias), _p(bias), _act(act),
                             _p(residual), ldr, M, N, K, _dt(out), _p(out), ldy, _p(pre), ldp, _p(work), nbytes, _stream()),
            "linear_fwd")
+    _wrote(given)
     return out if pre is None else (out, pre)
 
 
@@ -1176,6 +1260,7 @@ def linear_bwd_act(dY: torch.Tensor, pre=None, act: str = "none", dZ=None, db=No
     """The gradients of an activation and of the bias in front of it: (dZ = dY act'(pre) [M, N], db [N] fp32, the sums
     of dZ's columns before its rounding).  With act 'none' dZ is dY itself, unless a tensor dZ is given.  dZ may be dY
     or pre."""
+    given = (dZ, db)
     M, N = _two(dY, "dY")
     _here(dY, pre, dZ, db)
     lddy = _ld(dY, "dY")
@@ -1190,6 +1275,7 @@ def linear_bwd_act(dY: torch.Tensor, pre=None, act: str = "none", dZ=None, db=No
     work, nbytes = _workspace(work, _act_work_bytes(M, N), dY)
     _check(lib().linear_bwd_act(_dt(dY), _p(dY), lddy, _p(pre), ldp, a, M, N, _p(dZ), lddz, _p(db), _p(work), nbytes,
                                 _stream()), "linear_bwd_act")
+    _wrote(given)
     return dY if dZ is None else dZ, db
 
 
@@ -1198,6 +1284,7 @@ def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
     """dX = (dZ [M, N] @ W [N, K]) act'(pre): the gradient of linear_fwd's input, and with `act` of the
     pre-activations [M, K] that the input came from (with 'relu' the input itself does as well).  In place: out may
     be pre."""
+    given = (out,)
     M, N = _two(dZ, "dZ")
     K = _two(W, "W")[1]
     _here(dZ, W, pre, out)
@@ -1209,6 +1296,7 @@ def linear_bwd_x(dZ: torch.Tensor, W: torch.Tensor, pre=None, act: str = "none",
     work, nbytes = _linear_work(work, NM_LINEAR_BWD_X, M, N, K, dZ, lddz, W, ldw)
     _check(lib().linear_bwd_x(_dt(dZ), _p(dZ), lddz, _p(W), ldw, _p(pre), ldp, _act(act), M, N, K, _dt(out), _p(out),
                               lddx, _p(work), nbytes, _stream()), "linear_bwd_x")
+    _wrote(given)
     return out
 
 
@@ -1216,6 +1304,7 @@ def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = tor
                  accumulate: bool = False, work="auto") -> torch.Tensor:
     """dW [N, K] = dZ [M, N].T @ X [M, K], the gradient of linear_fwd's weight; with `accumulate` added to `out`
     (fp32), as micro-batches do."""
+    given = (out,)
     M, N = _two(dZ, "dZ")
     K = _two(X, "X")[1]
     _here(dZ, X, out)
@@ -1226,6 +1315,7 @@ def linear_bwd_w(dZ: torch.Tensor, X: torch.Tensor, out_dtype: torch.dtype = tor
     work, nbytes = _linear_work(work, NM_LINEAR_BWD_W, M, N, K, dZ, lddz, X, ldx)
     _check(lib().linear_bwd_w(_dt(dZ), _p(dZ), lddz, _p(X), ldx, M, N, K, int(bool(accumulate)), _dt(out), _p(out),
                               lddw, _p(work), nbytes, _stream()), "linear_bwd_w")
+    _wrote(given)
     return out
 
 
@@ -1279,12 +1369,14 @@ def _grads_work(work, n, counts, like):
 
 def grad_norm(grads, norm=None, work="auto") -> torch.Tensor:
     """The norm of all tensors together (bf16 and fp32, any shapes, each packed in memory): one fp32 value [1]."""
+    given = (norm,)
     grads = list(grads)
     dt, ptr, counts, _ = _grads_args(grads, "grads")
     _here(norm)
     norm = _new_vector(norm, 1, grads[0], "norm")
     work, nbytes = _grads_work(work, len(grads), counts, grads[0])
     _check(lib().grad_norm(len(grads), dt, ptr, counts, _p(norm), _p(work), nbytes, _stream()), "grad_norm")
+    _wrote(given)
     return norm
 
 
@@ -1316,4 +1408,5 @@ def grad_clip(grads, max_norm: float, norm=None, out=None, work="auto") -> torch
         work, nbytes = _grads_work(work, len(grads), counts, grads[0])
     _check(lib().grad_clip(len(grads), dt, ptr, counts, float(max_norm), int(have), _p(norm), odt, optr, _p(work), nbytes,
                            _stream()), "grad_clip")
+    _wrote(grads if out is None else out)
     return norm

@@ -41,3 +41,18 @@ def test_a_norm_in_place_returns_the_sum_that_its_gradient_reads(T, D, dtype):
     x, h = X.clone(), torch.empty_like(X)
     assert nm.rms_norm(x, w, Y=x, H=h)[1] is h and torch.equal(h, X)
     assert nm.rms_norm(X, w)[1] is X and nm.rms_norm(X, w, Y=torch.empty_like(X))[1] is X
+
+
+def test_a_pass_whose_input_the_library_overwrote_is_refused():
+    x, dy = _rand(0, 40, 64), _rand(1, 40, 64)
+    layer = nm.DenseFFN(1 + 0.1 * _rand(2, 64), _rand(3, 96, 64), _rand(4, 64, 96), train=True)
+    _, first = layer.forward(x, return_saved=True)
+    _, second = layer.forward(x, return_saved=True)
+    dx, _ = layer.backward(dy, first)
+    nm.rms_norm(_rand(5, 40, 64), _rand(6, 64), residual=x, H=x)
+    with pytest.raises(RuntimeError):
+        layer.backward(dy, second)
+    _, third = layer.forward(x, return_saved=True)
+    nm.grad_clip([layer.W_up], 0.5)                   # a parameter
+    with pytest.raises(RuntimeError):
+        layer.backward(dy, third)

@@ -747,8 +747,11 @@ nm_status moe_combine_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void*
  *
  * An output of these calls may be one of the call's own inputs, at the same
  * address with the same row stride and type, where that is stated; no other
- * overlap is allowed.  Work memory holds nothing between calls, but calls that
- * may run at the same time need their own.
+ * overlap is allowed: a call whose outputs and work memory share a byte with
+ * each other or with an input matrix returns NM_ERR_SHAPE (the input vectors w,
+ * bias and rstd are not looked at).  Columns of one buffer do not overlap.
+ * Work memory holds nothing between calls, but calls that may run at the same
+ * time need their own.
  * ---------------------------------------------------------------------------
  */
 
@@ -762,8 +765,8 @@ typedef enum { NM_ACT_NONE = 0, NM_ACT_RELU = 1, NM_ACT_GELU_TANH = 2, NM_ACT_SI
  *   X, residual, Y [T][..] dtype dt, w [D] dtype wdt, rstd fp32 [T] (NULL: not stored)
  *   H [T][ldh] dtype dt: h rounded, the next block's residual (NULL: not stored)
  * Sums and products are fp32 and taken from h before its rounding; every output is rounded once.
- * H may be X or the residual, Y may be X.  Squares are fp32: rows beyond 1e19 overflow.  0 < eps, finite, and
- * D <= 16384 (NM_ERR_UNSUPPORTED).
+ * H and Y may each be X or the residual, but not the same one.  Squares are fp32: rows beyond 1e19 overflow.
+ * 0 < eps, finite, and D <= 16384 (NM_ERR_UNSUPPORTED).
  */
 nm_status rms_norm(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
                    const void* w, float eps, int64_t T, int64_t D, void* H, int64_t ldh, void* Y, int64_t ldy,
@@ -789,7 +792,7 @@ nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* resi
  *   residual's; NULL: none), dX [T][..] dtype dt; w [D] dtype wdt; rstd fp32 [T]; dw fp32 [D]
  *   work  device memory, 4-byte aligned, of rms_norm_bwd_work_bytes bytes (NULL when that is 0;
  *         NM_ERR_SHAPE when work_bytes is less)
- * dX is the gradient of X and of the residual.  It may be dY or dH.  Sums are fp32; dw's are added in an order that
+ * dX is the gradient of X and of the residual.  It may be dY, dH or H.  Sums are fp32; dw's are added in an order that
  * depends on T and D alone.  D <= 16384 (NM_ERR_UNSUPPORTED).
  */
 nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H, int64_t ldh, nm_dtype wdt,

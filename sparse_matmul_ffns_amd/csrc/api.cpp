@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <new>
+#include <utility>
 
 #include "../../include/nmsparse.h"
 #include "launch.hpp"
@@ -64,21 +65,75 @@ nm_status fp8_gemm_check(nm_fp8 fa, const void* A, int64_t lda, const void* sa, 
 bool act_ok(nm_act a) { return a >= NM_ACT_NONE && a <= NM_ACT_SILU; }
 // A number of rows and a width that an int holds.
 bool rows_ok(int64_t R, int64_t C) { return R > 0 && C > 0 && R <= INT32_MAX && C <= INT32_MAX; }
-bool same(const void* a, int64_t lda, const void* b, int64_t ldb) { return a == b && lda == ldb; }
+
+// The bytes of a matrix: rows of `width` bytes, `stride` apart; an empty one where p is null.
+struct Area {
+  uintptr_t lo, hi;   // hi: behind the last byte
+  int64_t rows;
+  uintptr_t width, stride;
+};
+Area area(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+  if (!p || rows <= 0 || cols <= 0) return Area{0, 0, 0, 0, 0};
+  const uintptr_t lo = (uintptr_t)p, width = (uintptr_t)(cols * es);
+  if (rows == 1 || ld == cols) {   // one run of bytes
+    const uintptr_t all = (uintptr_t)rows * width, hi = lo + all < lo ? UINTPTR_MAX : lo + all;
+    return Area{lo, hi, 1, hi - lo, hi - lo};
+  }
+  const unsigned __int128 end = (unsigned __int128)(rows - 1) * ((uintptr_t)ld * (uintptr_t)es) + width + lo;
+  return Area{lo, end > UINTPTR_MAX ? UINTPTR_MAX : (uintptr_t)end, rows, width, (uintptr_t)ld * (uintptr_t)es};
+}
+bool same(const Area& a, const Area& b) {
+  return a.lo == b.lo && a.rows == b.rows && a.width == b.width && a.stride == b.stride;
+}
+// Whether two matrices share a byte: exactly, since columns of one buffer interleave without meeting.
+bool meet(Area a, Area b) {
+  if (a.lo >= b.hi || b.lo >= a.hi) return false;
+  if (a.stride == b.stride && a.rows > 1 && b.rows > 1) {
+    if (a.lo > b.lo) std::swap(a, b);
+    const uintptr_t r = (b.lo - a.lo) / a.stride, off = (b.lo - a.lo) % a.stride;   // b's first row begins behind a's row r
+    return (r < (uintptr_t)a.rows && off < a.width) || (r + 1 < (uintptr_t)a.rows && off + b.width > a.stride);
+  }
+  if (a.rows > b.rows) std::swap(a, b);
+  // every row of the one that has fewer (one, unless both have gaps and other strides) against the first of b's rows that ends behind its start
+  for (int64_t i = 0; i < a.rows; ++i) {
+    const uintptr_t lo = a.lo + (uintptr_t)i * a.stride;
+    if (lo >= b.hi) return false;
+    const uintptr_t k = lo < b.lo + b.width ? 0 : (lo - b.lo - b.width) / b.stride + 1;
+    if (k < (uintptr_t)b.rows && b.lo + k * b.stride < lo + a.width) return true;
+  }
+  return false;
+}
+// Whether an output meets another output or an input.  in_place: bit j of entry i where output i may be input j itself.
+template <size_t NO, size_t NI>
+bool overlap(const Area (&out)[NO], const Area (&in)[NI], const unsigned (&in_place)[NO]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+    for (size_t j = 0; j < NI; ++j)
+      if (meet(out[i], in[j]) && !(in_place[i] >> j & 1 && same(out[i], in[j]))) return true;
+  }
+  return false;
+}
 constexpr int64_t kNormWidth = 16384;   // a row stays in the registers of a workgroup
 
 // the checks rms_norm and rms_norm_fp8 share
 nm_status norm_check(nm_dtype dt, const void* X, int64_t ldx, const void* residual, int64_t ldr, nm_dtype wdt,
                      const void* w, float eps, int64_t T, int64_t D, const void* H, int64_t ldh, const void* Y,
-                     int64_t ldy, const float* rstd) {
+                     int64_t ldy, const float* rstd, const void* Q = nullptr, int64_t ldq = 0, const float* S = nullptr,
+                     int64_t lds = 0) {
   if (!X || !w) return NM_ERR_NULL;
   if (!dtype_ok(dt) || !dtype_ok(wdt) || !(eps > 0.f) || eps - eps != 0.f) return NM_ERR_UNSUPPORTED;
   if (!rows_ok(T, D) || ldx < D || (residual && ldr < D) || (H && ldh < D) || (Y && ldy < D)) return NM_ERR_SHAPE;
   if (D > kNormWidth) return NM_ERR_UNSUPPORTED;
+  if (Q && (ldq < up128(D) || lds < T)) return NM_ERR_SHAPE;
   if (!aligned(X, esize(dt)) || !aligned(residual, esize(dt)) || !aligned(w, esize(wdt)) || !aligned(H, esize(dt)) ||
-      !aligned(Y, esize(dt)) || !aligned(rstd, 4))
+      !aligned(Y, esize(dt)) || !aligned(rstd, 4) || !aligned(S, 4))
     return NM_ERR_ALIGN;
-  return NM_OK;
+  const int64_t e = esize(dt), Dp = up128(D);
+  const Area out[] = {area(H, T, D, ldh, e), area(Y, T, D, ldy, e), area(rstd, 1, T, T, 4), area(Q, T, Dp, ldq, 1),
+                      area(S, Dp / 128, T, lds, 4)};
+  const Area in[] = {area(X, T, D, ldx, e), area(residual, T, D, ldr, e)};
+  return overlap(out, in, {3, 3, 0, 0, 0}) ? NM_ERR_SHAPE : NM_OK;
 }
 
 // A contiguous range of device memory that a call over many tensors reads, or writes (out).
@@ -595,10 +650,8 @@ nm_status rms_norm_fp8(nm_dtype dt, const void* X, int64_t ldx, const void* resi
                        int64_t lds, void* H, int64_t ldh, void* Y, int64_t ldy, float* rstd, nm_stream stream) {
   if (!Q || !S) return NM_ERR_NULL;
   if (!fp8_ok(fmt)) return NM_ERR_UNSUPPORTED;
-  const nm_status st = norm_check(dt, X, ldx, residual, ldr, wdt, w, eps, T, D, H, ldh, Y, ldy, rstd);
+  const nm_status st = norm_check(dt, X, ldx, residual, ldr, wdt, w, eps, T, D, H, ldh, Y, ldy, rstd, Q, ldq, S, lds);
   if (st != NM_OK) return st;
-  if (ldq < up128(D) || lds < T) return NM_ERR_SHAPE;
-  if (!aligned(S, 4)) return NM_ERR_ALIGN;
   const nms::NormArgs a{X, ldx, residual, ldr, w, wdt == NM_BF16, eps, T, D, H, ldh, Y, ldy, rstd, Q, ldq, S, lds, fmt == NM_E5M2};
   return hip_status(nms::launch_rms_norm(dt, a, hs(stream)));
 }
@@ -626,6 +679,10 @@ nm_status rms_norm_bwd(nm_dtype dt, const void* dY, int64_t lddy, const void* H,
   if (!aligned(dY, esize(dt)) || !aligned(H, esize(dt)) || !aligned(w, esize(wdt)) || !aligned(rstd, 4) ||
       !aligned(dH, esize(dt)) || !aligned(dX, esize(dt)) || !aligned(dw, 4) || !aligned(work, 4))
     return NM_ERR_ALIGN;
+  const int64_t e = esize(dt);
+  const Area out[] = {area(dX, T, D, lddx, e), area(dw, 1, D, D, 4), area(work, 1, need, need, 1)};
+  const Area in[] = {area(dY, T, D, lddy, e), area(H, T, D, ldh, e), area(dH, T, D, lddh, e)};
+  if (overlap(out, in, {7, 0, 0})) return NM_ERR_SHAPE;
   const nms::NormBwdArgs a{dY, lddy, H, ldh, w, wdt == NM_BF16, rstd, dH, lddh, T, D, dX, lddx, dw, (float*)work};
   return hip_status(nms::launch_rms_norm_bwd(dt, a, hs(stream)));
 }
@@ -641,6 +698,9 @@ nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int
   if (!aligned(X, 2) || !aligned(W, 2) || (bias && !aligned(bias, esize(bdt))) || !aligned(residual, 2) ||
       !aligned(Y, esize(out)) || !aligned(pre, 2) || !aligned(work, 16))
     return NM_ERR_ALIGN;
+  const Area written[] = {area(Y, M, N, ldy, esize(out)), area(pre, M, N, ldp, 2), area(work, 1, work_bytes, work_bytes, 1)};
+  const Area read[] = {area(X, M, K, ldx, 2), area(W, N, K, ldw, 2), area(residual, M, N, ldr, 2)};
+  if (overlap(written, read, {out == NM_BF16 ? 4u : 0u, 0, 0})) return NM_ERR_SHAPE;
   const nms::Linear g{(const uint16_t*)X, ldx, (const uint16_t*)W, ldw, 0, 0, M, N, K, Y, ldy, out == NM_BF16,
                       nms::EPI_FWD, bias, bdt == NM_BF16, act, (const uint16_t*)residual, ldr, (uint16_t*)pre, ldp,
                       nullptr, 0, 0, 0, 0, 0, 0};
@@ -666,6 +726,9 @@ nm_status linear_bwd_act(nm_dtype dt, const void* dY, int64_t lddy, const void* 
   if (need > 0 && !work) return NM_ERR_NULL;
   if (work_bytes < need) return NM_ERR_SHAPE;
   if (!aligned(dY, 2) || !aligned(pre, 2) || !aligned(dZ, 2) || !aligned(db, 4) || !aligned(work, 4)) return NM_ERR_ALIGN;
+  const Area out[] = {area(dZ, M, N, lddz, 2), area(db, 1, N, N, 4), area(work, 1, need, need, 1)};
+  const Area in[] = {area(dY, M, N, lddy, 2), area(act == NM_ACT_NONE ? nullptr : pre, M, N, ldp, 2)};
+  if (overlap(out, in, {3, 0, 0})) return NM_ERR_SHAPE;
   const nms::ActBwdArgs a{dY, lddy, pre, ldp, act, M, N, dZ, lddz, db, (float*)work};
   return hip_status(nms::launch_linear_bwd_act(a, hs(stream)));
 }
@@ -679,6 +742,9 @@ nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W,
     return NM_ERR_SHAPE;
   if (!aligned(dZ, 2) || !aligned(W, 2) || !aligned(pre, 2) || !aligned(dX, esize(out)) || !aligned(work, 16))
     return NM_ERR_ALIGN;
+  const Area written[] = {area(dX, M, K, lddx, esize(out)), area(work, 1, work_bytes, work_bytes, 1)};
+  const Area read[] = {area(dZ, M, N, lddz, 2), area(W, N, K, ldw, 2), area(act == NM_ACT_NONE ? nullptr : pre, M, K, ldp, 2)};
+  if (overlap(written, read, {out == NM_BF16 ? 4u : 0u, 0})) return NM_ERR_SHAPE;
   // rows of dZ times columns of W: the product's columns are W's, its reduction runs over W's rows
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)W, ldw, 0, 1, M, K, N, dX, lddx, out == NM_BF16,
                       act == NM_ACT_NONE ? nms::EPI_PLAIN : nms::EPI_GATE, nullptr, 0, act, nullptr, 0, nullptr, 0,
@@ -693,6 +759,9 @@ nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X,
   if (dt != NM_BF16 || !dtype_ok(out) || (accumulate && out != NM_F32)) return NM_ERR_UNSUPPORTED;
   if (!rows_ok(M, N) || !rows_ok(K, 1) || lddz < N || ldx < K || lddw < K) return NM_ERR_SHAPE;
   if (!aligned(dZ, 2) || !aligned(X, 2) || !aligned(dW, esize(out)) || !aligned(work, 16)) return NM_ERR_ALIGN;
+  const Area written[] = {area(dW, N, K, lddw, esize(out)), area(work, 1, work_bytes, work_bytes, 1)};
+  const Area read[] = {area(dZ, M, N, lddz, 2), area(X, M, K, ldx, 2)};
+  if (overlap(written, read, {0, 0})) return NM_ERR_SHAPE;
   const nms::Linear g{(const uint16_t*)dZ, lddz, (const uint16_t*)X, ldx, 1, 1, N, K, M, dW, lddw, out == NM_BF16,
                       accumulate ? nms::EPI_ADD : nms::EPI_PLAIN, nullptr, 0, NM_ACT_NONE, nullptr, 0, nullptr, 0, nullptr, 0, 0, 0, 0, 0, 0};
   return hip_status(nms::launch_linear(g, work, work ? work_bytes : 0, hs(stream)));
@@ -722,6 +791,13 @@ nm_status grad_norm(int64_t n, const nm_dtype* dt, const void* const* grads, con
                     void* work, int64_t work_bytes, nm_stream stream) {
   const nm_status st = grads_check(n, dt, grads, counts, norm, work, work_bytes, true);
   if (st != NM_OK) return st;
+  const int64_t need = nms::grad_partials(counts, n) * 8;
+  const Area out[] = {area(norm, 1, 1, 1, 4), area(work, 1, need, need, 1)};
+  if (meet(out[0], out[1])) return NM_ERR_SHAPE;
+  for (int64_t i = 0; i < n; ++i) {
+    const Area g = area(grads[i], 1, counts[i], counts[i], esize(dt[i]));
+    if (meet(out[0], g) || meet(out[1], g)) return NM_ERR_SHAPE;
+  }
   const nms::Grads g{n, (const int*)dt, grads, counts, nullptr, nullptr};
   return hip_status(nms::launch_grads(g, false, norm, 0.f, (double*)work, hs(stream)));
 }

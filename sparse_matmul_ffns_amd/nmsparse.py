@@ -1154,7 +1154,7 @@ def _norm_args(X, w, residual, H, rstd, Y, *others):
 def rms_norm(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-5, residual=None, H=None, Y=None, rstd=None):
     """h = X [T, D] + residual, Y = h / sqrt(mean(h^2) + eps) * w: returns (Y, H, rstd), H the rounded sum
     (without a residual X itself, unless H is given or Y is X) and rstd [T] fp32, what rms_norm_bwd reads.  In place:
-    H may be X or the residual, Y may be X."""
+    H and Y may each be X or the residual, but not the same one."""
     given = (H, Y, rstd)
     T, D, ldx, ldr, H, ldh, rstd = _norm_args(X, w, residual, H, rstd, Y)
     Y, ldy = _new_or(Y, (T, D), X.dtype, X, "Y")
@@ -1193,7 +1193,7 @@ def _norm_work_bytes(T: int, D: int) -> int:
 def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, dH=None, dX=None, dw=None,
                  work="auto"):
     """The gradients of rms_norm at its stored H and rstd: (dX [T, D], the gradient of X and of the residual; dw [D]
-    fp32).  `dH` is the gradient that reaches H by other ways (through the residual); dX may be dY or dH."""
+    fp32).  `dH` is the gradient that reaches H by other ways (through the residual); dX may be dY, dH or H."""
     given = (dX, dw)
     T, D = _two(H, "H")
     _here(dY, H, w, rstd, dH, dX, dw)

@@ -56,3 +56,53 @@ def test_a_pass_whose_input_the_library_overwrote_is_refused():
     nm.grad_clip([layer.W_up], 0.5)                   # a parameter
     with pytest.raises(RuntimeError):
         layer.backward(dy, third)
+
+
+def test_outputs_among_the_inputs():
+    """What the header allows: each output in the place of an input, and columns of one buffer beside each other."""
+    for T, D in ((3, 520), (700, 4096), (600, 9000)):
+        X, R, dY, dH = (_rand(i, T, D) for i in range(4))
+        w = 1 + 0.1 * _rand(9, D)
+        y, h, rstd = nm.rms_norm(X, w, residual=R)
+        dx, dw = nm.rms_norm_bwd(dY, h, w, rstd, dH=dH)
+        for into_h, into_y in ((0, 1), (1, 0), (None, 1), (0, None), (1, None)):
+            xr = [X.clone(), R.clone()]
+            H, Y = None if into_h is None else xr[into_h], None if into_y is None else xr[into_y]
+            got = nm.rms_norm(xr[0], w, residual=xr[1], H=H, Y=Y)
+            assert torch.equal(got[0], y) and torch.equal(got[1], h) and torch.equal(got[2], rstd)
+            got8 = nm.rms_norm_fp8(X.clone(), w, residual=R)
+            xr = [X.clone(), R.clone()]
+            got = nm.rms_norm_fp8(xr[0], w, residual=xr[1], H=None if into_h is None else xr[into_h])
+            assert torch.equal(got[0].view(torch.uint8), got8[0].view(torch.uint8)) and all(torch.equal(a, b) for a, b in zip(got[1:], got8[1:]))
+        for k in range(3):
+            a = [dY.clone(), h.clone(), dH.clone()]
+            got = nm.rms_norm_bwd(a[0], a[1], w, rstd, dH=a[2], dX=a[k])
+            assert got[0] is a[k] and torch.equal(got[0], dx) and torch.equal(got[1], dw)
+        buf = torch.zeros(T, 4 * D, dtype=X.dtype, device="cuda")
+        x, r, hh, yy = buf.split(D, 1)
+        x.copy_(X), r.copy_(R)
+        nm.rms_norm(x, w, residual=r, H=hh, Y=yy)
+        assert torch.equal(yy, y) and torch.equal(hh, h) and torch.equal(x, X) and torch.equal(r, R)
+    X, W = _rand(0, 300, 64), _rand(1, 64, 64)
+    buf = torch.zeros(300, 192, dtype=X.dtype, device="cuda")
+    buf[:, :64] = X
+    out, pre = nm.linear_fwd(buf[:, :64], W, act="silu", residual=buf[:, :64], out=buf[:, 64:128], pre=buf[:, 128:])
+    want = nm.linear_fwd(X, W, act="silu", residual=X, return_pre=True)
+    assert torch.equal(out, want[0]) and torch.equal(pre, want[1]) and torch.equal(buf[:, :64], X)
+
+
+def test_overlaps_are_refused():
+    x, w = _rand(0, 40, 64), _rand(1, 64)
+    keep = x.clone()
+    with pytest.raises(nm.nmsparse.NmError):
+        nm.rms_norm(x, w, H=x, Y=x)
+    with pytest.raises(nm.nmsparse.NmError):
+        nm.rms_norm(x[:30], w, Y=x[10:])
+    with pytest.raises(nm.nmsparse.NmError):
+        nm.linear_fwd(x, _rand(2, 64, 64), out=x)
+    with pytest.raises(nm.nmsparse.NmError):
+        nm.linear_bwd_act(x[:39], x[1:], act="silu", dZ=x.view(-1)[32:32 + 39 * 64].view(39, 64))
+    flat = torch.zeros(100000, device="cuda")
+    with pytest.raises(nm.nmsparse.NmError):
+        nm.grad_norm([flat], norm=flat[5:6])
+    assert torch.equal(x, keep) and (flat == 0).all()

@@ -851,16 +851,17 @@ int64_t part_bytes(const LinearPlan& p, int64_t M, int64_t N) {
 }
 
 // Copies of operands that the tiled kernel cannot load: X [rows][line] to P [rows][up to a multiple of eight], zeros behind
-// the line.  The first `na` workgroups copy A, the others B.
+// the line.  The first `na` workgroups copy A, the others B; the launch's are those from `first` on.
 struct Pack {
   const uint16_t* X;
   int64_t ld, rows, line;
   uint16_t* P;             // null: nothing to copy
 };
-__global__ __launch_bounds__(256) void linear_pack_kernel(Pack a, Pack b, int64_t na) {
-  const bool second = blockIdx.x >= na;
+__global__ __launch_bounds__(256) void linear_pack_kernel(Pack a, Pack b, int64_t na, int64_t first) {
+  const int64_t wg = first + blockIdx.x;
+  const bool second = wg >= na;
   const Pack& p = second ? b : a;
-  const int64_t per = (p.line + 7) / 8, id = ((int64_t)blockIdx.x - (second ? na : 0)) * 256 + threadIdx.x;
+  const int64_t per = (p.line + 7) / 8, id = (wg - (second ? na : 0)) * 256 + threadIdx.x;
   const int64_t r = id / per, c = id % per * 8;
   if (r >= p.rows) return;
   const uint16_t* x = p.X + r * p.ld;
@@ -880,9 +881,11 @@ int64_t pack_bytes(int t, int64_t R, int64_t K) { return t ? K * up8(R) * 2 : R 
 hipError_t run_pack(const Pack& a, const Pack& b, hipStream_t s) {
   auto wgs = [](const Pack& p) { return p.P ? (p.rows * ((p.line + 7) / 8) + 255) / 256 : 0; };
   const int64_t na = wgs(a), nb = wgs(b);
-  if (!grid_ok(na + nb, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(linear_pack_kernel, dim3((unsigned)(na + nb)), dim3(256), 0, s, a, b, na);
-  return hipGetLastError();
+  constexpr int64_t PIECE = int64_t(1) << 23;   // workgroups of a launch: 2^31 work-items
+  return in_pieces(na + nb, PIECE, [&](int64_t first, int64_t n) {
+    hipLaunchKernelGGL(linear_pack_kernel, dim3((unsigned)n), dim3(256), 0, s, a, b, na, first);
+    return hipGetLastError();
+  });
 }
 
 hipError_t linear_piece(const Linear& g, LinearPlan p, void* work, int64_t work_bytes, hipStream_t s) {

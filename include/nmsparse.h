@@ -814,7 +814,7 @@ nm_status rms_norm_bwd_work_bytes(int64_t T, int64_t D, int64_t* bytes);
  *   Y [M][ldy] bf16 or fp32 (out); pre [M][ldp] bf16: z, what the backward pass reads (NULL: not stored)
  * Sums, z and the activation are fp32; Y and pre are rounded once each.  bf16 only (NM_ERR_UNSUPPORTED).  Y may be
  * the residual (bf16).  The tiled kernels load X and W as they are when K, ldx and ldw
- * are multiples of 8 and X and W 16-byte aligned; else by way of copies in `work` (linear_work_bytes), and without
+ * are multiples of 8, ldx and ldw below 2^22 and X and W 16-byte aligned; else by way of copies in `work` (linear_work_bytes), and without
  * that a slower general kernel runs.
  */
 nm_status linear_fwd(nm_dtype dt, const void* X, int64_t ldx, const void* W, int64_t ldw, nm_dtype bdt,
@@ -845,8 +845,8 @@ nm_status linear_bwd_act_work_bytes(int64_t M, int64_t N, int64_t* bytes);
  *   dZ [M][lddz], W [N][ldw] bf16; pre [M][ldp] bf16, the pre-activations X came from (NULL with NM_ACT_NONE)
  *   dX [M][lddx] bf16 or fp32 (out); it may be pre (bf16).
  * With ReLU, X itself gives the same derivative as its pre-activations.  Sums are fp32, the result is rounded once.
- * bf16 only.  The tiled kernels load dZ and W as they are when N, K and their leading dimensions are multiples of 8
- * and both 16-byte aligned; work as for linear_fwd.
+ * bf16 only.  The tiled kernels load dZ and W as they are when N, K and their leading dimensions are multiples of 8,
+ * the latter below 2^22, and both 16-byte aligned; work as for linear_fwd.
  */
 nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W, int64_t ldw, const void* pre,
                        int64_t ldp, nm_act act, int64_t M, int64_t N, int64_t K, nm_dtype out, void* dX, int64_t lddx,
@@ -857,7 +857,7 @@ nm_status linear_bwd_x(nm_dtype dt, const void* dZ, int64_t lddz, const void* W,
  *   dW[n][k] = sum over m of dZ[m][n] X[m][k]      (accumulate: added to dW)
  *   dZ [M][lddz], X [M][ldx] bf16; dW [N][lddw] fp32 or bf16 (out; accumulate needs fp32, NM_ERR_UNSUPPORTED)
  * Sums are fp32.  bf16 operands only.  The tiled kernels load dZ and X as they are when N, K and their leading dimensions
- * are multiples of 8 and both 16-byte aligned; work as for linear_fwd.
+ * are multiples of 8, the latter below 2^22, and both 16-byte aligned; work as for linear_fwd.
  */
 nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X, int64_t ldx, int64_t M, int64_t N,
                        int64_t K, int accumulate, nm_dtype out, void* dW, int64_t lddw, void* work, int64_t work_bytes,
@@ -865,7 +865,8 @@ nm_status linear_bwd_w(nm_dtype dt, const void* dZ, int64_t lddz, const void* X,
 
 /*
  * linear_work_bytes -- host only: the work memory that linear_fwd, linear_bwd_x or linear_bwd_w uses for these sizes
- * (*bytes; 0 for most), `aligned` nonzero where both operands have 16-byte aligned rows.  Where the result has too few
+ * (*bytes; 0 for most), `aligned` nonzero where both operands have 16-byte aligned rows whose stride is below 2^22
+ * elements (what the tiled kernels' descriptors hold; others are copied like unaligned ones).  Where the result has too few
  * tiles for the GPU, the reduction is cut into parts whose fp32 sums go through it, and a further launch adds them in their
  * order; operands whose rows the tiled kernels cannot load are copied to it first.  `work` is device memory, 16-byte
  * aligned (NM_ERR_ALIGN); with less of it, or NULL, the call does without and is slower.

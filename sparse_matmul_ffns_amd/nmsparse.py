@@ -1219,7 +1219,7 @@ def _linear_work_bytes(call: int, M: int, N: int, K: int, aligned: bool) -> int:
 
 
 def _linear_work(work, call: int, M: int, N: int, K: int, A, lda: int, B, ldb: int):
-    aligned = (A.data_ptr() | B.data_ptr()) % 16 == 0 and (lda | ldb) % 8 == 0
+    aligned = (A.data_ptr() | B.data_ptr()) % 16 == 0 and (lda | ldb) % 8 == 0 and max(lda, ldb) < 1 << 22
     return _workspace(work, _linear_work_bytes(call, M, N, K, aligned) if isinstance(work, str) else 0, A)
 
 

@@ -10,8 +10,9 @@ namespace nms {
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };
 
 // 1 / (1 + exp(-x)): the exponential and the reciprocal are correct to one unit in the last place of
-// fp32, and x enters the exponent rounded, so the result's relative error is below (|x| + 3) 2^-23;
-// +-infinity give 1 and 0.
+// fp32, and x enters the exponent rounded, so the result's relative error is below (|x| + 3) 2^-23 where it is
+// a normal number, x > -87.3.  Below that the reciprocal (and from -88.7 on the exponential's infinity) gives 0, which is
+// off by less than 2^-126: x sigmoid(x) then is -0, off by less than 88 2^-126 = 1.04e-36.  +-infinity give 1 and 0.
 __device__ inline float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
 }

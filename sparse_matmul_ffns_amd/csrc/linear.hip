@@ -321,9 +321,9 @@ struct Out {
 };
 
 // Any tile, element by element where it ends.
-template <int EPI, int FM, int FN>
+template <int FM, int FN>
 __device__ __forceinline__ void epilogue_edge(const Linear& g, const f32x4 (&acc)[FM][FN], unsigned char* region, int64_t m0,
-                                     int64_t n0, int lane) {
+                                              int64_t n0, int lane) {
   typedef Out<FM, FN> O;
   each_of<O::PASSES>([&](auto p) {
     O::template put<decltype(p)::value>(acc, region, lane);
@@ -429,7 +429,7 @@ __device__ __forceinline__ void tile_epilogue(const Linear& g, const f32x4 (&acc
   const bool whole = m0 + 16 * FM <= g.M && n0 + 16 * FN <= g.N && fours(g.C, g.ldc, g.bf16_out ? 2 : 4) &&
                      fours(g.R, g.ldr, 2) && fours(g.Z, g.ldz, 2) && fours(g.P, g.ldp, 2);
   if (!whole) {
-    epilogue_edge<EPI>(g, acc, region, m0, n0, lane);
+    epilogue_edge(g, acc, region, m0, n0, lane);
   } else if constexpr (EPI == EPI_FWD) {
     const bool other = g.R || g.Z;
     if (g.bf16_out) {

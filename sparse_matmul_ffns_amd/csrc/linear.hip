@@ -636,7 +636,8 @@ hipError_t run_tile(const Linear& g, int parts, hipStream_t s) {
 // the registers of the matrix instruction, with no LDS and no barrier on the way.  A workgroup computes 16 FM rows of A by
 // 16 FN rows of B; its KS waves take every KS-th chunk of 32 CH k, each with the next chunk's loads in flight, and
 // add their sums through LDS in the order of the waves.  The lanes of a row that does not exist load nothing.
-// 16 x 8192 x 2048 12.7 us, 16 x 2048 x 8192 19.2 (one workgroup a 16 columns leaves half of the CUs without work there; with 16 waves 19.8).
+// Weights that are not in a cache, replayed from a graph: 16 x 8192 x 2048 11.8 us, 16 x 2048 x 8192 18.8 (one workgroup a 16 columns leaves half
+// of the CUs without work there; 16 waves gain nothing), 32 x 8192 x 2048 13.4, 16 x 4096 x 16384 42.
 // ---------------------------------------------------------------------------
 template <int FM, int FN, int KS, int CH, bool TAIL>
 __global__ __launch_bounds__(64 * KS) void linear_rows_kernel(Linear g) {
@@ -960,7 +961,7 @@ double round_us(const TileCost& t, double k, int64_t workgroups) {
 
 LinearPlan linear_plan(int a_t, int b_t, int64_t M, int64_t N, int64_t K, bool aligned) {
   // Few rows: the kernel without LDS, against the best of the tiles in us: 1 x 2048 x 8192 12 and 16 (10 by the kernel for one
-  // row), 16 x 8192 x 2048 11 and 15, 16 x 2048 x 8192 18 and 18; 32 x 8192 x 2048 13 and 15, but 32 x 2048 x 8192 26 and 18
+  // row), 16 x 8192 x 2048 12 and 15, 16 x 2048 x 8192 19 and 18; 32 x 8192 x 2048 13 and 15, but 32 x 2048 x 8192 26 and 18
   if (!a_t && !b_t && (M <= 16 || (M <= 32 && K <= 2048))) return LinearPlan{LinearPlan::ROWS, 1, K, false};
   LinearPlan best{LinearPlan::T256, 1, K, false};
   double least = 1e30;

@@ -72,7 +72,8 @@ class DenseFFN:
 
     def backward(self, dy: torch.Tensor, saved=None):
         """The gradients of the last forward pass, or of the one that returned `saved`: dx [T, D] (of x and of residual), and
-        those of parameters(), in their order and fp32.
+        those of parameters(), in their order and fp32.  The gradients between the products are bf16: b_up's is the fp32 sum of what
+        W_up's is a product of, the rounded gradient behind the activation.
 
         Refused (RuntimeError): a second backward() of a pass that took the place of one without a backward pass; x or the
         parameters changed in place since the pass, by torch's calls or by this library's (a tensor's version counts both)."""

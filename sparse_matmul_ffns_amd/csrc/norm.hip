@@ -337,7 +337,8 @@ hipError_t run_bwd(const NormBwdArgs& a, hipStream_t s) {
 // The threads of a row and their vectors, by its width (at most 16384).  Measured on bf16 rows that are not in
 // a cache, us: 8192 x 4096 with a residual (268 MB) 44.5 with 256 threads, 43.4 with 128, 49 with 64, 51 with 1024 (its gradients, 268 MB,
 // 48.7, 55.6, - and 75); 64 x 4096 3.6, 4.3, 5.5, 3.3; 4096 x 2048 13.0, 11.3, 11.6, 16.9; 4096 x 8192 45.5 with 256 and 44.0 with 512.  To 8
-// bits 4096 x 2048 takes 14.8 (15.5 with 64; 15.9 before an XCD's workgroups took neighbouring rows).
+// bits 4096 x 2048 takes 15.3 (with 32-bit products 15.2, which with 64 threads a row were 0.7 slower, and 1.1 before an XCD's workgroups took
+// neighbouring rows).
 template <typename T>
 hipError_t fwd_by_width(const NormArgs& a, hipStream_t s) {
   const int64_t n = (a.D + 7) / 8;

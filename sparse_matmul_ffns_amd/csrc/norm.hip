@@ -142,7 +142,10 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void rms_norm_kernel(NormArgs 
       for (int q = 0; q < 8; ++q) {
         const Sum p = h[i][q] * rho * (Sum)w[q];
         y[q] = (float)p;
-        if constexpr (F8) v.w[q] = !TAIL || c + q < D ? odd_bits(p) : 0u;
+        if constexpr (F8) {
+          v.w[q] = !TAIL || c + q < D ? odd_bits(p) : 0u;
+          if constexpr (sizeof(T) == 2) y[q] = __uint_as_float(v.w[q]);   // for its one rounding to bf16
+        }
       }
       if (a.Y) store8f<T, TAIL>((T*)a.Y + row * a.ldy, c, D, y);
     }

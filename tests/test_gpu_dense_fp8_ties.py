@@ -124,3 +124,25 @@ def test_values_that_are_exact_and_not_finite():
     v, scale = blocks(y, "e4m3")
     assert np.array_equal(got[:2], (round8(v, "e4m3")[0] * scale[:, :, None]).reshape(2, D))
     assert np.isnan(got[2, 3]) and (np.delete(got[2], 3) == 0).all() and np.isnan(got[3]).all()
+
+
+@pytest.mark.parametrize("dtype,wdtype,T,D,shift", CASES)
+def test_the_result_beside_the_bytes_is_rounded_once(dtype, wdtype, T, D, shift):
+    """Y in bf16 or fp32 against 64 bits rounded once; the margin as above."""
+    g = torch.Generator().manual_seed(T + D + 1)
+    X = torch.randn(T, D, generator=g).to(TD[dtype])
+    R = None if shift is None else (torch.randn(T, D, generator=g) * 2.0 ** -shift).to(TD[dtype])
+    w = (1 + 0.2 * torch.randn(D, generator=g)).to(TD[wdtype])
+    h = X.double().numpy() + (0.0 if R is None else R.double().numpy())
+    eps = float(np.float32(1e-5))
+    y = h / np.sqrt((h * h).mean(1, keepdims=True) + eps) * w.double().numpy()
+    digits = 7 if dtype == "bf16" else 23
+    step = np.ldexp(1.0, np.frexp(y)[1] - 1 - digits)
+    q = y / step
+    want, margin = np.rint(q) * step, np.abs(np.abs(q - np.floor(q)) - 0.5) / np.maximum(np.abs(q), 1e-300)
+    if dtype == "bf16":
+        assert (torch.from_numpy(y).float().bfloat16().double().numpy() != want).any()     # by way of fp32 some differ
+    Y = torch.empty(T, D, dtype=TD[dtype], device="cuda")
+    nm.rms_norm_fp8(X.cuda(), w.cuda(), eps=eps, residual=None if R is None else R.cuda(), Y=Y)
+    bad = (Y.double().cpu().numpy() != want) & (margin > 2.0 ** -38)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist())

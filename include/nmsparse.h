@@ -775,7 +775,8 @@ nm_status rms_norm(nm_dtype dt, const void* X, int64_t ldx, const void* residual
 /*
  * rms_norm_fp8 -- rms_norm whose result is the operand of an 8-bit product: the rows
  * h * rstd * w to 8 bits in blocks of 128 with a power-of-two scale, by fp8_quantize's rule.  h, its squares' sum, 1 / sqrt
- * and the products are 64-bit here, and every byte and Y are rounded once from them; H as for rms_norm.
+ * and the products are 64-bit here, and every byte and Y are rounded once from them (no finite row
+ * overflows); H as for rms_norm.
  *   Q [T][ldq] bytes, ldq >= Dp = D rounded up to 128: columns D .. Dp-1 are written 0
  *   S fp32 [Dp / 128][lds], lds >= T
  *   Y as for rms_norm (NULL: not stored); the rest as for rms_norm.

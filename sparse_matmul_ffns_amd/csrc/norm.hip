@@ -115,14 +115,18 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void rms_norm_kernel(NormArgs 
   sum = row_sum<NT>(sum, part);
   Sum rho;
   if constexpr (F8) {
-    // two Newton steps in 64 bits from the 32-bit result (the second for its last eight bits)
+    // two Newton steps in 64 bits from the 32-bit result (the second for its last eight bits), of the mean scaled by a power of four: fp32 does
+    // not hold the squares of all fp32 rows
     const double m = sum / (double)D + (double)a.eps;
-    rho = (double)(1.f / sqrtf((float)m));
+    const int k = __builtin_amdgcn_frexp_exp(m) >> 1;
+    const double n = __builtin_amdgcn_ldexp(m, -2 * k);
+    rho = (double)(1.f / sqrtf((float)n));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const double e = rho * __builtin_fma(-0.5 * m * rho, rho, 1.5);
-      rho = __builtin_isfinite(e) ? e : rho;   // infinite or vanishing sums stay what they are
+      const double e = rho * __builtin_fma(-0.5 * n * rho, rho, 1.5);
+      rho = __builtin_isfinite(e) ? e : rho;   // an infinite sum's 0 stays
     }
+    rho = __builtin_amdgcn_ldexp(rho, -k);
   } else {
     rho = 1.f / sqrtf(sum / (float)D + a.eps);
   }

@@ -146,3 +146,31 @@ def test_the_result_beside_the_bytes_is_rounded_once(dtype, wdtype, T, D, shift)
     nm.rms_norm_fp8(X.cuda(), w.cuda(), eps=eps, residual=None if R is None else R.cuda(), Y=Y)
     bad = (Y.double().cpu().numpy() != want) & (margin > 2.0 ** -38)
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [96, 2048, 9000])
+def test_rows_of_any_size(dtype, D):
+    """Rows from 2^-100 to 2^127, whose squares fp32 does not hold, and sums that it does not hold."""
+    g = torch.Generator().manual_seed(D)
+    T = 40
+    size = torch.linspace(-100, 125, T).round()
+    X = (torch.randn(T, D, generator=g).clamp(-3.5, 3.5) * torch.exp2(size)[:, None]).to(TD[dtype])
+    w = 1 + 0.2 * torch.randn(D, generator=g)
+    for R in (None, X.clone()):                  # the last rows' doubles are beyond fp32
+        h = X.double().numpy() * (1 if R is None else 2)
+        for eps in (1e-5, 1e-38):
+            eps = float(np.float32(eps))
+            rstd = 1 / np.sqrt((h * h).mean(1) + eps)
+            y = h * rstd[:, None] * w.double().numpy()
+            Q, S, _, got = nm.rms_norm_fp8(X.cuda(), w.cuda(), eps=eps, residual=None if R is None else R.cuda())
+            # half a step of fp32: relative, and below 2^-126 (rows beyond 2^126) half of the subnormals' step of 2^-149
+            assert (np.abs(got.double().cpu().numpy() - rstd) <= np.maximum(2.0 ** -24 * rstd, 2.0 ** -150)).all()
+            v, scale = blocks(y, "e4m3")
+            want, margin = round8(v, "e4m3")
+            assert np.array_equal(S.cpu().double().numpy().T, scale)
+            # below fp32's normal numbers y is rounded twice
+            plain = (np.abs(y) >= 2.0 ** -126)
+            plain = np.pad(plain, ((0, 0), (0, -D % 128)), constant_values=True).reshape(v.shape)
+            bad = (Q.float().cpu().double().numpy().reshape(v.shape) != want) & (margin > 2.0 ** -38) & plain
+            assert not bad.any(), (eps, np.argwhere(bad)[:4].tolist())
